@@ -52,6 +52,22 @@ hipError_t launch_grouped_fp8(const void* a, const float* a_scale, const float* 
                               const int32_t* offsets, int64_t E, const void* w_tiled, size_t w_bytes_per_expert,
                               const void* w_scale, int64_t group, void* out, int64_t T, int64_t R, int64_t N,
                               int64_t K, hipStream_t stream);
+size_t route_workspace(int64_t T, int64_t E);
+hipError_t launch_route(const void* x, int dt, int64_t T, int64_t E, int64_t ld, int score, const float* bias,
+                        int64_t G, int64_t topk_groups, int64_t group_top, int64_t topk, bool renorm, double scale,
+                        int32_t* ids, float* weights, int32_t* row_token, int32_t* offsets, int32_t* row_of,
+                        void* ws, hipStream_t stream);
+hipError_t launch_block_quant(const void* x, bool bf16, bool swiglu, int64_t M, int64_t K, int64_t ldx, void* codes,
+                              float* scales, hipStream_t stream);
+size_t fp8_block_gemm_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_fp8_block_gemm(const void* a, const float* a_scale, const void* w, const float* w_scale,
+                                 const void* bias, void* out, int out_dt, int64_t M, int64_t N, int64_t K, void* ws,
+                                 hipStream_t stream);
+hipError_t launch_fp8_block_grouped(const void* a, const float* a_scale, const int32_t* row_token,
+                                    const int32_t* offsets, int64_t E, const void* w, const float* w_scale, void* out,
+                                    int out_dt, int64_t T, int64_t R, int64_t N, int64_t K, hipStream_t stream);
+hipError_t launch_combine(const void* y, int dt, const int32_t* row_of, const float* weights, const void* add,
+                          void* out, int64_t T, int64_t R, int64_t topk, int64_t N, hipStream_t stream);
 }  // namespace w4
 
 namespace {
@@ -700,6 +716,177 @@ int w4_pack_nibbles(const uint8_t* codes, int64_t N, int64_t K, uint8_t* packed,
 
 int w4_unpack_nibbles(const uint8_t* packed, int64_t N, int64_t K, uint8_t* codes, void* stream) {
   return nibbles("w4_unpack_nibbles", packed, N, K, codes, false, stream);
+}
+
+// ---- the FP8 expert path
+
+// bf16, fp16, fp32 as the kernels number them; -1: not one of them
+static int float_index(int dtype) {
+  return dtype == W4_BF16 ? 0 : (dtype == W4_F16 ? 1 : (dtype == W4_F32 ? 2 : -1));
+}
+
+static int check_route_sizes(const char* fn, int64_t T, int64_t E, int64_t topk) {
+  if (T < 0 || E <= 0 || topk <= 0)
+    return fail(W4_ERR_INVALID, "%s: sizes must be T >= 0, E > 0, topk > 0 (got T=%lld E=%lld topk=%lld)", fn,
+                (long long)T, (long long)E, (long long)topk);
+  if (topk > E) return fail(W4_ERR_INVALID, "%s: topk=%lld exceeds E=%lld", fn, (long long)topk, (long long)E);
+  if (E > 1024 || topk > 64 || T > kMaxDim || T * topk >= ((int64_t)1 << 31))
+    return fail(W4_ERR_UNSUPPORTED, "%s: T=%lld E=%lld topk=%lld outside E <= 1024, topk <= 64, T*topk < 2^31", fn,
+                (long long)T, (long long)E, (long long)topk);
+  return W4_OK;
+}
+
+int w4_route_workspace_bytes(int64_t T, int64_t E, int64_t topk, size_t* bytes) {
+  const char* fn = "w4_route_workspace_bytes";
+  if (!bytes) return fail(W4_ERR_INVALID, "%s: null output pointer", fn);
+  int rc = check_route_sizes(fn, T, E, topk);
+  if (rc) return rc;
+  *bytes = w4::route_workspace(T, E);
+  return ok();
+}
+
+int w4_route(const void* logits, int logits_dtype, int64_t T, int64_t E, int64_t ld, int score, const float* bias,
+             int64_t n_groups, int64_t topk_groups, int64_t group_top, int64_t topk, int renorm, double scale,
+             int32_t* ids, float* weights, int32_t* row_token, int32_t* expert_offsets, int32_t* row_of,
+             void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "w4_route";
+  const int dt = float_index(logits_dtype);
+  if (dt < 0) return fail(W4_ERR_DTYPE, "%s: logits must be bf16, fp16 or fp32 (dtype code %d)", fn, logits_dtype);
+  int rc = check_route_sizes(fn, T, E, topk);
+  if (rc) return rc;
+  if (score != W4_SCORE_SOFTMAX && score != W4_SCORE_SIGMOID)
+    return fail(W4_ERR_INVALID, "%s: unknown score %d", fn, score);
+  if (n_groups <= 0 || n_groups > 64 || E % n_groups)
+    return fail(W4_ERR_GROUP, "%s: n_groups=%lld must be 1..64 and divide E=%lld", fn, (long long)n_groups,
+                (long long)E);
+  if (topk_groups <= 0 || topk_groups > n_groups)
+    return fail(W4_ERR_GROUP, "%s: topk_groups=%lld must be 1..n_groups=%lld", fn, (long long)topk_groups,
+                (long long)n_groups);
+  if (group_top != 1 && group_top != 2)
+    return fail(W4_ERR_UNSUPPORTED, "%s: group_top=%lld must be 1 or 2", fn, (long long)group_top);
+  if (ld < E) return fail(W4_ERR_ALIGN, "%s: ld=%lld must be >= E=%lld", fn, (long long)ld, (long long)E);
+  if (!expert_offsets || (T > 0 && (!logits || !ids || !weights || !row_token || !row_of)))
+    return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
+  if ((reinterpret_cast<uintptr_t>(logits) & (dt == 2 ? 3u : 1u)) != 0)
+    return fail(W4_ERR_ALIGN, "%s: logits must be aligned to their type", fn);
+  const size_t need = w4::route_workspace(T, E);
+  if (workspace_bytes < need || (need && !workspace))
+    return fail(W4_ERR_INVALID, "%s: workspace of %zu bytes is smaller than the %zu needed for T=%lld E=%lld", fn,
+                workspace_bytes, need, (long long)T, (long long)E);
+  if (need && !aligned16(workspace)) return fail(W4_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  return hip_status(w4::launch_route(logits, dt, T, E, ld, score == W4_SCORE_SIGMOID ? 1 : 0, bias, n_groups,
+                                     topk_groups, group_top, topk, renorm != 0, scale, ids, weights, row_token,
+                                     expert_offsets, row_of, workspace, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int w4_fp8_block_quantize(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, int act, void* codes,
+                          float* scales, void* stream) {
+  const char* fn = "w4_fp8_block_quantize";
+  if (M < 0 || K < 0) return fail(W4_ERR_INVALID, "%s: negative size M=%lld K=%lld", fn, (long long)M, (long long)K);
+  if (x_dtype != W4_BF16 && x_dtype != W4_F16)
+    return fail(W4_ERR_DTYPE, "%s: activations must be bf16 or fp16 (dtype code %d)", fn, x_dtype);
+  if (act != W4_ACT_NONE && act != W4_ACT_SWIGLU) return fail(W4_ERR_INVALID, "%s: unknown activation %d", fn, act);
+  if (K % 8) return fail(W4_ERR_ALIGN, "%s: K=%lld is not a multiple of 8", fn, (long long)K);
+  if (M > kMaxDim || K > ((int64_t)1 << 24))
+    return fail(W4_ERR_UNSUPPORTED, "%s: sizes too large (M=%lld K=%lld)", fn, (long long)M, (long long)K);
+  const int64_t wide = act == W4_ACT_SWIGLU ? 2 * K : K;
+  if (ldx < wide || ldx % 8)
+    return fail(W4_ERR_ALIGN, "%s: ldx=%lld must be >= %lld and a multiple of 8", fn, (long long)ldx,
+                (long long)wide);
+  if (M == 0 || K == 0) return ok();
+  if (!x || !codes || !scales) return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
+  if (!aligned16(x)) return fail(W4_ERR_ALIGN, "%s: x must be 16-byte aligned", fn);
+  if ((reinterpret_cast<uintptr_t>(codes) & 7u) != 0) return fail(W4_ERR_ALIGN, "%s: codes must be 8-byte aligned", fn);
+  return hip_status(w4::launch_block_quant(x, x_dtype == W4_BF16, act == W4_ACT_SWIGLU, M, K, ldx, codes, scales,
+                                           static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+static int check_fp8_block(const char* fn, int64_t M, int64_t N, int64_t K) {
+  int rc = check_mnk(fn, M, N, K);
+  if (rc) return rc;
+  if (K % 16) return fail(W4_ERR_ALIGN, "%s: K=%lld is not a multiple of 16", fn, (long long)K);
+  return W4_OK;
+}
+
+int w4_fp8_block_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  const char* fn = "w4_fp8_block_gemm_workspace_bytes";
+  if (!bytes) return fail(W4_ERR_INVALID, "%s: null output pointer", fn);
+  int rc = check_fp8_block(fn, M, N, K);
+  if (rc) return rc;
+  *bytes = w4::fp8_block_gemm_workspace(M, N, K);
+  return ok();
+}
+
+int w4_fp8_block_gemm(const void* a, const float* a_scale, const void* w, const float* w_scale, const void* bias,
+                      void* out, int out_dtype, int64_t M, int64_t N, int64_t K, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  const char* fn = "w4_fp8_block_gemm";
+  const int dt = float_index(out_dtype);
+  if (dt < 0) return fail(W4_ERR_DTYPE, "%s: output must be bf16, fp16 or fp32 (dtype code %d)", fn, out_dtype);
+  int rc = check_fp8_block(fn, M, N, K);
+  if (rc) return rc;
+  if (M == 0 || N == 0) return ok();
+  if (!a || !a_scale || !w || !w_scale || !out) return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out))
+    return fail(W4_ERR_ALIGN, "%s: a, w and out must be 16-byte aligned", fn);
+  const size_t need = w4::fp8_block_gemm_workspace(M, N, K);
+  if (workspace_bytes < need || (need && !workspace))
+    return fail(W4_ERR_INVALID, "%s: workspace of %zu bytes is smaller than the %zu needed for M=%lld N=%lld K=%lld",
+                fn, workspace_bytes, need, (long long)M, (long long)N, (long long)K);
+  if (need && !aligned16(workspace)) return fail(W4_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  return hip_status(w4::launch_fp8_block_gemm(a, a_scale, w, w_scale, bias, out, dt, M, N, K, workspace,
+                                              static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int w4_fp8_block_grouped_gemm(const void* a, const float* a_scale, const int32_t* row_token,
+                              const int32_t* expert_offsets, int64_t E, const void* w, const float* w_scale,
+                              void* out, int out_dtype, int64_t T, int64_t R, int64_t N, int64_t K, void* stream) {
+  const char* fn = "w4_fp8_block_grouped_gemm";
+  if (out_dtype != W4_BF16 && out_dtype != W4_F16)
+    return fail(W4_ERR_DTYPE, "%s: output must be bf16 or fp16 (dtype code %d)", fn, out_dtype);
+  int rc = check_fp8_block(fn, R, N, K);
+  if (rc) return rc;
+  if (E < 0 || E > 65535 || T < 0)
+    return fail(W4_ERR_INVALID, "%s: E=%lld T=%lld out of range", fn, (long long)E, (long long)T);
+  if (R == 0 || N == 0 || E == 0) return ok();
+  if (row_token && (T <= 0 || T * K >= ((int64_t)1 << 31)))
+    return fail(W4_ERR_UNSUPPORTED, "%s: token count T=%lld out of range for K=%lld (T*K must be below 2^31)", fn,
+                (long long)T, (long long)K);
+  if (!row_token && T != R)
+    return fail(W4_ERR_INVALID, "%s: without row_token the activations need R=%lld rows, got T=%lld", fn,
+                (long long)R, (long long)T);
+  if (!a || !a_scale || !expert_offsets || !w || !w_scale || !out)
+    return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out))
+    return fail(W4_ERR_ALIGN, "%s: a, w and out must be 16-byte aligned", fn);
+  return hip_status(w4::launch_fp8_block_grouped(a, a_scale, row_token, expert_offsets, E, w, w_scale, out,
+                                                 float_index(out_dtype), T, R, N, K,
+                                                 static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int w4_combine(const void* y, int dtype, const int32_t* row_of, const float* weights, const void* add, void* out,
+               int64_t T, int64_t R, int64_t topk, int64_t N, void* stream) {
+  const char* fn = "w4_combine";
+  const int dt = float_index(dtype);
+  if (dt < 0) return fail(W4_ERR_DTYPE, "%s: rows must be bf16, fp16 or fp32 (dtype code %d)", fn, dtype);
+  if (T < 0 || R < 0 || topk <= 0 || N < 0)
+    return fail(W4_ERR_INVALID, "%s: sizes must be T, R, N >= 0, topk > 0 (got T=%lld R=%lld topk=%lld N=%lld)", fn,
+                (long long)T, (long long)R, (long long)topk, (long long)N);
+  if (N % 8) return fail(W4_ERR_ALIGN, "%s: N=%lld is not a multiple of 8", fn, (long long)N);
+  if (T > kMaxDim || R > kMaxDim || N > kMaxDim || topk > 1024 || T * (N / 8) >= ((int64_t)1 << 38))
+    return fail(W4_ERR_UNSUPPORTED, "%s: sizes too large (T=%lld R=%lld topk=%lld N=%lld)", fn, (long long)T,
+                (long long)R, (long long)topk, (long long)N);
+  if (T == 0 || N == 0) return ok();
+  if ((!y && R > 0) || !row_of || !weights || !out) return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
+  if (!aligned16(y) || !aligned16(add) || !aligned16(out))
+    return fail(W4_ERR_ALIGN, "%s: y, add and out must be 16-byte aligned", fn);
+  return hip_status(w4::launch_combine(y, dt, row_of, weights, add, out, T, R, topk, N,
+                                       static_cast<hipStream_t>(stream)),
+                    fn);
 }
 
 }  // extern "C"

@@ -308,6 +308,92 @@ __global__ __launch_bounds__(kQThreads) void quant_act_asym_kernel(const uint16_
   for (int c = t + kQCache * kQThreads; c < nchunks; c += kQThreads) emit(c, buffer_load16(xrs, 16u * (uint32_t)c));
 }
 
+// Block quantization to E4M3: one fp32 scale per row and 128 columns (the
+// activations of the block-scaled FP8 products).
+//
+//   scale = max |v| / 448 over the block,  code = E4M3(v / scale)
+//   v = x, or x[:, k] * sigmoid(x[:, k]) * x[:, K + k] in fp32 (SWIGLU)
+//
+// both divisions correctly rounded (the same row division as above, with the
+// block in place of the row). 16 lanes hold one block, 8 columns each, so the
+// maximum is four lane exchanges and the data are read once. The maximum is
+// taken over the bits of |v|: a NaN is the largest, gives the block a NaN
+// scale and so reaches the product's row; infinity likewise. A block of
+// zeros has scale 0 and codes 0.
+//
+// HBM-bound: 2 bytes in (4 with the gate) + 1 byte out per element + 4 per
+// block.
+constexpr int kBQUnits = kQThreads / 16;             // 128-blocks per pass of a thread block
+
+template <bool BF16, bool SWIGLU>
+__global__ __launch_bounds__(kQThreads) void block_quant_kernel(const uint16_t* __restrict__ x, int64_t ldx, int K,
+                                                                int KB, int64_t units, uint8_t* __restrict__ codes,
+                                                                float* __restrict__ scales) {
+  const int64_t u = (int64_t)blockIdx.x * kBQUnits + (threadIdx.x >> 4);
+  if (u >= units) return;                            // whole groups of 16 lanes leave
+  const int64_t m = u / KB;
+  const int kb = (int)(u - m * KB);
+  const int k = kb * 128 + (threadIdx.x & 15) * 8;
+  const bool in = k < K;                             // K is a multiple of 8
+  const uint16_t* xr = x + m * ldx + k;
+  v4i raw = v4i{0, 0, 0, 0}, up = v4i{0, 0, 0, 0};
+  if (in) {
+    raw = *reinterpret_cast<const v4i*>(xr);
+    if (SWIGLU) up = *reinterpret_cast<const v4i*>(xr + K);
+  }
+  float v[8];
+  unpack8<BF16>(raw, v);
+  if (SWIGLU) {
+    float g[8];
+    unpack8<BF16>(up, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * g[i];
+  }
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, off, kWave));
+  const float s = __fdiv_rn(__uint_as_float(amax), 448.0f);
+  RowScale r;
+  r.s = s;
+  const float y0 = __builtin_amdgcn_rcpf(s);
+  r.y = fmaf(fmaf(-s, y0, 1.0f), y0, y0);
+  r.b = 449.0f * s;
+  r.fast = s >= 0x1p-90f && s <= 0x1p90f;
+  r.zero_row = !(s > 0.f);
+  v2i o;
+  float q[8];
+  if (r.fast) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)   // |v| <= 448 s (1 + 2^-24): inside the division's range, only the result saturates
+      q[i] = clamp448(__builtin_copysignf(div_rn_row(v[i], r), v[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = clamp448(__fdiv_rn(v[i], s));
+  }
+  o = pack_fp8(q);
+  if (r.zero_row) o = v2i{0, 0};
+  if (in) *reinterpret_cast<v2i*>(codes + m * K + k) = o;
+  if ((threadIdx.x & 15) == 0) scales[u] = s;
+}
+
+hipError_t launch_block_quant(const void* x, bool bf16, bool swiglu, int64_t M, int64_t K, int64_t ldx, void* codes,
+                              float* scales, hipStream_t stream) {
+  const int64_t KB = (K + 127) / 128, units = M * KB;
+  if (units == 0) return hipSuccess;
+  const dim3 grid((unsigned)((units + kBQUnits - 1) / kBQUnits)), block(kQThreads);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, static_cast<const uint16_t*>(x), ldx, (int)K, (int)KB, units,
+                       static_cast<uint8_t*>(codes), scales);
+  };
+  if (bf16 && swiglu) go(block_quant_kernel<true, true>);
+  else if (bf16) go(block_quant_kernel<true, false>);
+  else if (swiglu) go(block_quant_kernel<false, true>);
+  else go(block_quant_kernel<false, false>);
+  return hipGetLastError();
+}
+
 // Test hook of the FP8 encode: the fp32 values with bit patterns first,
 // first + 1, ..., first + n - 1 (n a multiple of 8) go through the
 // quantizer's own clamp to +-448 and pair conversion to E4M3, 8 per thread.

@@ -50,6 +50,14 @@ _SIGS = {
     "w4_probe_mfma": [_I, _I64, _P, _I64, ctypes.POINTER(ctypes.c_double), _P],
     "w4_pack_nibbles": [_P, _I64, _I64, _P, _P],
     "w4_unpack_nibbles": [_P, _I64, _I64, _P, _P],
+    "w4_route_workspace_bytes": [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "w4_route": [_P, _I, _I64, _I64, _I64, _I, _P, _I64, _I64, _I64, _I64, _I, ctypes.c_double, _P, _P, _P, _P, _P,
+                 _P, ctypes.c_size_t, _P],
+    "w4_fp8_block_quantize": [_P, _I, _I64, _I64, _I64, _I, _P, _P, _P],
+    "w4_fp8_block_gemm_workspace_bytes": [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "w4_fp8_block_gemm": [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, ctypes.c_size_t, _P],
+    "w4_fp8_block_grouped_gemm": [_P, _P, _P, _P, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _P],
+    "w4_combine": [_P, _I, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P],
     "w4_last_error": [],
     "w4_version": [],
 }
@@ -412,4 +420,173 @@ def w4a16_prefill(x, w, scale, zero, group: int, out=None, workspace=None, strea
     _check("w4a16_prefill", lib().w4a16_prefill(
         _ptr(x), _ptr(w), _ptr(scale), _ptr(zero), _half_code(scale.dtype), group, _ptr(out), M, N, K,
         _ptr(workspace), workspace.numel(), _stream(stream)))
+    return out
+
+
+# ----------------------------------------------------------------- the FP8 expert path
+
+W4_SCORES = {"softmax": 0, "sigmoid": 1}
+W4_ACTS = {"none": 0, "swiglu": 1}
+_FLOAT_CODES = {torch.bfloat16: W4_BF16, torch.float16: W4_F16, torch.float32: W4_F32}
+
+
+def _float_code(dt) -> int:
+    if dt not in _FLOAT_CODES:
+        raise TypeError(f"unsupported dtype {dt}: bf16, fp16 or fp32")
+    return _FLOAT_CODES[dt]
+
+
+def _typed(t, dtype, shape, what: str):
+    """t with its type and shape checked (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _e4m3_codes(t, what: str):
+    if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise TypeError(f"{what} must hold E4M3 codes (torch.float8_e4m3fn or uint8), got {t.dtype}")
+    return t
+
+
+def _rows_ptr(t, what: str):
+    """Pointer and row stride of a matrix whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("tensor must be on the GPU")
+    if t.dim() != 2 or (t.numel() and t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a matrix with contiguous rows")
+    return t.data_ptr() or None, (t.stride(0) if t.numel() and t.shape[0] > 1 else t.shape[1])
+
+
+def w4_route_workspace(T: int, E: int, topk: int, device="cuda") -> torch.Tensor:
+    """Device scratch for w4_route at these sizes (uint8, possibly empty)."""
+    n = ctypes.c_size_t(0)
+    _check("w4_route_workspace_bytes", lib().w4_route_workspace_bytes(T, E, topk, ctypes.byref(n)))
+    return torch.empty((n.value,), dtype=torch.uint8, device=device)
+
+
+def w4_route(logits, topk: int, score: str = "softmax", bias=None, n_groups: int = 1, topk_groups: int = 1,
+             group_top: int = 1, renorm: bool = True, scale: float = 1.0, out=None, workspace=None, stream=None):
+    """logits [T, E] bf16/fp16/fp32 (rows may be strided) -> (ids int32 [T, topk], weights fp32 [T, topk],
+    row_token int32 [T * topk], expert_offsets int32 [E + 1], row_of int32 [T, topk]); include/w4.h has the
+    definition. `out` is such a tuple to write into; the workspace (w4_route_workspace) is allocated if not given."""
+    T, E = logits.shape
+    ptr, ld = _rows_ptr(logits, "logits")
+    dev = logits.device
+    if score not in W4_SCORES:
+        raise ValueError(f"score must be one of {sorted(W4_SCORES)}, got {score!r}")
+    if out is None:
+        out = (torch.empty((T, topk), dtype=torch.int32, device=dev),
+               torch.empty((T, topk), dtype=torch.float32, device=dev),
+               torch.empty((T * topk,), dtype=torch.int32, device=dev),
+               torch.empty((E + 1,), dtype=torch.int32, device=dev),
+               torch.empty((T, topk), dtype=torch.int32, device=dev))
+    ids, weights, row_token, offsets, row_of = out
+    _typed(bias, torch.float32, (E,), "bias")
+    _typed(ids, torch.int32, (T, topk), "ids")
+    _typed(weights, torch.float32, (T, topk), "weights")
+    _typed(row_token, torch.int32, (T * topk,), "row_token")
+    _typed(offsets, torch.int32, (E + 1,), "expert_offsets")
+    _typed(row_of, torch.int32, (T, topk), "row_of")
+    if workspace is None:
+        workspace = w4_route_workspace(T, E, topk, device=dev)
+    _check("w4_route", lib().w4_route(
+        ptr, _float_code(logits.dtype), T, E, ld, W4_SCORES[score], _ptr(bias), n_groups, topk_groups, group_top,
+        topk, int(renorm), scale, _ptr(ids), _ptr(weights), _ptr(row_token), _ptr(offsets), _ptr(row_of),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def w4_fp8_block_quantize(x, act: str = "none", out=None, stream=None):
+    """x [M, K] ([M, 2K] = gate | up with act="swiglu") bf16/fp16, rows may be strided -> (codes uint8 [M, K] of E4M3
+    bits, scales fp32 [M, ceil(K / 128)])."""
+    if act not in W4_ACTS:
+        raise ValueError(f"act must be one of {sorted(W4_ACTS)}, got {act!r}")
+    M, wide = x.shape
+    if act == "swiglu" and wide % 2:
+        raise ValueError(f"swiglu takes gate and up side by side: {wide} columns cannot be halved")
+    K = wide // 2 if act == "swiglu" else wide
+    ptr, ldx = _rows_ptr(x, "x")
+    KB = (K + 127) // 128
+    if out is None:
+        out = (torch.empty((M, K), dtype=torch.uint8, device=x.device),
+               torch.empty((M, KB), dtype=torch.float32, device=x.device))
+    codes, scales = out
+    _typed(_e4m3_codes(codes, "codes"), codes.dtype, (M, K), "codes")
+    _typed(scales, torch.float32, (M, KB), "scales")
+    _check("w4_fp8_block_quantize", lib().w4_fp8_block_quantize(
+        ptr, _half_code(x.dtype), M, K, ldx, W4_ACTS[act], _ptr(codes), _ptr(scales), _stream(stream)))
+    return out
+
+
+def w4_fp8_block_gemm_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    """Device scratch for w4_fp8_block_gemm at these sizes (uint8, possibly empty)."""
+    n = ctypes.c_size_t(0)
+    _check("w4_fp8_block_gemm_workspace_bytes", lib().w4_fp8_block_gemm_workspace_bytes(M, N, K, ctypes.byref(n)))
+    return torch.empty((n.value,), dtype=torch.uint8, device=device)
+
+
+def w4_fp8_block_gemm(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloat16, workspace=None,
+                      stream=None):
+    """a [M, K] and w [N, K] E4M3 codes with fp32 scales [M, ceil(K/128)] and [ceil(N/128), ceil(K/128)]
+    -> out [M, N] bf16/fp16/fp32 (+ bias [N] of the same type)."""
+    (M, K), (N, Kw) = _e4m3_codes(a, "a").shape, _e4m3_codes(w, "w").shape
+    if K != Kw:
+        raise ValueError(f"a has {K} columns, w {Kw}")
+    KB, NB = (K + 127) // 128, (N + 127) // 128
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    _typed(a_scale, torch.float32, (M, KB), "a_scale")
+    _typed(w_scale, torch.float32, (NB, KB), "w_scale")
+    _typed(bias, out.dtype, (N,), "bias")
+    _typed(out, out.dtype, (M, N), "out")
+    if workspace is None:
+        workspace = w4_fp8_block_gemm_workspace(M, N, K, device=a.device)
+    _check("w4_fp8_block_gemm", lib().w4_fp8_block_gemm(
+        _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(out), _float_code(out.dtype), M, N, K,
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def w4_fp8_block_grouped_gemm(a, a_scale, row_token, expert_offsets, w, w_scale, out=None, out_dtype=torch.bfloat16,
+                              stream=None):
+    """The block-scaled product over expert segments: w [E, N, K], w_scale [E, ceil(N/128), ceil(K/128)]; output row r
+    of expert e (expert_offsets) takes activation row row_token[r], or row r itself with row_token None. -> out [R, N]
+    bf16/fp16; rows past expert_offsets[E] are not written."""
+    (T, K), (E, N, Kw) = _e4m3_codes(a, "a").shape, _e4m3_codes(w, "w").shape
+    if K != Kw:
+        raise ValueError(f"a has {K} columns, w {Kw}")
+    KB, NB = (K + 127) // 128, (N + 127) // 128
+    R = T if row_token is None else row_token.shape[0]
+    if out is None:
+        out = torch.empty((R, N), dtype=out_dtype, device=a.device)
+    _typed(a_scale, torch.float32, (T, KB), "a_scale")
+    _typed(row_token, torch.int32, (R,), "row_token")
+    _typed(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    _typed(w_scale, torch.float32, (E, NB, KB), "w_scale")
+    _typed(out, out.dtype, (R, N), "out")
+    _check("w4_fp8_block_grouped_gemm", lib().w4_fp8_block_grouped_gemm(
+        _ptr(a), _ptr(a_scale), _ptr(row_token), _ptr(expert_offsets), E, _ptr(w), _ptr(w_scale), _ptr(out),
+        _half_code(out.dtype), T, R, N, K, _stream(stream)))
+    return out
+
+
+def w4_combine(y, row_of, weights, add=None, out=None, stream=None):
+    """out[t] = sum_j weights[t, j] * y[row_of[t, j]] (+ add[t]): y [R, N] bf16/fp16/fp32, row_of int32 and weights fp32
+    [T, topk] from w4_route."""
+    R, N = y.shape
+    T, topk = row_of.shape
+    if out is None:
+        out = torch.empty((T, N), dtype=y.dtype, device=y.device)
+    _typed(row_of, torch.int32, (T, topk), "row_of")
+    _typed(weights, torch.float32, (T, topk), "weights")
+    _typed(add, y.dtype, (T, N), "add")
+    _typed(out, y.dtype, (T, N), "out")
+    _check("w4_combine", lib().w4_combine(
+        _ptr(y), _float_code(y.dtype), _ptr(row_of), _ptr(weights), _ptr(add), _ptr(out), T, R, topk, N,
+        _stream(stream)))
     return out
