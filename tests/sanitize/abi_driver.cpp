@@ -129,6 +129,33 @@ int main() {
   expect(w4_unpack_nibbles((const uint8_t*)odd, 4, 256, (uint8_t*)p, nullptr), W4_ERR_ALIGN, "upk align");
   expect(w4_unpack_nibbles(nullptr, 0, 256, nullptr, nullptr), W4_OK, "upk empty");
   expect(w4_unpack_nibbles((const uint8_t*)p, 4, 256, nullptr, nullptr), W4_ERR_INVALID, "upk null");
+  // the FP8 expert path
+  int32_t* ip = (int32_t*)p;
+  float* fp = (float*)p;
+  expect(w4_route_workspace_bytes(64, 2000, 8, &n), W4_ERR_UNSUPPORTED, "rw E");
+  expect(w4_route_workspace_bytes(64, 64, 8, nullptr), W4_ERR_INVALID, "rw null");
+  expect(w4_route_workspace_bytes((int64_t)1 << 62, 64, 64, &n), W4_ERR_UNSUPPORTED, "rw T");
+  expect(w4_route(p, 9, 4, 64, 64, W4_SCORE_SOFTMAX, nullptr, 1, 1, 1, 8, 1, 1.0, ip, fp, ip, ip, ip, nullptr, 0, nullptr), W4_ERR_DTYPE, "rt dt");
+  expect(w4_route(p, W4_F32, 4, 64, 64, W4_SCORE_SOFTMAX, nullptr, 7, 1, 1, 8, 1, 1.0, ip, fp, ip, ip, ip, nullptr, 0, nullptr), W4_ERR_GROUP, "rt G");
+  expect(w4_route(p, W4_F32, 4, 64, 63, W4_SCORE_SOFTMAX, nullptr, 1, 1, 1, 8, 1, 1.0, ip, fp, ip, ip, ip, nullptr, 0, nullptr), W4_ERR_ALIGN, "rt ld");
+  expect(w4_route(p, W4_F32, 4000, 64, 64, W4_SCORE_SOFTMAX, nullptr, 1, 1, 1, 8, 1, 1.0, ip, fp, ip, ip, ip, nullptr, 0, nullptr), W4_ERR_INVALID, "rt ws");
+  expect(w4_fp8_block_quantize(p, W4_F32, 4, 256, 256, W4_ACT_NONE, p, fp, nullptr), W4_ERR_DTYPE, "bq dt");
+  expect(w4_fp8_block_quantize(p, W4_BF16, 4, 256, 256, W4_ACT_SWIGLU, p, fp, nullptr), W4_ERR_ALIGN, "bq ldx");
+  expect(w4_fp8_block_quantize(odd, W4_BF16, 4, 256, 256, W4_ACT_NONE, p, fp, nullptr), W4_ERR_ALIGN, "bq x");
+  expect(w4_fp8_block_quantize(nullptr, W4_BF16, 0, 256, 256, W4_ACT_NONE, nullptr, nullptr, nullptr), W4_OK, "bq empty");
+  expect(w4_fp8_block_gemm_workspace_bytes(1, 256, 4096, nullptr), W4_ERR_INVALID, "bw null");
+  expect(w4_fp8_block_gemm_workspace_bytes((int64_t)1 << 62, 256, 4096, &n), W4_ERR_UNSUPPORTED, "bw M");
+  expect(w4_fp8_block_gemm(p, fp, p, fp, nullptr, p, W4_I8, 4, 256, 256, nullptr, 0, nullptr), W4_ERR_DTYPE, "bg dt");
+  expect(w4_fp8_block_gemm(p, fp, p, fp, nullptr, p, W4_BF16, 4, 256, 250, nullptr, 0, nullptr), W4_ERR_ALIGN, "bg K");
+  expect(w4_fp8_block_gemm(p, fp, p, fp, nullptr, odd, W4_BF16, 4, 256, 256, p, 1 << 30, nullptr), W4_ERR_ALIGN, "bg out");
+  expect(w4_fp8_block_gemm(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, W4_BF16, 0, 256, 256, nullptr, 0, nullptr), W4_OK, "bg empty");
+  expect(w4_fp8_block_grouped_gemm(p, fp, ip, ip, 4, p, fp, p, W4_F32, 8, 64, 256, 256, nullptr), W4_ERR_DTYPE, "bgg dt");
+  expect(w4_fp8_block_grouped_gemm(p, fp, ip, ip, 4, p, fp, p, W4_BF16, 1 << 20, 64, 256, 4096, nullptr), W4_ERR_UNSUPPORTED, "bgg T*K");
+  expect(w4_fp8_block_grouped_gemm(p, fp, nullptr, ip, 4, p, fp, p, W4_BF16, 8, 64, 256, 256, nullptr), W4_ERR_INVALID, "bgg rows");
+  expect(w4_combine(p, 9, ip, fp, nullptr, p, 4, 8, 2, 256, nullptr), W4_ERR_DTYPE, "cb dt");
+  expect(w4_combine(p, W4_BF16, ip, fp, nullptr, p, 4, 8, 2, 252, nullptr), W4_ERR_ALIGN, "cb N");
+  expect(w4_combine(p, W4_BF16, ip, fp, odd, p, 4, 8, 2, 256, nullptr), W4_ERR_ALIGN, "cb add");
+  expect(w4_combine(nullptr, W4_BF16, nullptr, nullptr, nullptr, nullptr, 0, 8, 2, 256, nullptr), W4_OK, "cb empty");
   // the longest message paths: every argument named, sizes at their widest
   expect(w4a8_gemm((const int8_t*)p, (const float*)p, p, p, W4_F16, 128, nullptr, p, W4_BF16, 4,
                    (int64_t)1 << 62 | 4, ((int64_t)1 << 62) | 12, nullptr), W4_ERR_UNSUPPORTED, "g huge");
