@@ -16,68 +16,39 @@
 // measured), at half the rate. The weights are the A operand and the activations the
 // B operand, so a lane's 4 results lie in one activation row and share one
 // scale sa * sw, and a lane holds consecutive output columns.
-#include "w4_device.h"
+//
+// Tile kernel: WM x WN waves, each with a tile of 16 MI rows x 16 NJ columns.
+// - Both operands pass through LDS (two stages, one K block each) by LDS DMA.
+//   The DMA is an asm statement: with the builtin the compiler waits for all
+//   of it before the next LDS read, which cost 40% (1149 to 1834 TFLOP/s, with
+//   the order of work below).
+// - A step's last row of MFMAs runs behind the barrier that ends the step:
+//   every fragment of the step is in registers by then, so its stage is free
+//   for the DMA two steps ahead (a whole step in flight) and the next step's
+//   first fragments are read under those MFMAs.
+// - The FMAs of an MFMA follow it by kLag MFMAs, pinned there (left alone the
+//   compiler sinks them past the barrier and keeps every result alive: 60
+//   registers more, and spills in the 256 x 256 tile).
+// - The scales of 4 steps are loaded at a time, multiplied and kept in LDS.
+// - 256 x 256 with 8 waves is the largest tile whose accumulators (128
+//   registers a lane: vector FMAs cannot reach the other 256) leave room; it
+//   reads 3/4 of the LDS bytes per MFMA of a 64 x 64 wave tile.
+#include "fp8_block.h"
 
 namespace w4 {
 
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+constexpr int kLag = 3;
 
-// 8 E4M3 bytes (words w, w + 1 of a fragment) as fp16
-__device__ __forceinline__ v8h e4m3_to_f16(const v8i& f, int w) {
-  v8h h;
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const v2h lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(f[w + q], 1.0f, false);
-    const v2h hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(f[w + q], 1.0f, true);
-    h[4 * q] = lo[0];
-    h[4 * q + 1] = lo[1];
-    h[4 * q + 2] = hi[0];
-    h[4 * q + 3] = hi[1];
-  }
-  return h;
-}
-
-// One scale block: 16 weight rows x 16 activation rows x 128.
-template <bool F16>
-__device__ __forceinline__ v4f block_product(const v8i& w, const v8i& a) {
-  const v4f z = v4f{0.f, 0.f, 0.f, 0.f};
-  if constexpr (F16) {
-    v4f d = z;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      d = __builtin_amdgcn_mfma_f32_16x16x32_f16(e4m3_to_f16(w, 2 * c), e4m3_to_f16(a, 2 * c), d, 0, 0, 0);
-    return d;
-  } else {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, z, 0, 0, 0, 0, 0, 0);
-  }
-}
-
-constexpr int kFK = 128;                             // K step: one scale block
-
-struct Fp8Args {
-  const uint8_t* a;
-  const float* a_scale;
-  const int32_t* row_token;                          // grouped: null = rows in segment order
-  const int32_t* offsets;                            // grouped: [E + 1]
-  const uint8_t* w;
-  const float* w_scale;
-  const void* bias;
-  void* out;                                         // splits > 1: fp32 [splits][M][N]
-  int64_t M;                                         // dense rows, or activation rows (T) of the grouped form
-  int64_t R;                                         // grouped: output rows
-  int E, N, K, KB, NT, NBLK, splits;                 // NBLK: ceil(N / 128)
-  int64_t tiles;                                     // dense: row tiles * NT
-};
-
-// Wave tile 16 MI rows of activations x 16 NJ columns, WM x WN waves.
-template <int MI, int NJ, int WM, int WN, bool GROUPED, int OUT>   // OUT: 0 bf16, 1 fp16, 2 fp32
-__global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
+// OUT: 0 bf16, 1 fp16, 2 fp32.
+template <int MI, int NJ, int WM, int WN, bool GROUPED, bool F16, int OUT>
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args p) {
   constexpr int TH = 64 * WM * WN, BM = 16 * MI * WM, BN = 16 * NJ * WN;
   constexpr int RA = BM * 8 / TH, RB = BN * 8 / TH;  // LDS DMAs per thread and K step
   constexpr int NB = BN > 128 ? BN / 128 : 1;        // weight scale rows per tile
+  static_assert(MI % 2 == 0 && NJ % 2 == 0, "pairs of rows and of column blocks");
   static_assert(RA * TH == BM * 8 && RB * TH == BN * 8, "whole DMAs");
-  __shared__ __attribute__((aligned(16))) uint8_t sA0[BM * kFK], sA1[BM * kFK], sB0[BN * kFK], sB1[BN * kFK];
+  constexpr int STAGE = (BM + BN) * kFK;             // A rows, then weight rows
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
   __shared__ __attribute__((aligned(16))) float sS[2][4][NB][BM];   // sa * sw of 4 K steps, two chunks
 
   // ---- work item
@@ -87,55 +58,13 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   int e = 0, tn, split = 0;
   int64_t r0, row_end, out0 = 0;                     // first row and end of this tile's rows (segment-local if grouped)
   if constexpr (GROUPED) {
-    // row tiles of the experts, 64 experts per round (one per lane)
-    int total = 0;
-    for (int c = 0; c < p.E; c += 64) {
-      int mt = 0;
-      if (c + lane < p.E) mt = (p.offsets[c + lane + 1] - p.offsets[c + lane] + BM - 1) / BM;
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) mt += __shfl_xor(mt, off, kWave);
-      total += mt;
-    }
-    total = __builtin_amdgcn_readfirstlane(total) * p.NT;
-    // block ids go to the 8 XCDs in turn: XCD x takes the x-th eighth of the items
-    const int per = (total + 7) / 8, xi = (int)(blockIdx.x / 8);
-    if (xi >= per) return;
-    const int t = (int)(blockIdx.x % 8) * per + xi;
-    if (t >= total) return;
-    const int want = t / p.NT;                       // row tile, over all experts
-    tn = t - want * p.NT;
-    int cum = 0, mt = 0;
-    e = -1;
-    int seg0 = 0, cnt = 0;
-    for (int c = 0; c < p.E && e < 0; c += 64) {
-      int o0 = 0, o1 = 0;
-      if (c + lane < p.E) {
-        o0 = p.offsets[c + lane];
-        o1 = p.offsets[c + lane + 1];
-      }
-      const int n = (o1 - o0 + BM - 1) / BM;
-      int inc = n;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(inc, off, kWave);
-        if (lane >= off) inc += o;
-      }
-      const unsigned long long hit = __ballot(want < cum + inc);
-      if (hit) {
-        const int src = __ffsll(hit) - 1;
-        e = c + src;
-        mt = want - cum - (__shfl(inc, src, kWave) - __shfl(n, src, kWave));
-        seg0 = __shfl(o0, src, kWave);
-        cnt = __shfl(o1, src, kWave) - seg0;
-      }
-      cum += __shfl(inc, 63, kWave);
-    }
-    if (e < 0) return;
-    e = __builtin_amdgcn_readfirstlane(e);
-    r0 = (int64_t)__builtin_amdgcn_readfirstlane(mt) * BM;
-    out0 = __builtin_amdgcn_readfirstlane(seg0);
-    row_end = __builtin_amdgcn_readfirstlane(cnt);
-    if (out0 + row_end > p.R) row_end = p.R - out0;  // offsets past the output rows
+    const Segment s = find_segment<BM>(p);
+    if (s.e < 0) return;
+    e = s.e;
+    tn = s.tn;
+    r0 = (int64_t)s.mt * BM;
+    out0 = s.row0;
+    row_end = s.rows;
   } else {
     const int64_t t = xcd_remap((int)blockIdx.x, (int)gridDim.x);
     split = (int)(t / p.tiles);
@@ -153,10 +82,9 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   // fragment's row-group parity for the weights, so that the 8 rows that a
   // fragment read touches at a time lie in 8 different chunks. Rows and
   // columns past the end get an offset past the buffer, which reads as zero.
-  constexpr uint32_t kOut = 0x80000000u;
   const int lrow = lane >> 3, lchunk = lane & 7;
   const int64_t abase = (GROUPED && p.row_token) ? 0 : (out0 + r0) * p.K;
-  const int64_t aspan = (GROUPED && p.row_token) ? p.M * p.K : min((int64_t)BM, (GROUPED ? p.M : p.M) - out0 - r0) * p.K;
+  const int64_t aspan = (GROUPED && p.row_token) ? p.M * p.K : min((int64_t)BM, p.M - out0 - r0) * p.K;
   const __amdgpu_buffer_rsrc_t arsrc = make_rsrc(p.a + abase, (uint32_t)max(aspan, (int64_t)0));
   const int64_t wrow0 = (int64_t)e * p.N + n0;
   const __amdgpu_buffer_rsrc_t wrsrc = make_rsrc(p.w + wrow0 * p.K, (uint32_t)((int64_t)min(BN, p.N - n0) * p.K));
@@ -176,58 +104,66 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
     const int r = (TH / 8) * i + 8 * wave + lrow;
     const int c = lchunk ^ (r & 7);
     const int64_t t = token(r);
-    a_off[i] = t >= 0 ? (uint32_t)(t * p.K + 16 * c) : kOut;
+    a_off[i] = t >= 0 ? (uint32_t)(t * p.K + 16 * c) : kPast;
     if (16 * c >= klast) a_dead |= 1u << i;
   }
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
     const int r = (TH / 8) * i + 8 * wave + lrow;
-    const int c = lchunk ^ ((r & 3) + 4 * ((r / (4 * NJ)) & 1));
-    b_off[i] = n0 + r < p.N ? (uint32_t)((int64_t)r * p.K + 16 * c) : kOut;
+    const int c = lchunk ^ ((r & 3) + 4 * ((r >> 3) & 1));
+    b_off[i] = n0 + r < p.N ? (uint32_t)((int64_t)r * p.K + 16 * c) : kPast;
     if (16 * c >= klast) b_dead |= 1u << i;
   }
-  auto gload = [&](int tk, uint8_t* sa, uint8_t* sb) {
-    const bool last = tk == p.KB - 1;
-    const uint32_t ks = (uint32_t)tk * kFK;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  const uint32_t ldsw = __builtin_amdgcn_readfirstlane(lds0 + 8 * wave * kFK);
+  auto dma = [&](const __amdgpu_buffer_rsrc_t rs, uint32_t dst, uint32_t off, uint32_t ks) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(dst), "v"(off), "s"(rs), "s"(ks) : "memory");
+  };
+  // DMA q of a K step: the activations' RA, then the weights' RB
+  auto gload1 = [&](int tk, uint32_t stage, int q) {
+    const bool act = q < RA;
+    const int i = act ? q : q - RA;
+    uint32_t off = act ? a_off[i] : b_off[i];
+    if (tk == p.KB - 1 && (((act ? a_dead : b_dead) >> i) & 1)) off = kPast;
+    dma(act ? arsrc : wrsrc, ldsw + stage + ((act ? 0 : BM) + (TH / 8) * i) * kFK, off, (uint32_t)tk * kFK);
+  };
+  auto gload = [&](int tk, uint32_t stage) {
 #pragma unroll
-    for (int i = 0; i < RA; ++i) {
-      const uint32_t off = (last && ((a_dead >> i) & 1)) ? kOut : a_off[i];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          arsrc, (__attribute__((address_space(3))) void*)(sa + ((TH / 8) * i + 8 * wave) * kFK), 16, off, ks, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      const uint32_t off = (last && ((b_dead >> i) & 1)) ? kOut : b_off[i];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          wrsrc, (__attribute__((address_space(3))) void*)(sb + ((TH / 8) * i + 8 * wave) * kFK), 16, off, ks, 0, 0);
-    }
+    for (int q = 0; q < RA + RB; ++q) gload1(tk, stage, q);
   };
 
   // ---- scales: products sa * sw of 4 K steps at a time, thread (row, weight
   // block); LDS row order [wave row][16][MI], so a lane reads its MI in a run
   constexpr int RS = (BM * NB + TH - 1) / TH;
-  auto load_scales = [&](int tk, float (&s)[RS][4]) {
+  const int64_t sspan = (GROUPED && p.row_token) ? p.M * p.KB : min((int64_t)BM, p.M - out0 - r0) * p.KB;
+  const __amdgpu_buffer_rsrc_t asr = make_rsrc(p.a_scale + ((GROUPED && p.row_token) ? 0 : (out0 + r0) * p.KB),
+                                               (uint32_t)max(sspan * 4, (int64_t)0));
+  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(p.w_scale + ((int64_t)e * p.NBLK + n0 / 128) * p.KB,
+                                               (uint32_t)((int64_t)min(NB, p.NBLK - n0 / 128) * p.KB * 4));
+  uint32_t sa_off[RS], sw_off[RS];
+#pragma unroll
+  for (int i = 0; i < RS; ++i) {
+    const int u = tid + TH * i, r = u % BM, nb = u / BM;
+    const int64_t t = u < BM * NB ? token(r) : -1;
+    sa_off[i] = t >= 0 ? (uint32_t)(t * p.KB * 4) : kPast;
+    sw_off[i] = (uint32_t)(nb * p.KB * 4);
+  }
+  auto load_scales = [&](int tk, v4i (&s)[RS][2]) {
 #pragma unroll
     for (int i = 0; i < RS; ++i) {
-      const int u = tid + TH * i, r = u % BM, nb = u / BM;
-      const int64_t t = u < BM * NB ? token(r) : -1;
-      const int64_t arow = (GROUPED && p.row_token) ? t : out0 + r0 + t;
-      const int wb = n0 / 128 + nb;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = t >= 0 && tk + j < k1 && wb < p.NBLK;
-        s[i][j] = in ? p.a_scale[arow * p.KB + tk + j] * p.w_scale[((int64_t)e * p.NBLK + wb) * p.KB + tk + j] : 0.f;
-      }
+      s[i][0] = __builtin_amdgcn_raw_buffer_load_b128(asr, sa_off[i], 4u * (uint32_t)tk, 0);
+      s[i][1] = __builtin_amdgcn_raw_buffer_load_b128(wsr, sw_off[i], 4u * (uint32_t)tk, 0);
     }
   };
-  auto store_scales = [&](int buf, const float (&s)[RS][4]) {
+  auto store_scales = [&](int buf, const v4i (&s)[RS][2]) {
 #pragma unroll
     for (int i = 0; i < RS; ++i) {
       const int u = tid + TH * i, r = u % BM, nb = u / BM;
       if (u >= BM * NB) break;
       const int at = (r / (16 * MI)) * 16 * MI + (r % 16) * MI + (r / 16) % MI;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sS[buf][j][nb][at] = s[i][j];
+      for (int j = 0; j < 4; ++j) sS[buf][j][nb][at] = __int_as_float(s[i][0][j]) * __int_as_float(s[i][1][j]);
     }
   };
 
@@ -242,93 +178,169 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   // wave's 16 NJ, so a lane's results are 4 NJ consecutive columns.
   const int ar = 16 * MI * wm + l16;                 // + 16 i; 16 i leaves f unchanged
   const int a_ro = ar * kFK + 16 * (g ^ (ar & 7)), a_rx = ar * kFK + 16 * ((g + 4) ^ (ar & 7));
-  const int br = 16 * NJ * wn + 4 * NJ * (l16 >> 2) + (l16 & 3);
-  const int bpar = (l16 >> 2) & 1;                   // parity of br / (4 NJ): + 4 j stays inside the run of 4 NJ
-  const int b_ro = br * kFK + 16 * (g ^ ((br & 3) + 4 * bpar)), b_rx = br * kFK + 16 * ((g + 4) ^ ((br & 3) + 4 * bpar));
+  const int br = 16 * NJ * wn + 8 * (l16 >> 2) + (l16 & 3);   // + 32 (j / 2) + 4 (j % 2): those leave f unchanged
+  const int bfx = (l16 & 3) + 4 * ((l16 >> 2) & 1);
+  const int b_ro = (BM + br) * kFK + 16 * (g ^ bfx), b_rx = (BM + br) * kFK + 16 * ((g + 4) ^ bfx);
   const int snb = (16 * NJ * wn) / 128 % NB;
-
-  auto kstep = [&](int tk, const uint8_t* sa, const uint8_t* sb) {
-    const int rel = tk - k0;
-    float s[MI];
-#pragma unroll
-    for (int i = 0; i < MI; ++i) s[i] = sS[(rel >> 2) & 1][rel & 3][snb][16 * MI * wm + l16 * MI + i];
-    v8i bf[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const v4i x0 = *reinterpret_cast<const v4i*>(sb + b_ro + 4 * j * kFK);
-      const v4i x1 = *reinterpret_cast<const v4i*>(sb + b_rx + 4 * j * kFK);
-      bf[j] = v8i{x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
-    }
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const v4i x0 = *reinterpret_cast<const v4i*>(sa + a_ro + 16 * i * kFK);
-      const v4i x1 = *reinterpret_cast<const v4i*>(sa + a_rx + 16 * i * kFK);
-      const v8i af = v8i{x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const v4f d = block_product<OUT == 2>(bf[j], af);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[r], s[i], acc[i][j][r]);
-      }
-    }
+  auto frag = [&](const uint8_t* q0, const uint8_t* q1) -> v8i {
+    const v4i x0 = *reinterpret_cast<const v4i*>(q0);
+    const v4i x1 = *reinterpret_cast<const v4i*>(q1);
+    return v8i{x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
   };
 
+  constexpr int NM = MI * NJ;
   if (k0 < k1) {
-    float sc[RS][4];
+    v4i sc[RS][2];
     load_scales(k0, sc);
-    gload(k0, sA0, sB0);
+    gload(k0, 0);
     store_scales(0, sc);
-    __syncthreads();
-    for (int tk = k0; tk < k1; tk += 2) {
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    v8i bf[NJ], af[2];
+    af[0] = frag(lds + a_ro, lds + a_rx);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) bf[j] = frag(lds + b_ro + (32 * (j / 2) + 4 * (j % 2)) * kFK, lds + b_rx + (32 * (j / 2) + 4 * (j % 2)) * kFK);
+    if (k0 + 1 < k1) gload(k0 + 1, STAGE);
+    for (int tk = k0; tk < k1; ++tk) {
       const int rel = tk - k0;
+      const uint8_t* cur = lds + (rel & 1) * STAGE;
+      const uint8_t* nxt = lds + (1 - (rel & 1)) * STAGE;
+      const float* sp = &sS[(rel >> 2) & 1][rel & 3][snb][16 * MI * wm + l16 * MI];
+      float s[MI];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) s[i] = sp[i];
       const bool fetch = (rel & 3) == 0 && tk + 4 < k1;
       if (fetch) load_scales(tk + 4, sc);
-      if (tk + 1 < k1) gload(tk + 1, sA1, sB1);
-      kstep(tk, sA0, sB0);
-      if (fetch) store_scales(((rel >> 2) + 1) & 1, sc);
-      __syncthreads();
-      if (tk + 1 >= k1) break;
-      if (tk + 2 < k1) gload(tk + 2, sA0, sB0);
-      kstep(tk + 1, sA1, sB1);
-      __syncthreads();
+      const bool more = tk + 2 < k1;
+      v4f d[kLag + 1];
+#pragma unroll
+      for (int n = 0; n < NM + kLag; ++n) {
+        const int i = n / NJ, j = n % NJ;
+        if (n < NM) {
+          if (j == 0) {
+            if (i + 1 < MI) {
+              af[(i + 1) & 1] = frag(cur + a_ro + 16 * (i + 1) * kFK, cur + a_rx + 16 * (i + 1) * kFK);
+            } else {
+              if (fetch) store_scales(((rel >> 2) + 1) & 1, sc);
+              __builtin_amdgcn_s_waitcnt(0);
+              asm volatile("s_barrier" ::: "memory");
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+          d[n % (kLag + 1)] = block_product<F16>(bf[j], af[i & 1]);
+          if (i == MI - 1) {
+            bf[j] = frag(nxt + b_ro + (32 * (j / 2) + 4 * (j % 2)) * kFK, nxt + b_rx + (32 * (j / 2) + 4 * (j % 2)) * kFK);
+            if (j == 0) af[0] = frag(nxt + a_ro, nxt + a_rx);
+            constexpr int Q = (RA + RB + NJ - 1) / NJ;
+            if (more) {
+#pragma unroll
+              for (int q = j * Q; q < (j + 1) * Q && q < RA + RB; ++q) gload1(tk + 2, (rel & 1) * STAGE, q);
+            }
+          }
+        }
+        if (n >= kLag) {
+          const int m = n - kLag;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[m / NJ][m % NJ][r] = fmaf(d[m % (kLag + 1)][r], s[m / NJ], acc[m / NJ][m % NJ][r]);
+          asm volatile("" : "+v"(acc[m / NJ][m % NJ]));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
 
   // ---- output: lane's row per i, 4 NJ consecutive columns
-  const int nw = n0 + 16 * NJ * wn + 4 * NJ * g;
+  const int nw = n0 + 16 * NJ * wn + 8 * g;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int64_t r = r0 + 16 * MI * wm + 16 * i + l16;
     if (r >= row_end) continue;
     const int64_t orow = (out0 + r + (int64_t)split * p.M) * p.N;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int n = nw + 4 * j;
+    for (int j = 0; j < NJ; j += 2) {
+      const int n = nw + 16 * j;
       if (n >= p.N) continue;
-      float f[4];
+      float f[8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) f[c] = acc[i][j][c];
-      if (!GROUPED && p.bias && p.splits == 1) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          f[c] += OUT == 2 ? static_cast<const float*>(p.bias)[n + c]
-                           : (OUT == 0 ? bf16_to_f32(static_cast<const uint16_t*>(p.bias)[n + c])
-                                       : f16_to_f32(static_cast<const uint16_t*>(p.bias)[n + c]));
-      }
-      if constexpr (OUT == 2) {
-        *reinterpret_cast<v4f*>(static_cast<float*>(p.out) + orow + n) = v4f{f[0], f[1], f[2], f[3]};
-      } else {
-        uint32_t h[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) h[c] = OUT == 0 ? f32_to_bf16_rne(f[c]) : f32_to_f16_rne(f[c]);
-        *reinterpret_cast<v2i*>(static_cast<uint16_t*>(p.out) + orow + n) =
-            v2i{(int)(h[0] | (h[1] << 16)), (int)(h[2] | (h[3] << 16))};
-      }
+      for (int c = 0; c < 8; ++c) f[c] = acc[i][j + c / 4][c % 4];
+      store_columns<OUT, 8>(p, f, orow, n, !GROUPED && p.bias && p.splits == 1);
     }
   }
 }
 
-size_t fp8_block_gemm_workspace(int64_t M, int64_t N, int64_t K) { return 0; }
+// Split K: the partial sums [splits][rows][N], in order, to the output.
+template <int OUT>
+__global__ __launch_bounds__(256) void fp8_reduce_kernel(Fp8Args p, const float* __restrict__ part) {
+  const int nc = p.N >> 3;
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= p.M * nc) return;
+  const int64_t span = p.M * p.N;
+  const float* q = part + c * 8;
+  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < p.splits; ++s, q += span) {
+    const v4f x = *reinterpret_cast<const v4f*>(q), y = *reinterpret_cast<const v4f*>(q + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] += x[e];
+      f[4 + e] += y[e];
+    }
+  }
+  store_columns<OUT, 8>(p, f, c / nc * p.N, (int)(c % nc) * 8, p.bias != nullptr);
+}
+
+// What the dense product runs as: rows streamed, or a tile and its K splits.
+struct DensePlan {
+  int tile;                                          // 0: streamed; else the tile's side in rows (64, 128, 256)
+  int splits;
+};
+
+static DensePlan plan_dense(int64_t M, int64_t N, int64_t K) {
+  if (M <= 64) return {0, 1};
+  const int64_t KB = (K + 127) / 128;
+  auto tiles = [&](int64_t b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
+  if (tiles(256) >= 192) return {256, 1};
+  const int64_t t = tiles(128);
+  int64_t splits = 512 / t;
+  if (splits > KB / 4) splits = KB / 4;
+  if (splits < 1) splits = 1;
+  return {128, (int)splits};
+}
+
+size_t fp8_block_gemm_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || N == 0) return 0;
+  const DensePlan pl = plan_dense(M, N, K);
+  return pl.splits > 1 ? (size_t)pl.splits * (size_t)M * (size_t)N * 4 : 0;
+}
+
+// f16: the fp32-exact products (fp32 results)
+template <int MI, int NJ, int WM, int WN>
+static hipError_t tile_go(Fp8Args p, bool f16, int out_dt, hipStream_t stream) {
+  constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN;
+  p.NT = (p.N + BN - 1) / BN;
+  const dim3 block(64 * WM * WN);
+  auto go = [&](auto kernel, dim3 grid) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p); };
+  if (p.offsets) {
+    const int64_t items = (p.R / BM + (p.E < p.R ? p.E : p.R)) * p.NT;
+    const dim3 grid((unsigned)((items + 7) / 8 * 8));
+    if (out_dt == 0) go(fp8_tile_kernel<MI, NJ, WM, WN, true, false, 0>, grid);
+    else go(fp8_tile_kernel<MI, NJ, WM, WN, true, false, 1>, grid);
+  } else {
+    p.tiles = (p.M + BM - 1) / BM * p.NT;
+    const dim3 grid((unsigned)(p.tiles * p.splits));
+    if constexpr (MI * NJ <= 16) {
+      if (f16) {
+        go(fp8_tile_kernel<MI, NJ, WM, WN, false, true, 2>, grid);
+        return hipGetLastError();
+      }
+    }
+    if (out_dt == 0) go(fp8_tile_kernel<MI, NJ, WM, WN, false, false, 0>, grid);
+    else if (out_dt == 1) go(fp8_tile_kernel<MI, NJ, WM, WN, false, false, 1>, grid);
+    else go(fp8_tile_kernel<MI, NJ, WM, WN, false, false, 2>, grid);   // partial sums
+  }
+  return hipGetLastError();
+}
 
 hipError_t launch_fp8_block_gemm(const void* a, const float* a_scale, const void* w, const float* w_scale,
                                  const void* bias, void* out, int out_dt, int64_t M, int64_t N, int64_t K, void* ws,
@@ -347,14 +359,21 @@ hipError_t launch_fp8_block_gemm(const void* a, const float* a_scale, const void
   p.K = (int)K;
   p.KB = (int)((K + 127) / 128);
   p.NBLK = (int)((N + 127) / 128);
-  p.splits = 1;
-  constexpr int BM = 64, BN = 64;
-  p.NT = (int)((N + BN - 1) / BN);
-  p.tiles = (M + BM - 1) / BM * p.NT;
-  const dim3 grid((unsigned)p.tiles), block(256);
-  if (out_dt == 0) hipLaunchKernelGGL((fp8_tile_kernel<2, 2, 2, 2, false, 0>), grid, block, 0, stream, p);
-  else if (out_dt == 1) hipLaunchKernelGGL((fp8_tile_kernel<2, 2, 2, 2, false, 1>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((fp8_tile_kernel<2, 2, 2, 2, false, 2>), grid, block, 0, stream, p);
+  const DensePlan pl = plan_dense(M, N, K);
+  p.splits = pl.splits;
+  if (pl.tile == 0) return launch_fp8_stream(p, out_dt, M, stream);
+  Fp8Args part = p;
+  if (p.splits > 1) part.out = ws;
+  const int dt = p.splits > 1 ? 2 : out_dt;
+  // (converting to fp16 in the 256 x 256 tile spills registers)
+  const hipError_t e = pl.tile == 256 && out_dt != 2 ? tile_go<8, 4, 2, 4>(part, false, dt, stream)
+                                      : tile_go<4, 4, 2, 2>(part, out_dt == 2, dt, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const dim3 grid((unsigned)((M * (N / 8) + 255) / 256)), block(256);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p, static_cast<const float*>(ws)); };
+  if (out_dt == 0) go(fp8_reduce_kernel<0>);
+  else if (out_dt == 1) go(fp8_reduce_kernel<1>);
+  else go(fp8_reduce_kernel<2>);
   return hipGetLastError();
 }
 
@@ -378,14 +397,10 @@ hipError_t launch_fp8_block_grouped(const void* a, const float* a_scale, const i
   p.KB = (int)((K + 127) / 128);
   p.NBLK = (int)((N + 127) / 128);
   p.splits = 1;
-  constexpr int BM = 64, BN = 64;
-  p.NT = (int)((N + BN - 1) / BN);
-  const int64_t upper = (R / BM + (E < R ? E : R)) * p.NT;
-  const dim3 grid((unsigned)((upper + 7) / 8 * 8)), block(256);
-  if (out_dt == 0) hipLaunchKernelGGL((fp8_tile_kernel<2, 2, 2, 2, true, 0>), grid, block, 0, stream, p);
-  else if (out_dt == 1) hipLaunchKernelGGL((fp8_tile_kernel<2, 2, 2, 2, true, 1>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((fp8_tile_kernel<2, 2, 2, 2, true, 2>), grid, block, 0, stream, p);
-  return hipGetLastError();
+  const int64_t avg = (R + E - 1) / E;
+  if (avg <= 24) return launch_fp8_stream(p, out_dt, avg, stream);
+  if (avg <= 128) return tile_go<4, 4, 2, 2>(p, false, out_dt, stream);
+  return tile_go<8, 4, 2, 4>(p, false, out_dt, stream);
 }
 
 }  // namespace w4

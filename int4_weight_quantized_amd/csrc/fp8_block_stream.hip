@@ -1,0 +1,144 @@
+// Block-scaled FP8 products of few rows (a decode step: up to 64 dense rows,
+// or experts that hold a handful each): the weights are streamed once.
+//
+// The arithmetic is that of fp8_block_gemm.hip; with so few rows the time is
+// the weights' bytes. A block of WS waves owns 16 NJ weight rows (output
+// columns) and 16 MI activation rows; its waves take the K blocks in turn,
+// each loading weights and activations straight into the registers the matrix
+// instruction reads (a weight byte is used by one wave only, so LDS would add
+// a copy), and their sums meet in LDS at the end. Without a barrier in the
+// loop, every resident wave keeps U K blocks of loads in flight.
+#include "fp8_block.h"
+
+namespace w4 {
+
+template <int MI, int NJ, int WS, int U, bool GROUPED, bool F16, int OUT>
+__global__ __launch_bounds__(64 * WS) void fp8_stream_kernel(Fp8Args p) {
+  constexpr int BM = 16 * MI, BN = 16 * NJ, NQ = MI * NJ * 64;   // NQ: quads of results
+  __shared__ __attribute__((aligned(16))) v4f red[WS][NQ];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, l16 = lane & 15;
+  int e = 0, tn;
+  int64_t r0, rows, out0 = 0;                        // first row of the tile, end of the rows (segment-local if grouped)
+  if constexpr (GROUPED) {
+    const Segment s = find_segment<BM>(p);
+    if (s.e < 0) return;
+    e = s.e;
+    tn = s.tn;
+    r0 = (int64_t)s.mt * BM;
+    out0 = s.row0;
+    rows = s.rows;
+  } else {
+    tn = (int)(blockIdx.x % (unsigned)p.NT);
+    r0 = (int64_t)(blockIdx.x / (unsigned)p.NT) * BM;
+    rows = p.M;
+  }
+  const int n0 = tn * BN;
+
+  const bool gather = GROUPED && p.row_token;
+  const int64_t base = gather ? 0 : out0 + r0, left = gather ? p.M : min((int64_t)BM, p.M - base);
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.a + base * p.K, (uint32_t)max(left * p.K, (int64_t)0));
+  const __amdgpu_buffer_rsrc_t asr = make_rsrc(p.a_scale + base * p.KB, (uint32_t)max(left * p.KB * 4, (int64_t)0));
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.w + ((int64_t)e * p.N + n0) * p.K, (uint32_t)(min(BN, p.N - n0) * (int64_t)p.K));
+  const float* __restrict__ ws = p.w_scale + ((int64_t)e * p.NBLK + n0 / 128) * p.KB;   // BN divides 128: one row of scales
+  uint32_t a_off[MI], s_off[MI], w_off[NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t r = r0 + 16 * i + l16;
+    int64_t t = r < rows ? (gather ? (int64_t)p.row_token[out0 + r] : 16 * i + l16) : -1;
+    if (gather && t >= p.M) t = -1;
+    if (!gather && t >= left) t = -1;
+    a_off[i] = t >= 0 ? (uint32_t)(t * p.K + 16 * g) : kPast;
+    s_off[i] = t >= 0 ? (uint32_t)(t * p.KB * 4) : kPast;
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+    w_off[j] = n0 + 16 * j + l16 < p.N ? (uint32_t)((16 * j + l16) * (int64_t)p.K + 16 * g) : kPast;
+
+  // the 16-byte chunks g and g + 4 of a K block; past K's end they read as zero
+  auto load = [&](const __amdgpu_buffer_rsrc_t rs, uint32_t off, int kb) -> v8i {
+    const uint32_t ks = (uint32_t)kb * kFK, end = (uint32_t)p.K - ks;
+    const v4i x = __builtin_amdgcn_raw_buffer_load_b128(rs, 16u * g < end ? off : kPast, ks, 0);
+    const v4i y = __builtin_amdgcn_raw_buffer_load_b128(rs, 16u * g + 64u < end ? (off == kPast ? kPast : off + 64u) : kPast, ks, 0);
+    return v8i{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+  };
+  v4f acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int kb = wave; kb < p.KB; kb += WS * U) {
+    v8i wf[U][NJ], af[U][MI];
+    float s[U][MI], sw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = min(kb + WS * u, p.KB - 1);      // past the end: loaded again, not used
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) wf[u][j] = load(wr, w_off[j], k);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) af[u][i] = load(ar, a_off[i], k);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+        s[u][i] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(asr, s_off[i], 4u * (uint32_t)k, 0));
+      sw[u] = ws[k];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (kb + WS * u >= p.KB) break;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const float sc = s[u][i] * sw[u];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const v4f d = block_product<F16>(wf[u][j], af[u][i]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[r], sc, acc[i][j][r]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) red[wave][(i * NJ + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  for (int q = tid; q < NQ; q += 64 * WS) {
+    const int i = q / (64 * NJ), j = q / 64 % NJ;
+    const int64_t r = r0 + 16 * i + l16;
+    const int n = n0 + 16 * j + 4 * g;
+    if (r >= rows || n >= p.N) continue;
+    v4f v = red[0][q];
+#pragma unroll
+    for (int w = 1; w < WS; ++w) v += red[w][q];
+    float f[4] = {v[0], v[1], v[2], v[3]};
+    store_columns<OUT, 4>(p, f, (out0 + r) * p.N, n, !GROUPED && p.bias);
+  }
+}
+
+template <int MI, int NJ, int WS, int U>
+static hipError_t stream_go(Fp8Args p, int out_dt, hipStream_t stream) {
+  constexpr int BM = 16 * MI, BN = 16 * NJ;
+  p.NT = (p.N + BN - 1) / BN;
+  const dim3 block(64 * WS);
+  if (p.offsets) {
+    const int64_t items = (p.R / BM + (p.E < p.R ? p.E : p.R)) * p.NT;
+    const dim3 grid((unsigned)((items + 7) / 8 * 8));
+    if (out_dt == 0) hipLaunchKernelGGL((fp8_stream_kernel<MI, NJ, WS, U, true, false, 0>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((fp8_stream_kernel<MI, NJ, WS, U, true, false, 1>), grid, block, 0, stream, p);
+  } else {
+    const dim3 grid((unsigned)((p.M + BM - 1) / BM * p.NT));
+    if (out_dt == 0) hipLaunchKernelGGL((fp8_stream_kernel<MI, NJ, WS, U, false, false, 0>), grid, block, 0, stream, p);
+    else if (out_dt == 1) hipLaunchKernelGGL((fp8_stream_kernel<MI, NJ, WS, U, false, false, 1>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((fp8_stream_kernel<MI, NJ, WS, U, false, true, 2>), grid, block, 0, stream, p);
+  }
+  return hipGetLastError();
+}
+
+// rows: the product's, or an expert's on average
+hipError_t launch_fp8_stream(const Fp8Args& p, int out_dt, int64_t rows, hipStream_t stream) {
+  if (rows <= (p.offsets ? 4 : 16)) return stream_go<1, 2, 4, 2>(p, out_dt, stream);
+  if (rows <= 32 && !p.offsets) return stream_go<2, 4, 4, 1>(p, out_dt, stream);
+  return stream_go<4, 4, 4, 1>(p, out_dt, stream);
+}
+
+}  // namespace w4
