@@ -148,6 +148,6 @@ __device__ __forceinline__ void store_columns(const Fp8Args& p, float (&f)[C], i
   }
 }
 
-hipError_t launch_fp8_stream(const Fp8Args& p, int out_dt, int64_t rows, hipStream_t stream);
+hipError_t launch_fp8_stream(const Fp8Args& p, int out_dt, hipStream_t stream);
 
 }  // namespace w4

@@ -47,9 +47,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args p) {
   constexpr int NB = BN > 128 ? BN / 128 : 1;        // weight scale rows per tile
   static_assert(MI % 2 == 0 && NJ % 2 == 0, "pairs of rows and of column blocks");
   static_assert(RA * TH == BM * 8 && RB * TH == BN * 8, "whole DMAs");
-  constexpr int STAGE = (BM + BN) * kFK;             // A rows, then weight rows
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
-  __shared__ __attribute__((aligned(16))) float sS[2][4][NB][BM];   // sa * sw of 4 K steps, two chunks
+  constexpr int STAGE = (BM + BN) * kFK, CHUNK = TH * 16;
+  static_assert(BM + NB <= TH, "a row of scales per thread");
+  // two stages (activation rows, then weight rows), two chunks of the scales of 4 K steps (sa of each row, then sw)
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE + 2 * CHUNK];
 
   // ---- work item
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -120,51 +121,42 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args p) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(dst), "v"(off), "s"(rs), "s"(ks) : "memory");
   };
-  // DMA q of a K step: the activations' RA, then the weights' RB
-  auto gload1 = [&](int tk, uint32_t stage, int q) {
-    const bool act = q < RA;
-    const int i = act ? q : q - RA;
-    uint32_t off = act ? a_off[i] : b_off[i];
-    if (tk == p.KB - 1 && (((act ? a_dead : b_dead) >> i) & 1)) off = kPast;
-    dma(act ? arsrc : wrsrc, ldsw + stage + ((act ? 0 : BM) + (TH / 8) * i) * kFK, off, (uint32_t)tk * kFK);
-  };
-  auto gload = [&](int tk, uint32_t stage) {
-#pragma unroll
-    for (int q = 0; q < RA + RB; ++q) gload1(tk, stage, q);
-  };
-
-  // ---- scales: products sa * sw of 4 K steps at a time, thread (row, weight
-  // block); LDS row order [wave row][16][MI], so a lane reads its MI in a run
-  constexpr int RS = (BM * NB + TH - 1) / TH;
+  // the row of scales that this thread fetches
   const int64_t sspan = (GROUPED && p.row_token) ? p.M * p.KB : min((int64_t)BM, p.M - out0 - r0) * p.KB;
   const __amdgpu_buffer_rsrc_t asr = make_rsrc(p.a_scale + ((GROUPED && p.row_token) ? 0 : (out0 + r0) * p.KB),
                                                (uint32_t)max(sspan * 4, (int64_t)0));
   const __amdgpu_buffer_rsrc_t wsr = make_rsrc(p.w_scale + ((int64_t)e * p.NBLK + n0 / 128) * p.KB,
                                                (uint32_t)((int64_t)min(NB, p.NBLK - n0 / 128) * p.KB * 4));
-  uint32_t sa_off[RS], sw_off[RS];
-#pragma unroll
-  for (int i = 0; i < RS; ++i) {
-    const int u = tid + TH * i, r = u % BM, nb = u / BM;
-    const int64_t t = u < BM * NB ? token(r) : -1;
-    sa_off[i] = t >= 0 ? (uint32_t)(t * p.KB * 4) : kPast;
-    sw_off[i] = (uint32_t)(nb * p.KB * 4);
+  const bool rows_wave = 64 * wave < BM;             // BM is a multiple of 64: a wave fetches sa or sw
+  uint32_t s_off;
+  if (rows_wave) {
+    const int64_t t = token(tid);
+    s_off = t >= 0 ? (uint32_t)(t * p.KB * 4) : kPast;
+  } else {
+    s_off = tid - BM < NB ? (uint32_t)((tid - BM) * p.KB * 4) : kPast;
   }
-  auto load_scales = [&](int tk, v4i (&s)[RS][2]) {
-#pragma unroll
-    for (int i = 0; i < RS; ++i) {
-      s[i][0] = __builtin_amdgcn_raw_buffer_load_b128(asr, sa_off[i], 4u * (uint32_t)tk, 0);
-      s[i][1] = __builtin_amdgcn_raw_buffer_load_b128(wsr, sw_off[i], 4u * (uint32_t)tk, 0);
+  // DMA q of a K step: the activations' RA, the weights' RB, then every 4
+  // steps the scales (of steps past K: whatever follows, not used)
+  constexpr int ND = RA + RB + 1;
+  auto gload1 = [&](int tk, uint32_t stage, int q) {
+    const uint32_t ks = (uint32_t)tk * kFK;
+    if (q == RA + RB) {
+      const int rel = tk - k0;
+      if (rel & 3) return;
+      const uint32_t dst = lds0 + 2 * STAGE + ((rel >> 2) & 1) * CHUNK + 1024 * wave;
+      if (rows_wave) dma(asr, dst, s_off, (uint32_t)tk * 4);
+      else dma(wsr, dst, s_off, (uint32_t)tk * 4);
+      return;
     }
+    const bool act = q < RA;
+    const int i = act ? q : q - RA;
+    uint32_t off = act ? a_off[i] : b_off[i];
+    if (tk == p.KB - 1 && (((act ? a_dead : b_dead) >> i) & 1)) off = kPast;
+    dma(act ? arsrc : wrsrc, ldsw + stage + ((act ? 0 : BM) + (TH / 8) * i) * kFK, off, ks);
   };
-  auto store_scales = [&](int buf, const v4i (&s)[RS][2]) {
+  auto gload = [&](int tk, uint32_t stage) {
 #pragma unroll
-    for (int i = 0; i < RS; ++i) {
-      const int u = tid + TH * i, r = u % BM, nb = u / BM;
-      if (u >= BM * NB) break;
-      const int at = (r / (16 * MI)) * 16 * MI + (r % 16) * MI + (r / 16) % MI;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sS[buf][j][nb][at] = __int_as_float(s[i][0][j]) * __int_as_float(s[i][1][j]);
-    }
+    for (int q = 0; q < ND; ++q) gload1(tk, stage, q);
   };
 
   v4f acc[MI][NJ];
@@ -190,29 +182,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args p) {
 
   constexpr int NM = MI * NJ;
   if (k0 < k1) {
-    v4i sc[RS][2];
-    load_scales(k0, sc);
     gload(k0, 0);
-    store_scales(0, sc);
-    __builtin_amdgcn_s_waitcnt(0);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    if (k0 + 1 < k1) gload(k0 + 1, STAGE);
     v8i bf[NJ], af[2];
     af[0] = frag(lds + a_ro, lds + a_rx);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) bf[j] = frag(lds + b_ro + (32 * (j / 2) + 4 * (j % 2)) * kFK, lds + b_rx + (32 * (j / 2) + 4 * (j % 2)) * kFK);
-    if (k0 + 1 < k1) gload(k0 + 1, STAGE);
+    for (int j = 0; j < NJ; ++j)
+      bf[j] = frag(lds + b_ro + (32 * (j / 2) + 4 * (j % 2)) * kFK, lds + b_rx + (32 * (j / 2) + 4 * (j % 2)) * kFK);
     for (int tk = k0; tk < k1; ++tk) {
       const int rel = tk - k0;
-      const uint8_t* cur = lds + (rel & 1) * STAGE;
-      const uint8_t* nxt = lds + (1 - (rel & 1)) * STAGE;
-      const float* sp = &sS[(rel >> 2) & 1][rel & 3][snb][16 * MI * wm + l16 * MI];
+      const uint32_t st = (rel & 1) * STAGE;         // this step's stage
+      const uint8_t* cur = lds + st;
+      const uint8_t* nxt = lds + (STAGE - st);
+      const float* sp = reinterpret_cast<const float*>(lds + 2 * STAGE + ((rel >> 2) & 1) * CHUNK) + (rel & 3);
+      const float sw = sp[4 * (BM + snb)];
       float s[MI];
 #pragma unroll
-      for (int i = 0; i < MI; ++i) s[i] = sp[i];
-      const bool fetch = (rel & 3) == 0 && tk + 4 < k1;
-      if (fetch) load_scales(tk + 4, sc);
-      const bool more = tk + 2 < k1;
+      for (int i = 0; i < MI; ++i) s[i] = sp[4 * (16 * (MI * wm + i) + l16)];
       v4f d[kLag + 1];
 #pragma unroll
       for (int n = 0; n < NM + kLag; ++n) {
@@ -222,22 +209,26 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args p) {
             if (i + 1 < MI) {
               af[(i + 1) & 1] = frag(cur + a_ro + 16 * (i + 1) * kFK, cur + a_rx + 16 * (i + 1) * kFK);
             } else {
-              if (fetch) store_scales(((rel >> 2) + 1) & 1, sc);
-              __builtin_amdgcn_s_waitcnt(0);
-              asm volatile("s_barrier" ::: "memory");
+              // every fragment of this step is in registers; once the next step's tiles have landed: swap
+              asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
               __builtin_amdgcn_sched_barrier(0);
             }
           }
           d[n % (kLag + 1)] = block_product<F16>(bf[j], af[i & 1]);
           if (i == MI - 1) {
+            // the next step's fragments (at the end: of a stage whose contents are not used)
             bf[j] = frag(nxt + b_ro + (32 * (j / 2) + 4 * (j % 2)) * kFK, nxt + b_rx + (32 * (j / 2) + 4 * (j % 2)) * kFK);
             if (j == 0) af[0] = frag(nxt + a_ro, nxt + a_rx);
-            constexpr int Q = (RA + RB + NJ - 1) / NJ;
-            if (more) {
+            constexpr int Q = (ND + NJ - 1) / NJ;
+            if (tk + 2 < k1) {
 #pragma unroll
-              for (int q = j * Q; q < (j + 1) * Q && q < RA + RB; ++q) gload1(tk + 2, (rel & 1) * STAGE, q);
+              for (int q = j * Q; q < (j + 1) * Q && q < ND; ++q) gload1(tk + 2, st, q);
             }
           }
+        }
+        if (n == kLag) {
+#pragma unroll
+          for (int i2 = 0; i2 < MI; ++i2) s[i2] *= sw;
         }
         if (n >= kLag) {
           const int m = n - kLag;
@@ -279,6 +270,7 @@ __global__ __launch_bounds__(256) void fp8_reduce_kernel(Fp8Args p, const float*
   const int64_t span = p.M * p.N;
   const float* q = part + c * 8;
   float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int s = 0; s < p.splits; ++s, q += span) {
     const v4f x = *reinterpret_cast<const v4f*>(q), y = *reinterpret_cast<const v4f*>(q + 4);
 #pragma unroll
@@ -290,22 +282,36 @@ __global__ __launch_bounds__(256) void fp8_reduce_kernel(Fp8Args p, const float*
   store_columns<OUT, 8>(p, f, c / nc * p.N, (int)(c % nc) * 8, p.bias != nullptr);
 }
 
-// What the dense product runs as: rows streamed, or a tile and its K splits.
+// What the dense product runs as: rows streamed (tile 0), or a tile and its
+// K splits.
 struct DensePlan {
-  int tile;                                          // 0: streamed; else the tile's side in rows (64, 128, 256)
-  int splits;
+  int tile, splits;
 };
 
+// The smaller tiles run one step in about 0.9 us while at most two of their
+// blocks share a CU (the next step's tiles arrive from memory), so K is split
+// while the steps saved outweigh the partial sums' way to memory and back
+// (4.5 TB/s) and the second kernel (2 us, 0.1 us per split). 200 x 4096 x
+// 14336: 8 splits 29 us, 4 36; 256 x 4096 x 4096: 4 splits 18 us, 8 24; 1024 x
+// 4096 x 4096: none 27 us, 2 34. The 256 x 256 tile takes over where it fills
+// most CUs (1024 x 14336 x 4096: 62 us; 128 x 128 2 us slower), and streaming
+// up to 16 rows (12 x 4096 x 4096: 7 us; 64 x 128 tiles 11).
 static DensePlan plan_dense(int64_t M, int64_t N, int64_t K) {
-  if (M <= 64) return {0, 1};
+  if (M <= 16) return {0, 1};
   const int64_t KB = (K + 127) / 128;
-  auto tiles = [&](int64_t b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
-  if (tiles(256) >= 192) return {256, 1};
-  const int64_t t = tiles(128);
-  int64_t splits = 512 / t;
-  if (splits > KB / 4) splits = KB / 4;
-  if (splits < 1) splits = 1;
-  return {128, (int)splits};
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  if (tiles(256, 256) >= 192) return {256, 1};
+  const int tile = M <= 64 ? 64 : 128;
+  const int64_t t = tiles(tile, 128);
+  int64_t best = 1, cost = 4000 + 900 * KB;   // ns
+  for (int64_t s = 2; s * t <= 512 && 2 * s <= KB; ++s) {
+    const int64_t c = 6000 + 900 * ((KB + s - 1) / s) + 100 * s + s * M * N * 8 / 4500;
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return {tile, (int)best};
 }
 
 size_t fp8_block_gemm_workspace(int64_t M, int64_t N, int64_t K) {
@@ -361,13 +367,15 @@ hipError_t launch_fp8_block_gemm(const void* a, const float* a_scale, const void
   p.NBLK = (int)((N + 127) / 128);
   const DensePlan pl = plan_dense(M, N, K);
   p.splits = pl.splits;
-  if (pl.tile == 0) return launch_fp8_stream(p, out_dt, M, stream);
+  if (pl.tile == 0) return launch_fp8_stream(p, out_dt, stream);
   Fp8Args part = p;
   if (p.splits > 1) part.out = ws;
   const int dt = p.splits > 1 ? 2 : out_dt;
   // (converting to fp16 in the 256 x 256 tile spills registers)
-  const hipError_t e = pl.tile == 256 && out_dt != 2 ? tile_go<8, 4, 2, 4>(part, false, dt, stream)
-                                      : tile_go<4, 4, 2, 2>(part, out_dt == 2, dt, stream);
+  hipError_t e;
+  if (pl.tile == 64) e = tile_go<2, 4, 2, 2>(part, out_dt == 2, dt, stream);
+  else if (pl.tile == 128 || out_dt == 2) e = tile_go<4, 4, 2, 2>(part, out_dt == 2, dt, stream);
+  else e = tile_go<8, 4, 2, 4>(part, false, dt, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   const dim3 grid((unsigned)((M * (N / 8) + 255) / 256)), block(256);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p, static_cast<const float*>(ws)); };
@@ -397,9 +405,8 @@ hipError_t launch_fp8_block_grouped(const void* a, const float* a_scale, const i
   p.KB = (int)((K + 127) / 128);
   p.NBLK = (int)((N + 127) / 128);
   p.splits = 1;
-  const int64_t avg = (R + E - 1) / E;
-  if (avg <= 24) return launch_fp8_stream(p, out_dt, avg, stream);
-  if (avg <= 128) return tile_go<4, 4, 2, 2>(p, false, out_dt, stream);
+  if (R <= 4 * E) return launch_fp8_stream(p, out_dt, stream);
+  if (R <= 96 * E) return tile_go<4, 4, 2, 2>(p, false, out_dt, stream);
   return tile_go<8, 4, 2, 4>(p, false, out_dt, stream);
 }
 

@@ -134,11 +134,9 @@ static hipError_t stream_go(Fp8Args p, int out_dt, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// rows: the product's, or an expert's on average
-hipError_t launch_fp8_stream(const Fp8Args& p, int out_dt, int64_t rows, hipStream_t stream) {
-  if (rows <= (p.offsets ? 4 : 16)) return stream_go<1, 2, 4, 2>(p, out_dt, stream);
-  if (rows <= 32 && !p.offsets) return stream_go<2, 4, 4, 1>(p, out_dt, stream);
-  return stream_go<4, 4, 4, 1>(p, out_dt, stream);
+hipError_t launch_fp8_stream(const Fp8Args& p, int out_dt, hipStream_t stream) {
+  if (!p.offsets && p.N < 32 * 256) return stream_go<1, 1, 16, 2>(p, out_dt, stream);
+  return stream_go<1, 2, 4, 2>(p, out_dt, stream);
 }
 
 }  // namespace w4

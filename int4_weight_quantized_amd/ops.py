@@ -103,8 +103,9 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream=None) -> int | None:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream or None
+    if stream is None:      # the handle alone: building a Stream object costs a microsecond
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
+    return stream.cuda_stream or None
 
 
 def _half_code(dt) -> int:
@@ -436,15 +437,18 @@ def _float_code(dt) -> int:
     return _FLOAT_CODES[dt]
 
 
-def _typed(t, dtype, shape, what: str):
-    """t with its type and shape checked (None passes)."""
+def _arg(t, dtype, shape: tuple, what: str) -> int | None:
+    """Pointer of a contiguous GPU tensor, its type and shape checked (None passes). One pass over the common case:
+    these checks are most of a small call's host time."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    return _ptr(t)
 
 
 def _e4m3_codes(t, what: str):
@@ -486,18 +490,18 @@ def w4_route(logits, topk: int, score: str = "softmax", bias=None, n_groups: int
                torch.empty((E + 1,), dtype=torch.int32, device=dev),
                torch.empty((T, topk), dtype=torch.int32, device=dev))
     ids, weights, row_token, offsets, row_of = out
-    _typed(bias, torch.float32, (E,), "bias")
-    _typed(ids, torch.int32, (T, topk), "ids")
-    _typed(weights, torch.float32, (T, topk), "weights")
-    _typed(row_token, torch.int32, (T * topk,), "row_token")
-    _typed(offsets, torch.int32, (E + 1,), "expert_offsets")
-    _typed(row_of, torch.int32, (T, topk), "row_of")
+    p_bias = _arg(bias, torch.float32, (E,), "bias")
+    p_ids = _arg(ids, torch.int32, (T, topk), "ids")
+    p_weights = _arg(weights, torch.float32, (T, topk), "weights")
+    p_token = _arg(row_token, torch.int32, (T * topk,), "row_token")
+    p_off = _arg(offsets, torch.int32, (E + 1,), "expert_offsets")
+    p_row = _arg(row_of, torch.int32, (T, topk), "row_of")
     if workspace is None:
         workspace = w4_route_workspace(T, E, topk, device=dev)
     _check("w4_route", lib().w4_route(
-        ptr, _float_code(logits.dtype), T, E, ld, W4_SCORES[score], _ptr(bias), n_groups, topk_groups, group_top,
-        topk, int(renorm), scale, _ptr(ids), _ptr(weights), _ptr(row_token), _ptr(offsets), _ptr(row_of),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        ptr, _float_code(logits.dtype), T, E, ld, W4_SCORES[score], p_bias, n_groups, topk_groups, group_top, topk,
+        int(renorm), scale, p_ids, p_weights, p_token, p_off, p_row, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
 
 
@@ -516,10 +520,10 @@ def w4_fp8_block_quantize(x, act: str = "none", out=None, stream=None):
         out = (torch.empty((M, K), dtype=torch.uint8, device=x.device),
                torch.empty((M, KB), dtype=torch.float32, device=x.device))
     codes, scales = out
-    _typed(_e4m3_codes(codes, "codes"), codes.dtype, (M, K), "codes")
-    _typed(scales, torch.float32, (M, KB), "scales")
+    p_codes = _arg(_e4m3_codes(codes, "codes"), codes.dtype, (M, K), "codes")
     _check("w4_fp8_block_quantize", lib().w4_fp8_block_quantize(
-        ptr, _half_code(x.dtype), M, K, ldx, W4_ACTS[act], _ptr(codes), _ptr(scales), _stream(stream)))
+        ptr, _half_code(x.dtype), M, K, ldx, W4_ACTS[act], p_codes, _arg(scales, torch.float32, (M, KB), "scales"),
+        _stream(stream)))
     return out
 
 
@@ -540,15 +544,15 @@ def w4_fp8_block_gemm(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=tor
     KB, NB = (K + 127) // 128, (N + 127) // 128
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=a.device)
-    _typed(a_scale, torch.float32, (M, KB), "a_scale")
-    _typed(w_scale, torch.float32, (NB, KB), "w_scale")
-    _typed(bias, out.dtype, (N,), "bias")
-    _typed(out, out.dtype, (M, N), "out")
+    p_as = _arg(a_scale, torch.float32, (M, KB), "a_scale")
+    p_ws = _arg(w_scale, torch.float32, (NB, KB), "w_scale")
+    p_bias = _arg(bias, out.dtype, (N,), "bias")
+    p_out = _arg(out, out.dtype, (M, N), "out")
     if workspace is None:
         workspace = w4_fp8_block_gemm_workspace(M, N, K, device=a.device)
     _check("w4_fp8_block_gemm", lib().w4_fp8_block_gemm(
-        _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(out), _float_code(out.dtype), M, N, K,
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _ptr(a), p_as, _ptr(w), p_ws, p_bias, p_out, _float_code(out.dtype), M, N, K, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
 
 
@@ -564,14 +568,13 @@ def w4_fp8_block_grouped_gemm(a, a_scale, row_token, expert_offsets, w, w_scale,
     R = T if row_token is None else row_token.shape[0]
     if out is None:
         out = torch.empty((R, N), dtype=out_dtype, device=a.device)
-    _typed(a_scale, torch.float32, (T, KB), "a_scale")
-    _typed(row_token, torch.int32, (R,), "row_token")
-    _typed(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
-    _typed(w_scale, torch.float32, (E, NB, KB), "w_scale")
-    _typed(out, out.dtype, (R, N), "out")
+    p_as = _arg(a_scale, torch.float32, (T, KB), "a_scale")
+    p_token = _arg(row_token, torch.int32, (R,), "row_token")
+    p_off = _arg(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    p_ws = _arg(w_scale, torch.float32, (E, NB, KB), "w_scale")
+    p_out = _arg(out, out.dtype, (R, N), "out")
     _check("w4_fp8_block_grouped_gemm", lib().w4_fp8_block_grouped_gemm(
-        _ptr(a), _ptr(a_scale), _ptr(row_token), _ptr(expert_offsets), E, _ptr(w), _ptr(w_scale), _ptr(out),
-        _half_code(out.dtype), T, R, N, K, _stream(stream)))
+        _ptr(a), p_as, p_token, p_off, E, _ptr(w), p_ws, p_out, _half_code(out.dtype), T, R, N, K, _stream(stream)))
     return out
 
 
@@ -582,11 +585,8 @@ def w4_combine(y, row_of, weights, add=None, out=None, stream=None):
     T, topk = row_of.shape
     if out is None:
         out = torch.empty((T, N), dtype=y.dtype, device=y.device)
-    _typed(row_of, torch.int32, (T, topk), "row_of")
-    _typed(weights, torch.float32, (T, topk), "weights")
-    _typed(add, y.dtype, (T, N), "add")
-    _typed(out, y.dtype, (T, N), "out")
     _check("w4_combine", lib().w4_combine(
-        _ptr(y), _float_code(y.dtype), _ptr(row_of), _ptr(weights), _ptr(add), _ptr(out), T, R, topk, N,
-        _stream(stream)))
+        _ptr(y), _float_code(y.dtype), _arg(row_of, torch.int32, (T, topk), "row_of"),
+        _arg(weights, torch.float32, (T, topk), "weights"), _arg(add, y.dtype, (T, N), "add"),
+        _arg(out, y.dtype, (T, N), "out"), T, R, topk, N, _stream(stream)))
     return out
