@@ -12,12 +12,19 @@
 //   offsets[e] .. offsets[e+1] are expert e's rows, row_token names each
 //   row's token (-1 past the last), row_of is the inverse (-1 for none).
 //
-// One wave routes one token, expert j * 64 + lane in register j. A block
-// takes kTok = 64 tokens, so that a token is one bit of a 64-bit mask per
-// expert: the rank of (token, expert) inside the block is the number of lower
-// bits set, which needs no sort and no order of atomics. One block does the
-// whole plan up to 64 tokens; above, a second kernel scans the blocks' counts
-// per expert and a third places the rows.
+// Up to 256 experts, 16 lanes route one token (a wave four), each holding V
+// consecutive experts: the argmax rounds exchange within a row of 16 lanes,
+// by DPP, and all 64 tokens of a block go through at once. More experts, and
+// groups that do not fall on whole lanes, take one wave per token, expert
+// j * 64 + lane in register j. What bounds it is the latency of topk dependent
+// argmax rounds and, with fp64 scores, the vector units.
+// A block takes kTok = 64 tokens, so that a token is one bit of a 64-bit mask
+// per expert: the rank of (token, expert) inside the block is the number of
+// lower bits set, which needs no sort and no order of atomics. One block does
+// the whole plan up to 64 tokens; above, it leaves its counts per expert (a
+// byte each) and a second kernel places the rows: each of its blocks adds up
+// all blocks' counts, which are few and lie in the L2. Past kSumBlocks blocks
+// that square of reads is too long and a kernel between them scans the counts.
 #include "w4_device.h"
 
 namespace w4 {
@@ -35,20 +42,78 @@ struct RouteArgs {
   double scale;
   int32_t *ids, *row_token, *offsets, *row_of;
   float* weights;
-  int32_t* counts;                       // [blocks][E], then totals [E]; null: one block
+  uint8_t* counts;                       // [blocks][ceil(E / 4) * 4]; null: one block
+  int32_t* prefix;                       // past kSumBlocks blocks: counts before each block [blocks][E], totals [E]
+  int vec;                               // rows of logits are aligned for whole-lane loads
 };
+
+// All lanes' best of L consecutive lanes (16: DPP inside a row of 16; 64: two
+// exchanges more), op(own, other).
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) { return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false); }
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const long long b = __double_as_longlong(v);
+  const uint32_t lo = (uint32_t)dpp<CTRL>((int)b), hi = (uint32_t)dpp<CTRL>((int)(b >> 32));
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) { return __int_as_float(dpp<CTRL>(__float_as_int(v))); }
+
+template <int L, typename T, typename F>
+__device__ __forceinline__ T lanes_reduce(T v, F op) {
+  v = op(v, dpp<0xB1>(v));               // lane ^ 1
+  v = op(v, dpp<0x4E>(v));               // lane ^ 2
+  v = op(v, dpp<0x141>(v));              // mirror of 8 lanes: the other four
+  v = op(v, dpp<0x140>(v));              // mirror of 16: the other eight
+  if constexpr (L == 64) {
+    v = op(v, __shfl_xor(v, 16, kWave));
+    v = op(v, __shfl_xor(v, 32, kWave));
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ double lanes_sum(double v) {
+  return lanes_reduce<L>(v, [](double a, double b) { return a + b; });
+}
+
+// The best (largest key, then lowest id) of L lanes.
+template <typename K, int CTRL>
+__device__ __forceinline__ void best_step(K& key, int& id) {
+  const K o = dpp<CTRL>(key);
+  const int oi = dpp<CTRL>(id);
+  if (o > key || (o == key && oi < id)) {
+    key = o;
+    id = oi;
+  }
+}
+template <int L, typename K>
+__device__ __forceinline__ void lanes_best(K& key, int& id) {
+  best_step<K, 0xB1>(key, id);
+  best_step<K, 0x4E>(key, id);
+  best_step<K, 0x141>(key, id);
+  best_step<K, 0x140>(key, id);
+  if constexpr (L == 64) {
+#pragma unroll
+    for (int off = 16; off <= 32; off <<= 1) {
+      const K o = __shfl_xor(key, off, kWave);
+      const int oi = __shfl_xor(id, off, kWave);
+      if (o > key || (o == key && oi < id)) {
+        key = o;
+        id = oi;
+      }
+    }
+  }
+}
+
+constexpr float kF32Max = 3.40282347e38f;
+constexpr int kSumBlocks = 512;
 
 template <int DT>
 __device__ __forceinline__ float load_logit(const void* x, int64_t i) {
   if constexpr (DT == 2) return static_cast<const float*>(x)[i];
   const uint16_t v = static_cast<const uint16_t*>(x)[i];
   return DT == 0 ? bf16_to_f32(v) : f16_to_f32(v);
-}
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-  return v;
 }
 
 // Inclusive sum over the wave.
@@ -103,6 +168,180 @@ __device__ __forceinline__ void place_rows(const RouteArgs& a, int64_t t0, int t
   }
 }
 
+// The end of a routing block: its counts, or (one block) the plan itself.
+__device__ __forceinline__ void finish_block(const RouteArgs& a, int64_t t0, int tokens, const int32_t* s_ids,
+                                             const unsigned long long* mask, int* base, int* red) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  const int cnt = tid < a.E ? __popcll(mask[tid]) : 0;
+  if (a.counts) {
+    const int ep = (a.E + 3) & ~3;
+    if (tid < ep) a.counts[(int64_t)blockIdx.x * ep + tid] = (uint8_t)cnt;
+    return;
+  }
+  int total;
+  const int start = block_scan(cnt, red, total);
+  if (tid < a.E) {
+    base[tid] = start;
+    a.offsets[tid] = start;
+  }
+  if (tid == 0) a.offsets[a.E] = total;
+  __syncthreads();
+  place_rows(a, t0, tokens, s_ids, mask, base, total);
+}
+
+// 16 lanes per token, V consecutive experts per lane (E <= 16 V). K: the key,
+// float (the logit) or double (a bias or groups). Groups cover GL = per_group
+// / V whole lanes, a power of two.
+template <int DT, int V, typename K>
+__global__ __launch_bounds__(kRThreads) void route_rows_kernel(RouteArgs a) {
+  constexpr bool GENERAL = sizeof(K) == 8;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem);
+  int32_t* s_ids = reinterpret_cast<int32_t*>(mask + a.E);
+  int* base = s_ids + kTok * a.topk;
+  int* red = base + a.E;
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, tl = tid >> 4;
+  for (int e = tid; e < a.E; e += kRThreads) mask[e] = 0;
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * kTok, t = t0 + tl;
+  const int tokens = (int)min((int64_t)kTok, a.T - t0);
+  const bool real = tl < tokens;
+  const int e0 = l16 * V;
+  constexpr float kClosed = -__builtin_inff();
+  const K kLow = -(K)__builtin_inff();
+
+  float x[V];
+  if (a.vec && real && e0 + V <= a.E) {
+    if constexpr (DT == 2) {
+      const float* q = static_cast<const float*>(a.x) + t * a.ld + e0;
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const v4f v = *reinterpret_cast<const v4f*>(q + j);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[j + c] = v[c];
+      }
+    } else {
+      const uint16_t* q = static_cast<const uint16_t*>(a.x) + t * a.ld + e0;
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const v2i v = *reinterpret_cast<const v2i*>(q + j);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint16_t h = (uint16_t)((uint32_t)v[c / 2] >> (16 * (c % 2)));
+          x[j + c] = DT == 0 ? bf16_to_f32(h) : f16_to_f32(h);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = real && e0 + j < a.E ? load_logit<DT>(a.x, t * a.ld + e0 + j) : kClosed;
+  }
+  float top = kClosed;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    x[j] = x[j] > kClosed ? fminf(x[j], kF32Max) : kClosed;   // NaN: closed
+    top = fmaxf(top, x[j]);
+  }
+  if (a.score == 0) top = lanes_reduce<16>(top, [](float p, float q) { return fmaxf(p, q); });
+  if (!(top > kClosed)) top = 0.f;                   // every expert closed: no score is used
+  K key[V];
+  double sum = 1.0;
+  if (GENERAL || (a.score == 0 && !a.renorm)) {
+    double part = 0.0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const double p = x[j] > kClosed ? score_of(x[j], a.score, top) : 0.0;
+      if constexpr (GENERAL) key[j] = p;
+      part += p;
+    }
+    if (a.score == 0) sum = fmax(lanes_sum<16>(part), 1e-300);
+  }
+  if constexpr (GENERAL) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const double c = (a.score == 0 ? key[j] / sum : key[j]) +
+                       (double)(a.bias && e0 + j < a.E ? a.bias[e0 + j] : 0.f);
+      key[j] = (x[j] > kClosed && c > kLow) ? c : kLow;   // a NaN or -inf bias closes its expert
+    }
+    if (a.G > 1) {
+      const int GL = a.per_group / V;                // lanes per group
+      double b0 = kLow, b1 = kLow;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        b1 = fmax(b1, fmin(b0, key[j]));
+        b0 = fmax(b0, key[j]);
+      }
+      for (int off = 1; off < GL; off <<= 1) {
+        const double o0 = __shfl_xor(b0, off, kWave), o1 = __shfl_xor(b1, off, kWave);
+        b1 = fmax(fmax(b1, o1), fmin(b0, o0));
+        b0 = fmax(b0, o0);
+      }
+      const double value = (a.group_top == 2 && b1 > kLow) ? b0 + b1 : b0;
+      const int g = l16 / GL;
+      int before = 0;                                // groups that rank before this lane's
+      for (int h = 0; h < a.G; ++h) {
+        const double o = __shfl(value, (lane & 48) + h * GL, kWave);
+        before += (o > value || (o == value && h < g)) ? 1 : 0;
+      }
+      if (before >= a.topk_groups) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = kLow;
+      }
+    }
+    if (!a.bias) {                                   // the key is the logit itself
+#pragma unroll
+      for (int j = 0; j < V; ++j) key[j] = key[j] > kLow ? (double)x[j] : kLow;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = x[j];
+  }
+
+  // topk rounds of argmax; lane i of the token's 16 keeps choices i, 16 + i, ..
+  int mine[4] = {-1, -1, -1, -1};
+  double part = 0.0;
+  double w[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    for (int i = 16 * q; i < min(a.topk, 16 * q + 16); ++i) {
+      K best = key[0];
+      int id = e0;
+#pragma unroll
+      for (int j = 1; j < V; ++j)
+        if (key[j] > best) {
+          best = key[j];
+          id = e0 + j;
+        }
+      lanes_best<16>(best, id);
+      if (best > kLow) {                             // the same in all 16 lanes
+        if (l16 == i - 16 * q) mine[q] = id;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (id == e0 + j) key[j] = kLow;
+      }
+    }
+    if (mine[q] >= 0) {
+      w[q] = score_of(fminf(load_logit<DT>(a.x, t * a.ld + mine[q]), kF32Max), a.score, top) / sum;
+      atomicOr(&mask[mine[q]], 1ull << tl);
+    }
+    part += w[q];
+    if (16 * q + 16 >= a.topk) break;
+  }
+  const double norm = a.renorm ? fmax(lanes_sum<16>(part), 1e-300) : 1.0;
+  if (real) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = 16 * q + l16;
+      if (i >= a.topk) break;
+      a.ids[t * a.topk + i] = mine[q];
+      a.weights[t * a.topk + i] = (float)(w[q] / norm * a.scale);
+      s_ids[tl * a.topk + i] = mine[q];
+    }
+  }
+  finish_block(a, t0, tokens, s_ids, mask, base, red);
+}
+
 // V: experts per lane (E <= 64 V).  GENERAL: keys in fp64 (a bias or groups).
 template <int DT, int V, bool GENERAL>
 __global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
@@ -136,7 +375,7 @@ __global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
     for (int j = 0; j < V; ++j) {
       const int e = j * 64 + lane;
       const float v = e < a.E ? load_logit<DT>(a.x, t * a.ld + e) : -__builtin_inff();
-      x[j] = v > -__builtin_inff() ? fminf(v, 3.40282347e38f) : -__builtin_inff();   // NaN: closed
+      x[j] = v > -__builtin_inff() ? fminf(v, kF32Max) : -__builtin_inff();   // NaN: closed
       top = fmaxf(top, x[j]);
     }
     top = wave_max(top);
@@ -151,7 +390,7 @@ __global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
         key[j] = p;
         part += p;
       }
-      if (a.score == 0) sum = fmax(wave_sum(part), 1e-300);
+      if (a.score == 0) sum = fmax(lanes_sum<64>(part), 1e-300);
     }
     if constexpr (GENERAL) {
 #pragma unroll
@@ -213,15 +452,7 @@ __global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
           best = key[j];
           id = j * 64 + lane;
         }
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) {
-        const double o = __shfl_xor(best, off, kWave);
-        const int oi = __shfl_xor(id, off, kWave);
-        if (o > best || (o == best && oi < id)) {
-          best = o;
-          id = oi;
-        }
-      }
+      lanes_best<64>(best, id);
       if (!(best > kLow)) break;                         // nothing left (uniform)
       if (lane == i) my_id = id;
 #pragma unroll
@@ -230,37 +461,25 @@ __global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
     }
     double w = 0.0;
     if (my_id >= 0) {
-      const float xi = fminf(load_logit<DT>(a.x, t * a.ld + my_id), 3.40282347e38f);
+      const float xi = fminf(load_logit<DT>(a.x, t * a.ld + my_id), kF32Max);
       w = score_of(xi, a.score, top) / sum;
       atomicOr(&mask[my_id], 1ull << tl);
     }
-    if (a.renorm) w = w / fmax(wave_sum(w), 1e-300);
+    if (a.renorm) w = w / fmax(lanes_sum<64>(w), 1e-300);
     if (lane < a.topk) {
       a.ids[t * a.topk + lane] = my_id;
       a.weights[t * a.topk + lane] = (float)(w * a.scale);
       s_ids[tl * a.topk + lane] = my_id;
     }
   }
-  __syncthreads();
-  const int cnt = tid < a.E ? __popcll(mask[tid]) : 0;
-  if (a.counts) {
-    if (tid < a.E) a.counts[(int64_t)blockIdx.x * a.E + tid] = cnt;
-    return;
-  }
-  int total;
-  const int start = block_scan(cnt, red, total);
-  if (tid < a.E) {
-    base[tid] = start;
-    a.offsets[tid] = start;
-  }
-  if (tid == 0) a.offsets[a.E] = total;
-  __syncthreads();
-  place_rows(a, t0, tokens, s_ids, mask, base, total);
+  finish_block(a, t0, tokens, s_ids, mask, base, red);
 }
 
-// Per expert, the exclusive sums of the blocks' counts (in place) and the
-// total: 64 experts per block (lane), the blocks' range cut over the waves.
-__global__ __launch_bounds__(kRThreads) void route_scan_kernel(int32_t* __restrict__ counts, int E, int blocks) {
+// Per expert, the exclusive sums of the blocks' counts and the total: 64
+// experts per block (lane), the blocks' range cut over the waves.
+__global__ __launch_bounds__(kRThreads) void route_scan_kernel(const uint8_t* __restrict__ counts,
+                                                               int32_t* __restrict__ prefix, int E, int blocks) {
+  const int ep = (E + 3) & ~3;
   __shared__ int part[kRWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e = blockIdx.x * 64 + lane;
@@ -268,7 +487,7 @@ __global__ __launch_bounds__(kRThreads) void route_scan_kernel(int32_t* __restri
   const int b0 = min(wave * per, blocks), b1 = min(b0 + per, blocks);
   int s = 0;
   if (e < E)
-    for (int b = b0; b < b1; ++b) s += counts[(int64_t)b * E + e];
+    for (int b = b0; b < b1; ++b) s += counts[(int64_t)b * ep + e];
   part[wave][lane] = s;
   __syncthreads();
   int run = 0, total = 0;
@@ -280,11 +499,11 @@ __global__ __launch_bounds__(kRThreads) void route_scan_kernel(int32_t* __restri
   }
   if (e >= E) return;
   for (int b = b0; b < b1; ++b) {
-    const int v = counts[(int64_t)b * E + e];
-    counts[(int64_t)b * E + e] = run;
+    const int v = counts[(int64_t)b * ep + e];
+    prefix[(int64_t)b * E + e] = run;
     run += v;
   }
-  if (wave == 0) counts[(int64_t)blocks * E + e] = total;
+  if (wave == 0) prefix[(int64_t)blocks * E + e] = total;
 }
 
 __global__ __launch_bounds__(kRThreads) void route_place_kernel(RouteArgs a, int blocks) {
@@ -297,10 +516,47 @@ __global__ __launch_bounds__(kRThreads) void route_place_kernel(RouteArgs a, int
   const int64_t t0 = (int64_t)blockIdx.x * kTok;
   const int tokens = (int)min((int64_t)kTok, a.T - t0);
   if (tid < a.E) mask[tid] = 0;
+  int sum = 0, mine = 0;                             // rows of expert tid, in all and in the blocks before
+  if (a.prefix) {
+    if (tid < a.E) {
+      sum = a.prefix[(int64_t)blocks * a.E + tid];
+      mine = a.prefix[(int64_t)blockIdx.x * a.E + tid];
+    }
+  } else {
+    // thread (row group, 4 experts): two sums of the counts' bytes, joined in LDS
+    int* s_sum = red + kRWaves;
+    int* s_mine = s_sum + ((a.E + 3) & ~3);
+    const int words = (a.E + 3) >> 2, groups = kRThreads / words, q = tid % words, rg = tid / words;
+    for (int e = tid; e < 2 * 4 * words; e += kRThreads) s_sum[e] = 0;
+    __syncthreads();
+    if (rg < groups) {
+      int all[4] = {0, 0, 0, 0}, low[4] = {0, 0, 0, 0};
+#pragma unroll 4
+      for (int b = rg; b < blocks; b += groups) {
+        const uint32_t v = reinterpret_cast<const uint32_t*>(a.counts)[(int64_t)b * words + q];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int n = (int)((v >> (8 * c)) & 0xFFu);
+          all[c] += n;
+          low[c] += b < (int)blockIdx.x ? n : 0;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        atomicAdd(&s_sum[4 * q + c], all[c]);
+        atomicAdd(&s_mine[4 * q + c], low[c]);
+      }
+    }
+    __syncthreads();
+    if (tid < a.E) {
+      sum = s_sum[tid];
+      mine = s_mine[tid];
+    }
+  }
   int total;
-  const int start = block_scan(tid < a.E ? a.counts[(int64_t)blocks * a.E + tid] : 0, red, total);
+  const int start = block_scan(sum, red, total);
   if (tid < a.E) {
-    base[tid] = start + a.counts[(int64_t)blockIdx.x * a.E + tid];
+    base[tid] = start + mine;
     if (blockIdx.x == 0) a.offsets[tid] = start;
   }
   if (blockIdx.x == 0 && tid == 0) a.offsets[a.E] = total;
@@ -315,9 +571,12 @@ __global__ __launch_bounds__(kRThreads) void route_place_kernel(RouteArgs a, int
 
 int64_t route_blocks(int64_t T) { return (T + kTok - 1) / kTok; }
 
+static size_t counts_bytes(int64_t nb, int64_t E) { return ((size_t)nb * (size_t)((E + 3) & ~3) + 15) & ~(size_t)15; }
+
 size_t route_workspace(int64_t T, int64_t E) {
   const int64_t nb = route_blocks(T);
-  return nb <= 1 ? 0 : (size_t)(nb + 1) * (size_t)E * 4;
+  if (nb <= 1) return 0;
+  return counts_bytes(nb, E) + (nb > kSumBlocks ? (size_t)(nb + 1) * (size_t)E * 4 : 0);
 }
 
 hipError_t launch_route(const void* x, int dt, int64_t T, int64_t E, int64_t ld, int score, const float* bias,
@@ -331,35 +590,50 @@ hipError_t launch_route(const void* x, int dt, int64_t T, int64_t E, int64_t ld,
   a.topk_groups = (int)topk_groups; a.group_top = (int)group_top; a.score = score; a.renorm = renorm ? 1 : 0;
   a.scale = scale;
   a.ids = ids; a.row_token = row_token; a.offsets = offsets; a.row_of = row_of; a.weights = weights;
-  a.counts = nb <= 1 ? nullptr : static_cast<int32_t*>(ws);
+  a.counts = nb <= 1 ? nullptr : static_cast<uint8_t*>(ws);
+  a.prefix = nb <= kSumBlocks ? nullptr : reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + counts_bytes(nb, E));
+  const int64_t unit = dt == 2 ? 4 : 8;              // elements per 16 bytes
+  a.vec = ld % unit == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
   const bool general = bias || G > 1;
-  size_t lds = (size_t)((8 * E + 4 * kTok * topk + 4 * E + 4 * kRWaves + 15) & ~15);
-  const size_t place_lds = lds;
-  if (G > 1) lds += (size_t)8 * E * kRWaves;
+  const size_t lds = (size_t)((8 * E + 4 * kTok * topk + 4 * E + 4 * kRWaves + 15) & ~15);
   const dim3 grid((unsigned)(nb > 0 ? nb : 1)), block(kRThreads);
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, stream, a); };
-  auto by_v = [&](auto dtc, auto gen) {
-    constexpr int D = decltype(dtc)::value;
-    constexpr bool Gn = decltype(gen)::value;
-    if (E <= 64) go(route_kernel<D, 1, Gn>);
-    else if (E <= 128) go(route_kernel<D, 2, Gn>);
-    else if (E <= 256) go(route_kernel<D, 4, Gn>);
-    else if (E <= 512) go(route_kernel<D, 8, Gn>);
-    else go(route_kernel<D, 16, Gn>);
+  const int V = E <= 64 ? 4 : (E <= 128 ? 8 : 16);   // experts per lane with 16 lanes
+  const int64_t lanes = a.per_group / V;             // lanes per group
+  const bool rows = E <= 256 && (G == 1 || (lanes > 0 && a.per_group % V == 0 && (lanes & (lanes - 1)) == 0));
+  auto by_dt = [&](auto f) {
+    if (dt == 0) f(std::integral_constant<int, 0>{});
+    else if (dt == 1) f(std::integral_constant<int, 1>{});
+    else f(std::integral_constant<int, 2>{});
   };
-  auto by_dt = [&](auto gen) {
-    if (dt == 0) by_v(std::integral_constant<int, 0>{}, gen);
-    else if (dt == 1) by_v(std::integral_constant<int, 1>{}, gen);
-    else by_v(std::integral_constant<int, 2>{}, gen);
-  };
-  if (general) by_dt(std::true_type{});
-  else by_dt(std::false_type{});
+  if (rows) {
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, stream, a); };
+    by_dt([&](auto d) {
+      constexpr int D = decltype(d)::value;
+      if (V == 4) general ? go(route_rows_kernel<D, 4, double>) : go(route_rows_kernel<D, 4, float>);
+      else if (V == 8) general ? go(route_rows_kernel<D, 8, double>) : go(route_rows_kernel<D, 8, float>);
+      else general ? go(route_rows_kernel<D, 16, double>) : go(route_rows_kernel<D, 16, float>);
+    });
+  } else {
+    const size_t need = lds + (G > 1 ? (size_t)8 * E * kRWaves : 0);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, need, stream, a); };
+    by_dt([&](auto d) {
+      constexpr int D = decltype(d)::value;
+      if (!general) E <= 512 ? go(route_kernel<D, 8, false>) : go(route_kernel<D, 16, false>);
+      else if (E <= 256) go(route_kernel<D, 4, true>);
+      else if (E <= 512) go(route_kernel<D, 8, true>);
+      else go(route_kernel<D, 16, true>);
+    });
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || nb <= 1) return e;
-  hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)((E + 63) / 64)), block, 0, stream, a.counts, (int)E, (int)nb);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(route_place_kernel, grid, block, place_lds, stream, a, (int)nb);
+  if (a.prefix) {
+    hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)((E + 63) / 64)), block, 0, stream, a.counts, a.prefix, (int)E,
+                       (int)nb);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const size_t place = lds + (size_t)8 * (size_t)((E + 3) & ~3);
+  hipLaunchKernelGGL(route_place_kernel, grid, block, place, stream, a, (int)nb);
   return hipGetLastError();
 }
 
