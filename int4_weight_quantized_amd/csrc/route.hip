@@ -16,8 +16,10 @@
 // consecutive experts: the argmax rounds exchange within a row of 16 lanes,
 // by DPP, and all 64 tokens of a block go through at once. More experts, and
 // groups that do not fall on whole lanes, take one wave per token, expert
-// j * 64 + lane in register j. What bounds it is the latency of topk dependent
-// argmax rounds and, with fp64 scores, the vector units.
+// j * 64 + lane in register j. 16384 tokens of 256 experts in 8 groups take 35
+// us: 256 blocks run through once, 9 us of it their latency, 10 the fp64
+// scores (own exponentials over several experts at a time spilled and gained
+// nothing), 8 the argmax rounds, 7 the plan. 8192 of 64 experts take 12.5.
 // A block takes kTok = 64 tokens, so that a token is one bit of a 64-bit mask
 // per expert: the rank of (token, expert) inside the block is the number of
 // lower bits set, which needs no sort and no order of atomics. One block does
@@ -77,31 +79,28 @@ __device__ __forceinline__ double lanes_sum(double v) {
   return lanes_reduce<L>(v, [](double a, double b) { return a + b; });
 }
 
-// The best (largest key, then lowest id) of L lanes.
-template <typename K, int CTRL>
-__device__ __forceinline__ void best_step(K& key, int& id) {
-  const K o = dpp<CTRL>(key);
+// The best (largest key, then lowest id) of the wave.
+template <int CTRL>
+__device__ __forceinline__ void best_step(double& key, int& id) {
+  const double o = dpp<CTRL>(key);
   const int oi = dpp<CTRL>(id);
   if (o > key || (o == key && oi < id)) {
     key = o;
     id = oi;
   }
 }
-template <int L, typename K>
-__device__ __forceinline__ void lanes_best(K& key, int& id) {
-  best_step<K, 0xB1>(key, id);
-  best_step<K, 0x4E>(key, id);
-  best_step<K, 0x141>(key, id);
-  best_step<K, 0x140>(key, id);
-  if constexpr (L == 64) {
+__device__ __forceinline__ void wave_best(double& key, int& id) {
+  best_step<0xB1>(key, id);
+  best_step<0x4E>(key, id);
+  best_step<0x141>(key, id);
+  best_step<0x140>(key, id);
 #pragma unroll
-    for (int off = 16; off <= 32; off <<= 1) {
-      const K o = __shfl_xor(key, off, kWave);
-      const int oi = __shfl_xor(id, off, kWave);
-      if (o > key || (o == key && oi < id)) {
-        key = o;
-        id = oi;
-      }
+  for (int off = 16; off <= 32; off <<= 1) {
+    const double o = __shfl_xor(key, off, kWave);
+    const int oi = __shfl_xor(id, off, kWave);
+    if (o > key || (o == key && oi < id)) {
+      key = o;
+      id = oi;
     }
   }
 }
@@ -189,6 +188,15 @@ __device__ __forceinline__ void finish_block(const RouteArgs& a, int64_t t0, int
   __syncthreads();
   place_rows(a, t0, tokens, s_ids, mask, base, total);
 }
+
+__device__ __forceinline__ float max_of(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double max_of(double a, double b) { return fmax(a, b); }
+// A chosen key: below every open one (their magnitude is an fp32's). Of a
+// double only the high word is written.
+__device__ __forceinline__ float shut(float) { return -__builtin_inff(); }
+__device__ __forceinline__ double shut(double v) { return __hiloint2double((int)0xFFEFFFFFu, __double2loint(v)); }
+template <typename K>
+__device__ __forceinline__ K shut_below() { return sizeof(K) == 8 ? (K)-1e300 : -(K)__builtin_inff(); }
 
 // 16 lanes per token, V consecutive experts per lane (E <= 16 V). K: the key,
 // float (the logit) or double (a bias or groups). Groups cover GL = per_group
@@ -306,19 +314,17 @@ __global__ __launch_bounds__(kRThreads) void route_rows_kernel(RouteArgs a) {
   for (int q = 0; q < 4; ++q) {
     for (int i = 16 * q; i < min(a.topk, 16 * q + 16); ++i) {
       K best = key[0];
-      int id = e0;
 #pragma unroll
-      for (int j = 1; j < V; ++j)
-        if (key[j] > best) {
-          best = key[j];
-          id = e0 + j;
-        }
-      lanes_best<16>(best, id);
-      if (best > kLow) {                             // the same in all 16 lanes
+      for (int j = 1; j < V; ++j) best = max_of(best, key[j]);
+      best = lanes_reduce<16>(best, [](K p, K q) { return max_of(p, q); });
+      int id = 0x7FFFFFFF;
+#pragma unroll
+      for (int j = V - 1; j >= 0; --j) id = key[j] == best ? e0 + j : id;
+      id = lanes_reduce<16>(id, [](int p, int q) { return min(p, q); });
+      if (best > shut_below<K>()) {                  // the same in all 16 lanes
         if (l16 == i - 16 * q) mine[q] = id;
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (id == e0 + j) key[j] = kLow;
+        for (int j = 0; j < V; ++j) key[j] = id == e0 + j ? shut(key[j]) : key[j];
       }
     }
     if (mine[q] >= 0) {
@@ -452,7 +458,7 @@ __global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
           best = key[j];
           id = j * 64 + lane;
         }
-      lanes_best<64>(best, id);
+      wave_best(best, id);
       if (!(best > kLow)) break;                         // nothing left (uniform)
       if (lane == i) my_id = id;
 #pragma unroll
