@@ -788,7 +788,7 @@ int w4_fp8_block_quantize(const void* x, int x_dtype, int64_t M, int64_t K, int6
     return fail(W4_ERR_DTYPE, "%s: activations must be bf16 or fp16 (dtype code %d)", fn, x_dtype);
   if (act != W4_ACT_NONE && act != W4_ACT_SWIGLU) return fail(W4_ERR_INVALID, "%s: unknown activation %d", fn, act);
   if (K % 8) return fail(W4_ERR_ALIGN, "%s: K=%lld is not a multiple of 8", fn, (long long)K);
-  if (M > kMaxDim || K > ((int64_t)1 << 24))
+  if (M > kMaxDim || K > ((int64_t)1 << 24) || M * ((K + 127) / 128) >= ((int64_t)1 << 31))
     return fail(W4_ERR_UNSUPPORTED, "%s: sizes too large (M=%lld K=%lld)", fn, (long long)M, (long long)K);
   const int64_t wide = act == W4_ACT_SWIGLU ? 2 * K : K;
   if (ldx < wide || ldx % 8)

