@@ -570,7 +570,8 @@ int w4_fp8_block_quantize(const void* x, int x_dtype, int64_t M, int64_t K, int6
  *   w        device, E4M3 [N, K];  w_scale: device, fp32 [ceil(N / 128), ceil(K / 128)]
  *   bias     device or NULL, [N] in the output type
  *   out      device, [M, N] in out_dtype: bf16, fp16 or fp32
- *   a, w and out must be 16-byte aligned; N a multiple of 8, K of 16.
+ *   a, w and out must be 16-byte aligned; N a multiple of 8, K of 16 and at
+ *   most 2^22.
  *   workspace device, w4_fp8_block_gemm_workspace_bytes (16-byte aligned;
  *            may be NULL when that is 0): fp32 partial tiles where few rows
  *            make the product split K, summed in a fixed order (results are
@@ -596,7 +597,8 @@ int w4_fp8_block_gemm(const void* a, const float* a_scale, const void* w, const 
  *   w        device, E4M3 [E, N, K];  w_scale: device, fp32
  *            [E, ceil(N / 128), ceil(K / 128)]
  *   out      device, [R, N] in out_dtype (bf16 or fp16)
- *   a, w and out must be 16-byte aligned; N a multiple of 8, K of 16.
+ *   a, w and out must be 16-byte aligned; N a multiple of 8, K of 16 and at
+ *   most 2^22.
  * Errors: INVALID, ALIGN, DTYPE, UNSUPPORTED (T*K >= 2^31 with row_token),
  *         HIP. Decreasing offsets are undefined behaviour.
  */

@@ -807,6 +807,8 @@ static int check_fp8_block(const char* fn, int64_t M, int64_t N, int64_t K) {
   int rc = check_mnk(fn, M, N, K);
   if (rc) return rc;
   if (K % 16) return fail(W4_ERR_ALIGN, "%s: K=%lld is not a multiple of 16", fn, (long long)K);
+  // a tile's 256 rows are addressed with 32-bit offsets
+  if (K > ((int64_t)1 << 22)) return fail(W4_ERR_UNSUPPORTED, "%s: K=%lld exceeds 2^22", fn, (long long)K);
   return W4_OK;
 }
 

@@ -185,6 +185,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args p) {
     gload(k0, 0);
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
     if (k0 + 1 < k1) gload(k0 + 1, STAGE);
+    if (GROUPED && r0 + 16 * MI * wm >= row_end) {   // a wave whose rows all lie past the segment only fetches
+      for (int tk = k0; tk < k1; ++tk) {
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        if (tk + 2 < k1) gload(tk + 2, ((tk - k0) & 1) * STAGE);
+      }
+      return;
+    }
     v8i bf[NJ], af[2];
     af[0] = frag(lds + a_ro, lds + a_rx);
 #pragma unroll
