@@ -445,3 +445,71 @@ def test_combine_far_rows():
     w = gpu(np.array([[1., 2.], [5., -1.]], dtype=np.float32))
     out = ops.w4_combine(y, row_of, w)
     assert (out[0] == 3).all() and (out[1] == -2).all()
+
+
+def layer_case(E, H, I, topk, T, seed, **kw):
+    from int4_weight_quantized_amd.fp8_experts import Fp8Experts
+    r = rng_for(E, H, I, T, seed)
+    w13, w2 = fp8_inputs(r, (E, 2 * I, H), 0), fp8_inputs(r, (E, H, I), 0)
+    s13 = r.uniform(1e-4, 3e-4, (E, -(-2 * I // 128), -(-H // 128))).astype(np.float32)
+    s2 = r.uniform(1e-4, 3e-4, (E, -(-H // 128), -(-I // 128))).astype(np.float32)
+    layer = Fp8Experts(gpu(w13), gpu(s13), gpu(w2), gpu(s2), topk, 4 * T, **kw)
+    x = gpu(r.standard_normal((T, H)), torch.bfloat16)
+    logits = gpu(r.standard_normal((T, E)), torch.float32)
+    logits[T // 2] = -float("inf")                               # a token without any expert
+    return layer, (w13, s13, w2, s2), x, logits
+
+
+@pytest.mark.parametrize("T", [1, 7, 90])
+def test_expert_layer(T):
+    """The layer stage by stage: each stage's 64-bit definition on what the stage before it gave."""
+    E, H, I, topk = 6, 400, 144, 3
+    layer, (w13, s13, w2, s2), x, logits = layer_case(E, H, I, topk, T, 1, score="sigmoid", scale=1.5)
+    res = gpu(rng_for(T).standard_normal((T, H)), torch.bfloat16)
+    out = layer(x, logits, add=res)
+    torch.cuda.synchronize()
+    ids, weights = O.route(logits.cpu().numpy(), topk, score="sigmoid", scale=1.5)
+    row_token, off, row_of = O.plan(ids, E)
+    assert np.array_equal(layer._ids[:T].cpu().numpy(), ids)
+    n, KB = int(off[-1]), -(-H // 128)
+    xq, xs = O.block_quantize(x.float().cpu().numpy())
+    y, mag = O.grouped_gemm(xq, xs, row_token, off, w13, s13)
+    check(layer._h[:n], y, product_tol(y, mag, "bf16", KB), "gate and up")
+    aq, asc = layer._a[:n].cpu().numpy(), layer._as[:n].cpu().numpy()
+    v = O.silu_gate(layer._h[:n].double().cpu().numpy())
+    for b in range(-(-I // 128)):
+        blk = v[:, b * 128:(b + 1) * 128]
+        s = np.abs(blk).max(1) / 448
+        assert (np.abs(asc[:, b] - s) <= 10 * U * s + 2.0 ** -149).all()
+    y, mag = O.grouped_gemm(aq, asc, None, off, w2, s2)
+    check(layer._y[:n], y, product_tol(y, mag, "bf16", -(-I // 128)), "down")
+    full = np.zeros((T * topk, H))
+    full[:n] = layer._y[:n].double().cpu().numpy()
+    want, mag = O.combine(full, row_of, weights.astype(np.float32), res.double().cpu().numpy())
+    # the weights carry half an fp32 step of their own
+    check(out, want, half_step(want, "bf16") * (1 + 1e-6) + (topk + 4) * U * mag, "combine")
+    assert torch.equal(out[T // 2], res[T // 2])
+
+
+def test_expert_layer_graph():
+    """Captured: replays on new inputs equal eager calls, with eager work between them."""
+    E, H, I, topk, T = 16, 512, 256, 4, 130
+    layer, _, x, logits = layer_case(E, H, I, topk, T, 2)
+    out = torch.empty_like(x)
+    layer(x, logits, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer(x, logits, out=out)
+    for i in range(4):
+        gen = torch.Generator(DEV).manual_seed(i)
+        x.copy_(torch.randn(x.shape, device=DEV, generator=gen))
+        logits.copy_(torch.randn(logits.shape, device=DEV, generator=gen))
+        want = layer(x, logits).clone()
+        torch.cuda.synchronize()
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    with pytest.raises(ValueError):
+        layer(x.repeat(5, 1), logits.repeat(5, 1))
