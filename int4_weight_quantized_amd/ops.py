@@ -437,18 +437,28 @@ def _float_code(dt) -> int:
     return _FLOAT_CODES[dt]
 
 
-def _arg(t, dtype, shape: tuple, what: str) -> int | None:
+def _arg(t, dtype, shape: tuple, what: str):
     """Pointer of a contiguous GPU tensor, its type and shape checked (None passes). One pass over the common case:
-    these checks are most of a small call's host time."""
+    these checks are most of a small call's host time. A tensor that is not on the GPU, or not contiguous, is returned
+    itself, for _call to refuse once every type and shape has been looked at."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _ptr(t)
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr() if t.is_cuda and t.is_contiguous() else t
+
+
+def _call(fn: str, *args) -> None:
+    try:
+        rc = getattr(lib(), fn)(*args)
+    except ctypes.ArgumentError:
+        for v in args:
+            if isinstance(v, torch.Tensor):
+                _ptr(v)                                  # names what is wrong with it
+        raise
+    _check(fn, rc)
 
 
 def _e4m3_codes(t, what: str):
@@ -498,10 +508,10 @@ def w4_route(logits, topk: int, score: str = "softmax", bias=None, n_groups: int
     p_row = _arg(row_of, torch.int32, (T, topk), "row_of")
     if workspace is None:
         workspace = w4_route_workspace(T, E, topk, device=dev)
-    _check("w4_route", lib().w4_route(
+    _call("w4_route",
         ptr, _float_code(logits.dtype), T, E, ld, W4_SCORES[score], p_bias, n_groups, topk_groups, group_top, topk,
         int(renorm), scale, p_ids, p_weights, p_token, p_off, p_row, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace.numel() * workspace.element_size(), _stream(stream))
     return out
 
 
@@ -521,9 +531,9 @@ def w4_fp8_block_quantize(x, act: str = "none", out=None, stream=None):
                torch.empty((M, KB), dtype=torch.float32, device=x.device))
     codes, scales = out
     p_codes = _arg(_e4m3_codes(codes, "codes"), codes.dtype, (M, K), "codes")
-    _check("w4_fp8_block_quantize", lib().w4_fp8_block_quantize(
+    _call("w4_fp8_block_quantize",
         ptr, _half_code(x.dtype), M, K, ldx, W4_ACTS[act], p_codes, _arg(scales, torch.float32, (M, KB), "scales"),
-        _stream(stream)))
+        _stream(stream))
     return out
 
 
@@ -550,9 +560,9 @@ def w4_fp8_block_gemm(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=tor
     p_out = _arg(out, out.dtype, (M, N), "out")
     if workspace is None:
         workspace = w4_fp8_block_gemm_workspace(M, N, K, device=a.device)
-    _check("w4_fp8_block_gemm", lib().w4_fp8_block_gemm(
+    _call("w4_fp8_block_gemm",
         _ptr(a), p_as, _ptr(w), p_ws, p_bias, p_out, _float_code(out.dtype), M, N, K, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace.numel() * workspace.element_size(), _stream(stream))
     return out
 
 
@@ -573,8 +583,8 @@ def w4_fp8_block_grouped_gemm(a, a_scale, row_token, expert_offsets, w, w_scale,
     p_off = _arg(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
     p_ws = _arg(w_scale, torch.float32, (E, NB, KB), "w_scale")
     p_out = _arg(out, out.dtype, (R, N), "out")
-    _check("w4_fp8_block_grouped_gemm", lib().w4_fp8_block_grouped_gemm(
-        _ptr(a), p_as, p_token, p_off, E, _ptr(w), p_ws, p_out, _half_code(out.dtype), T, R, N, K, _stream(stream)))
+    _call("w4_fp8_block_grouped_gemm",
+        _ptr(a), p_as, p_token, p_off, E, _ptr(w), p_ws, p_out, _half_code(out.dtype), T, R, N, K, _stream(stream))
     return out
 
 
@@ -585,8 +595,8 @@ def w4_combine(y, row_of, weights, add=None, out=None, stream=None):
     T, topk = row_of.shape
     if out is None:
         out = torch.empty((T, N), dtype=y.dtype, device=y.device)
-    _check("w4_combine", lib().w4_combine(
+    _call("w4_combine",
         _ptr(y), _float_code(y.dtype), _arg(row_of, torch.int32, (T, topk), "row_of"),
         _arg(weights, torch.float32, (T, topk), "weights"), _arg(add, y.dtype, (T, N), "add"),
-        _arg(out, y.dtype, (T, N), "out"), T, R, topk, N, _stream(stream)))
+        _arg(out, y.dtype, (T, N), "out"), T, R, topk, N, _stream(stream))
     return out
