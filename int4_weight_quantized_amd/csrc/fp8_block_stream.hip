@@ -134,6 +134,9 @@ static hipError_t stream_go(Fp8Args p, int out_dt, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// 32 columns a block; 16, with 16 waves along K, where the former would leave
+// CUs without a block (1 x 4096 x 14336: 11.4 us, 22.6 with 32 columns and 4
+// waves; 1 x 14336 x 4096: 11.8 us with the latter, 14.7 with the former).
 hipError_t launch_fp8_stream(const Fp8Args& p, int out_dt, hipStream_t stream) {
   if (!p.offsets && p.N < 32 * 256) return stream_go<1, 1, 16, 2>(p, out_dt, stream);
   return stream_go<1, 2, 4, 2>(p, out_dt, stream);

@@ -25,8 +25,10 @@
 // lower bits set, which needs no sort and no order of atomics. One block does
 // the whole plan up to 64 tokens; above, it leaves its counts per expert (a
 // byte each) and a second kernel places the rows: each of its blocks adds up
-// all blocks' counts, which are few and lie in the L2. Past kSumBlocks blocks
-// that square of reads is too long and a kernel between them scans the counts.
+// all blocks' counts, which are few and lie in the L2. Where that square of
+// reads passes 128 MiB a kernel between them scans the counts (64 experts: 16384
+// tokens 12 us summed, 18 scanned, 65536 36 and 52; 256 experts: 32768 tokens
+// 36 and 42, 65536 79 and 73, 131072 210 and 140).
 #include "w4_device.h"
 
 namespace w4 {
@@ -45,7 +47,7 @@ struct RouteArgs {
   int32_t *ids, *row_token, *offsets, *row_of;
   float* weights;
   uint8_t* counts;                       // [blocks][ceil(E / 4) * 4]; null: one block
-  int32_t* prefix;                       // past kSumBlocks blocks: counts before each block [blocks][E], totals [E]
+  int32_t* prefix;                       // where the counts are scanned: those before each block [blocks][E], totals [E]
   int vec;                               // rows of logits are aligned for whole-lane loads
 };
 
@@ -106,7 +108,6 @@ __device__ __forceinline__ void wave_best(double& key, int& id) {
 }
 
 constexpr float kF32Max = 3.40282347e38f;
-constexpr int kSumBlocks = 512;
 
 template <int DT>
 __device__ __forceinline__ float load_logit(const void* x, int64_t i) {
@@ -579,10 +580,12 @@ int64_t route_blocks(int64_t T) { return (T + kTok - 1) / kTok; }
 
 static size_t counts_bytes(int64_t nb, int64_t E) { return ((size_t)nb * (size_t)((E + 3) & ~3) + 15) & ~(size_t)15; }
 
+static bool scans(int64_t nb, int64_t E) { return nb * nb * E > ((int64_t)1 << 27); }
+
 size_t route_workspace(int64_t T, int64_t E) {
   const int64_t nb = route_blocks(T);
   if (nb <= 1) return 0;
-  return counts_bytes(nb, E) + (nb > kSumBlocks ? (size_t)(nb + 1) * (size_t)E * 4 : 0);
+  return counts_bytes(nb, E) + (scans(nb, E) ? (size_t)(nb + 1) * (size_t)E * 4 : 0);
 }
 
 hipError_t launch_route(const void* x, int dt, int64_t T, int64_t E, int64_t ld, int score, const float* bias,
@@ -597,7 +600,7 @@ hipError_t launch_route(const void* x, int dt, int64_t T, int64_t E, int64_t ld,
   a.scale = scale;
   a.ids = ids; a.row_token = row_token; a.offsets = offsets; a.row_of = row_of; a.weights = weights;
   a.counts = nb <= 1 ? nullptr : static_cast<uint8_t*>(ws);
-  a.prefix = nb <= kSumBlocks ? nullptr : reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + counts_bytes(nb, E));
+  a.prefix = !scans(nb, E) ? nullptr : reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + counts_bytes(nb, E));
   const int64_t unit = dt == 2 ? 4 : 8;              // elements per 16 bytes
   a.vec = ld % unit == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
   const bool general = bias || G > 1;

@@ -162,6 +162,23 @@ def test_route_many_tokens_plan():
     assert np.array_equal(off.cpu().numpy(), np.concatenate([[0], np.cumsum(np.bincount(flat[flat >= 0], minlength=E))]))
 
 
+def test_route_scanned_plan():
+    """So many blocks that their counts are scanned by a kernel of their own."""
+    T, E, k = 100003, 256, 3
+    x = torch.randn((T, E), device=DEV, generator=torch.Generator(DEV).manual_seed(5))
+    x[::41] = -float("inf")
+    ids, _, row_token, off, row_of = (t.cpu().numpy() for t in ops.w4_route(x, k))
+    flat = ids.reshape(-1)
+    order = np.argsort(np.where(flat < 0, E, flat), kind="stable")
+    n = int((flat >= 0).sum())
+    assert n == (T - len(range(0, T, 41))) * k
+    assert np.array_equal(row_token, np.where(np.arange(flat.size) < n, order // k, -1))
+    inv = np.full(flat.size, -1)
+    inv[order[:n]] = np.arange(n)
+    assert np.array_equal(row_of.reshape(-1), inv)
+    assert np.array_equal(off, np.concatenate([[0], np.cumsum(np.bincount(flat[flat >= 0], minlength=E))]))
+
+
 # ------------------------------------------------------------------ quantizer
 
 @pytest.mark.parametrize("M,K", [(1, 8), (1, 128), (3, 136), (5, 1000), (17, 4096), (2, 14336), (257, 264), (64, 2048)])
