@@ -295,6 +295,10 @@ __global__ __launch_bounds__(256) void fp8_reduce_kernel(Fp8Args p, const float*
   store_columns<OUT, 8>(p, f, c / nc * p.N, (int)(c % nc) * 8, p.bias != nullptr);
 }
 
+// The 256 x 256 tile does a third more work per time than four of 128 x 128, as
+// long as its padding takes no more than that.
+static bool wide_pays(int64_t t256, int64_t t128) { return 3 * t256 <= t128; }
+
 // What the dense product runs as: rows streamed (tile 0), or a tile and its
 // K splits.
 struct DensePlan {
@@ -313,7 +317,7 @@ static DensePlan plan_dense(int64_t M, int64_t N, int64_t K) {
   if (M <= 16) return {0, 1};
   const int64_t KB = (K + 127) / 128;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 192) return {256, 1};
+  if (tiles(256, 256) >= 192 && wide_pays(tiles(256, 256), tiles(128, 128))) return {256, 1};
   const int tile = M <= 64 ? 64 : 128;
   const int64_t t = tiles(tile, 128);
   int64_t best = 1, cost = 4000 + 900 * KB;   // ns
@@ -421,7 +425,10 @@ hipError_t launch_fp8_block_grouped(const void* a, const float* a_scale, const i
   // by the average rows of an expert (64 experts of 2048 x 7168): 4 rows 157 us streamed, 159 in 128-row tiles; 8 rows
   // 184 and 163; 96 rows 203 in 128-row tiles, 202 in 256-row ones; 128 rows 280 and 237
   if (R <= 4 * E) return launch_fp8_stream(p, out_dt, stream);
-  if (R <= 96 * E) return tile_go<4, 4, 2, 2>(p, false, out_dt, stream);
+  // few tiles: the smaller ones reach more CUs (4 experts, 2000 rows, 512 x 4096: 26 us, 52 in 256-row tiles; about 144
+  // tiles 38 and 56, about 160 109 and 98); 128 columns: 16384 rows 28 us, 52 in 256-wide tiles
+  const int64_t c256 = (N + 255) / 256, c128 = (N + 127) / 128;
+  if (R <= 96 * E || (R / 256 + E / 2) * c256 < 160 || !wide_pays(2 * c256, 4 * c128)) return tile_go<4, 4, 2, 2>(p, false, out_dt, stream);
   return tile_go<8, 4, 2, 4>(p, false, out_dt, stream);
 }
 

@@ -450,6 +450,14 @@ def _arg(t, dtype, shape: tuple, what: str):
     return t.data_ptr() if t.is_cuda and t.is_contiguous() else t
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor of the stream that will write it: memory of another stream could still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _call(fn: str, *args) -> None:
     try:
         rc = getattr(lib(), fn)(*args)
@@ -476,11 +484,11 @@ def _rows_ptr(t, what: str):
     return t.data_ptr() or None, (t.stride(0) if t.numel() and t.shape[0] > 1 else t.shape[1])
 
 
-def w4_route_workspace(T: int, E: int, topk: int, device="cuda") -> torch.Tensor:
-    """Device scratch for w4_route at these sizes (uint8, possibly empty)."""
+def w4_route_workspace(T: int, E: int, topk: int, device="cuda", stream=None) -> torch.Tensor:
+    """Device scratch for w4_route at these sizes (uint8, possibly empty), for use on `stream`."""
     n = ctypes.c_size_t(0)
     _check("w4_route_workspace_bytes", lib().w4_route_workspace_bytes(T, E, topk, ctypes.byref(n)))
-    return torch.empty((n.value,), dtype=torch.uint8, device=device)
+    return _new((n.value,), torch.uint8, device, stream)
 
 
 def w4_route(logits, topk: int, score: str = "softmax", bias=None, n_groups: int = 1, topk_groups: int = 1,
@@ -494,11 +502,9 @@ def w4_route(logits, topk: int, score: str = "softmax", bias=None, n_groups: int
     if score not in W4_SCORES:
         raise ValueError(f"score must be one of {sorted(W4_SCORES)}, got {score!r}")
     if out is None:
-        out = (torch.empty((T, topk), dtype=torch.int32, device=dev),
-               torch.empty((T, topk), dtype=torch.float32, device=dev),
-               torch.empty((T * topk,), dtype=torch.int32, device=dev),
-               torch.empty((E + 1,), dtype=torch.int32, device=dev),
-               torch.empty((T, topk), dtype=torch.int32, device=dev))
+        out = (_new((T, topk), torch.int32, dev, stream), _new((T, topk), torch.float32, dev, stream),
+               _new((T * topk,), torch.int32, dev, stream), _new((E + 1,), torch.int32, dev, stream),
+               _new((T, topk), torch.int32, dev, stream))
     ids, weights, row_token, offsets, row_of = out
     p_bias = _arg(bias, torch.float32, (E,), "bias")
     p_ids = _arg(ids, torch.int32, (T, topk), "ids")
@@ -507,7 +513,7 @@ def w4_route(logits, topk: int, score: str = "softmax", bias=None, n_groups: int
     p_off = _arg(offsets, torch.int32, (E + 1,), "expert_offsets")
     p_row = _arg(row_of, torch.int32, (T, topk), "row_of")
     if workspace is None:
-        workspace = w4_route_workspace(T, E, topk, device=dev)
+        workspace = w4_route_workspace(T, E, topk, dev, stream)
     _call("w4_route",
         ptr, _float_code(logits.dtype), T, E, ld, W4_SCORES[score], p_bias, n_groups, topk_groups, group_top, topk,
         int(renorm), scale, p_ids, p_weights, p_token, p_off, p_row, _ptr(workspace),
@@ -527,8 +533,7 @@ def w4_fp8_block_quantize(x, act: str = "none", out=None, stream=None):
     ptr, ldx = _rows_ptr(x, "x")
     KB = (K + 127) // 128
     if out is None:
-        out = (torch.empty((M, K), dtype=torch.uint8, device=x.device),
-               torch.empty((M, KB), dtype=torch.float32, device=x.device))
+        out = (_new((M, K), torch.uint8, x.device, stream), _new((M, KB), torch.float32, x.device, stream))
     codes, scales = out
     p_codes = _arg(_e4m3_codes(codes, "codes"), codes.dtype, (M, K), "codes")
     _call("w4_fp8_block_quantize",
@@ -537,11 +542,11 @@ def w4_fp8_block_quantize(x, act: str = "none", out=None, stream=None):
     return out
 
 
-def w4_fp8_block_gemm_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
-    """Device scratch for w4_fp8_block_gemm at these sizes (uint8, possibly empty)."""
+def w4_fp8_block_gemm_workspace(M: int, N: int, K: int, device="cuda", stream=None) -> torch.Tensor:
+    """Device scratch for w4_fp8_block_gemm at these sizes (uint8, possibly empty), for use on `stream`."""
     n = ctypes.c_size_t(0)
     _check("w4_fp8_block_gemm_workspace_bytes", lib().w4_fp8_block_gemm_workspace_bytes(M, N, K, ctypes.byref(n)))
-    return torch.empty((n.value,), dtype=torch.uint8, device=device)
+    return _new((n.value,), torch.uint8, device, stream)
 
 
 def w4_fp8_block_gemm(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloat16, workspace=None,
@@ -553,13 +558,13 @@ def w4_fp8_block_gemm(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=tor
         raise ValueError(f"a has {K} columns, w {Kw}")
     KB, NB = (K + 127) // 128, (N + 127) // 128
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        out = _new((M, N), out_dtype, a.device, stream)
     p_as = _arg(a_scale, torch.float32, (M, KB), "a_scale")
     p_ws = _arg(w_scale, torch.float32, (NB, KB), "w_scale")
     p_bias = _arg(bias, out.dtype, (N,), "bias")
     p_out = _arg(out, out.dtype, (M, N), "out")
     if workspace is None:
-        workspace = w4_fp8_block_gemm_workspace(M, N, K, device=a.device)
+        workspace = w4_fp8_block_gemm_workspace(M, N, K, a.device, stream)
     _call("w4_fp8_block_gemm",
         _ptr(a), p_as, _ptr(w), p_ws, p_bias, p_out, _float_code(out.dtype), M, N, K, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
@@ -577,7 +582,7 @@ def w4_fp8_block_grouped_gemm(a, a_scale, row_token, expert_offsets, w, w_scale,
     KB, NB = (K + 127) // 128, (N + 127) // 128
     R = T if row_token is None else row_token.shape[0]
     if out is None:
-        out = torch.empty((R, N), dtype=out_dtype, device=a.device)
+        out = _new((R, N), out_dtype, a.device, stream)
     p_as = _arg(a_scale, torch.float32, (T, KB), "a_scale")
     p_token = _arg(row_token, torch.int32, (R,), "row_token")
     p_off = _arg(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
@@ -594,7 +599,7 @@ def w4_combine(y, row_of, weights, add=None, out=None, stream=None):
     R, N = y.shape
     T, topk = row_of.shape
     if out is None:
-        out = torch.empty((T, N), dtype=y.dtype, device=y.device)
+        out = _new((T, N), y.dtype, y.device, stream)
     _call("w4_combine",
         _ptr(y), _float_code(y.dtype), _arg(row_of, torch.int32, (T, topk), "row_of"),
         _arg(weights, torch.float32, (T, topk), "weights"), _arg(add, y.dtype, (T, N), "add"),

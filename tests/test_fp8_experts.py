@@ -464,6 +464,34 @@ def test_combine_far_rows():
     assert (out[0] == 3).all() and (out[1] == -2).all()
 
 
+def test_stream_argument():
+    """Outputs and workspaces of calls on a given stream come from that stream's memory; results as on the default."""
+    T, E, H, N, k = 300, 8, 512, 256, 2
+    g = torch.Generator(DEV).manual_seed(8)
+    x = torch.randn((T, H), device=DEV, generator=g).bfloat16()
+    logits = torch.randn((T, E), device=DEV, generator=g)
+    w = torch.randint(0, 0x7F, (E, N, H), device=DEV, generator=g, dtype=torch.uint8)
+    ws = torch.rand((E, N // 128, H // 128), device=DEV, generator=g) * 1e-4
+
+    def chain(st):
+        _, wt, rt, off, ro = ops.w4_route(logits, k, stream=st)
+        q, qs = ops.w4_fp8_block_quantize(x, stream=st)
+        y = ops.w4_fp8_block_grouped_gemm(q, qs, rt, off, w, ws, stream=st)
+        z = ops.w4_fp8_block_gemm(q, qs, w[0], ws[0], stream=st)
+        return ops.w4_combine(y, ro, wt, add=z, stream=st)
+    want = chain(None)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    busy = torch.empty(1 << 26, device=DEV)
+    for _ in range(3):
+        busy.normal_()                                           # pending work and freed blocks on the default stream
+        del busy
+        busy = torch.empty(1 << 26, device=DEV)
+        got = chain(st)
+        st.synchronize()
+        assert torch.equal(got, want)
+
+
 def layer_case(E, H, I, topk, T, seed, **kw):
     from int4_weight_quantized_amd.fp8_experts import Fp8Experts
     r = rng_for(E, H, I, T, seed)
