@@ -317,6 +317,41 @@ def test_block_gemm_larger(M, N, K, dt):
           (M, N, K, dt))
 
 
+@pytest.mark.parametrize("M,N,K", [(4101, 3080, 400), (3329, 4104, 144), (2305, 6152, 1152)])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_block_gemm_many_tiles(M, N, K, dt):
+    """Enough tiles for the largest kind, its last row and column tiles and last K block partial."""
+    say("gemm many tiles", M, N, K, dt)
+    a, sa, w, sw = dense_inputs(M, N, K, 5)
+    bias = torch.from_numpy(rng_for(N).standard_normal(N)).to(DT[dt]).float().numpy()
+    got = run_dense(a, sa, w, sw, bias, dt, M, N)
+    rows = np.unique(np.r_[0, 255, 256, M - 2, M - 1, rng_for(M).integers(0, M, 30)])
+    y, mag = O.block_gemm(a[rows], sa[rows], w, sw, bias)
+    check(got[torch.from_numpy(rows).to(DEV)], y, product_tol(y, mag, dt, -(-K // 128)), (M, N, K, dt))
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_grouped_gemm_many_tiles(gather, dt):
+    """The largest tiles over segments: several row tiles, one row, half a tile (idle waves), none."""
+    counts = np.array([700, 513, 0, 256, 31, 1100, 1, 120])
+    E, R, N, K, tail = len(counts), int(counts.sum()), 3720, 400, 2
+    say("grouped many tiles", gather, dt)
+    r = rng_for(E, R, N, K)
+    T = 333 if gather else R + tail
+    a, w = fp8_inputs(r, (T, K), 4), fp8_inputs(r, (E, N, K), 4)
+    sa = r.uniform(1e-4, 3e-3, (T, 4)).astype(np.float32)
+    sw = r.uniform(1e-4, 3e-3, (E, -(-N // 128), 4)).astype(np.float32)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rt = np.concatenate([r.integers(0, T, R), [-1] * tail]).astype(np.int32) if gather else None
+    out = torch.full((R + tail, N), 7.0, dtype=DT[dt], device=DEV)
+    ops.w4_fp8_block_grouped_gemm(gpu(a), gpu(sa), None if rt is None else gpu(rt), gpu(off), gpu(w), gpu(sw), out=out)
+    torch.cuda.synchronize()
+    y, mag = O.grouped_gemm(a, sa, rt, off, w, sw)
+    check(out[:R], y, product_tol(y, mag, dt, 4), (gather, dt))
+    assert (out[R:] == 7).all()
+
+
 @pytest.mark.parametrize("M", [1, 20, 300])
 def test_block_gemm_nan_and_reproducible(M):
     """NaN codes and scales reach exactly their rows and columns, and two runs agree bit for bit."""
