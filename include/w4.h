@@ -547,7 +547,9 @@ int w4_route(const void* logits, int logits_dtype, int64_t T, int64_t E, int64_t
  *   v = x, or with W4_ACT_SWIGLU x[:, k] * sigmoid(x[:, k]) * x[:, K + k]
  *   scale = max |v| / 448;  code = E4M3(v / scale), nearest even, saturating
  * both divisions correctly rounded. A block of zeros has scale 0 and codes 0.
- * A NaN in a block makes its scale NaN (codes 0), an infinity makes it +inf.
+ * A NaN in a block makes its scale NaN and its codes 0. An infinity makes the
+ * scale +inf, its own code NaN (inf / inf) and the finite columns' codes 0.
+ * Either way the products' row is NaN.
  *   x       device, [M, K] ([M, 2K] with W4_ACT_SWIGLU), row stride ldx (a
  *           multiple of 8), bf16 or fp16, 16-byte aligned
  *   codes   device, [M, K] E4M3 bytes, 8-byte aligned

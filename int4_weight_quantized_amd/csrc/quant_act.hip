@@ -317,9 +317,11 @@ __global__ __launch_bounds__(kQThreads) void quant_act_asym_kernel(const uint16_
 // both divisions correctly rounded (the same row division as above, with the
 // block in place of the row). 16 lanes hold one block, 8 columns each, so the
 // maximum is four lane exchanges and the data are read once. The maximum is
-// taken over the bits of |v|: a NaN is the largest, gives the block a NaN
-// scale and so reaches the product's row; infinity likewise. A block of
-// zeros has scale 0 and codes 0.
+// taken over the bits of |v|: a NaN is the largest and gives the block a NaN
+// scale, and codes 0. An infinity gives the scale +inf; inf / inf is NaN, so
+// its code is the NaN code (the clamp alone would make it -448), and the
+// finite columns' codes are 0. Either way the product's row is NaN. A block
+// of zeros has scale 0 and codes 0.
 //
 // HBM-bound: 2 bytes in (4 with the gate) + 1 byte out per element + 4 per
 // block.
@@ -374,6 +376,11 @@ __global__ __launch_bounds__(kQThreads) void block_quant_kernel(const uint16_t* 
     for (int i = 0; i < 8; ++i) q[i] = clamp448(__fdiv_rn(v[i], s));
   }
   o = pack_fp8(q);
+  if (!r.fast) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)   // E4M3's NaN codes are 0x7F and 0xFF
+      if (__builtin_isinf(v[i])) o[i / 4] |= 0x7F << (8 * (i % 4));
+  }
   if (r.zero_row) o = v2i{0, 0};
   if (in) *reinterpret_cast<v2i*>(codes + m * K + k) = o;
   if ((threadIdx.x & 15) == 0) scales[u] = s;

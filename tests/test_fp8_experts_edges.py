@@ -1,0 +1,94 @@
+"""GPU tests of the FP8 expert path's edges: infinities and NaN on their way
+through the quantizer and the products."""
+import numpy as np
+import pytest
+import torch
+
+from int4_weight_quantized_amd import ops
+from test_fp8_experts import DEV, DT, fp8_inputs, gpu, rng_for, say
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ infinities in the quantizer
+
+INF, NAN = float("inf"), float("nan")
+# row -> {column: value of v}; columns of the second and third 128-block
+ODD = {1: {130: INF}, 2: {131: -INF}, 3: {256: INF, 257: -INF}, 4: {c: INF for c in range(128, 256)},
+       5: {140: -INF, 141: NAN}, 6: {300: NAN}}
+
+
+def odd_rows(dt, act):
+    """x whose v has the infinities and NaN of ODD and is finite elsewhere, [8, 384] (or gate | up side by side)."""
+    r = rng_for(len(dt), len(act), 31)
+    v = r.standard_normal((8, 384))
+    if act == "none":
+        for row, at in ODD.items():
+            for c, val in at.items():
+                v[row, c] = val
+        return gpu(v, DT[dt])
+    up = 1.0 + r.random((8, 384))
+    for row, at in ODD.items():
+        for i, (c, val) in enumerate(at.items()):
+            # +-inf by the gate, by the other factor, and (bf16) by a product past fp32's range
+            if np.isnan(val):
+                v[row, c] = NAN
+            elif i % 2 == 0:
+                v[row, c], up[row, c] = INF, np.copysign(1.5, val)
+            elif dt == "bf16":
+                v[row, c], up[row, c] = 2e38, np.copysign(2e38, val)
+            else:
+                v[row, c], up[row, c] = 2.0, val
+    return gpu(np.concatenate([v, up], axis=1), DT[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_block_quantize_infinities(dt, act):
+    """An infinity makes its block's scale +inf, its own code NaN and the finite columns' codes 0 (inf / inf and
+    v / inf); a NaN in the block makes the scale NaN and every code 0. Other blocks know nothing of it."""
+    say("quant infinities", dt, act)
+    x = odd_rows(dt, act)
+    codes, scales = ops.w4_fp8_block_quantize(x, act=act)
+    d = codes.view(torch.float8_e4m3fn).float().cpu().numpy().reshape(8, 3, 128)
+    s = scales.cpu().numpy()
+    hit = np.zeros((8, 3), dtype=bool)
+    for row, at in ODD.items():
+        b = next(iter(at)) // 128
+        hit[row, b] = True
+        vals = np.zeros(128)
+        for c, val in at.items():
+            vals[c - 128 * b] = val
+        if np.isnan(vals).any():
+            assert np.isnan(s[row, b]) and (d[row, b] == 0).all(), row
+        else:
+            assert np.isposinf(s[row, b]), row
+            assert np.array_equal(np.isnan(d[row, b]), np.isinf(vals)), row
+            assert (d[row, b][np.isfinite(vals)] == 0).all(), row
+    assert np.isfinite(s[~hit]).all() and (s[~hit] > 0).all() and np.isfinite(d[~hit]).all()
+    assert (np.abs(d[~hit]).max(1) == 448).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("copies", [1, 5, 25])
+def test_infinities_reach_their_rows(dt, act, copies):
+    """Rows with an infinity or a NaN come out of the products as NaN whatever its sign, the others finite: streamed
+    (8 rows), 64-row tiles (40), 128-row tiles (200), and over expert segments."""
+    say("infinities through the product", dt, act, copies)
+    x = odd_rows(dt, act).repeat(copies, 1)
+    M, N, K = 8 * copies, 72, 384
+    codes, scales = ops.w4_fp8_block_quantize(x, act=act)
+    r = rng_for(N, K, 5)
+    w = gpu(fp8_inputs(r, (3, N, K), 3))
+    ws = gpu(r.uniform(1e-3, 3e-3, (3, 1, 3)).astype(np.float32))
+    want = torch.tensor([row in ODD for row in range(8)], device=DEV).repeat(copies)[:, None].expand(M, N)
+    for out_dt in (torch.bfloat16, torch.float16, torch.float32):
+        y = ops.w4_fp8_block_gemm(codes, scales, w[0], ws[0], out_dtype=out_dt)
+        assert torch.equal(torch.isnan(y), want) and torch.isfinite(y[~want]).all(), out_dt
+    off = gpu(np.array([0, M // 2, M // 2, M], dtype=np.int32))
+    y = ops.w4_fp8_block_grouped_gemm(codes, scales, None, off, w, ws)
+    assert torch.equal(torch.isnan(y), want) and torch.isfinite(y[~want]).all()
+    order = torch.arange(M - 1, -1, -1, dtype=torch.int32, device=DEV)
+    y = ops.w4_fp8_block_grouped_gemm(codes, scales, order, off, w, ws, out_dtype=torch.float16)
+    assert torch.equal(torch.isnan(y), want.flip(0)) and torch.isfinite(y[~want.flip(0)]).all()
