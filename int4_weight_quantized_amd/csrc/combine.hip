@@ -57,17 +57,17 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[8]) 
 }
 
 // One thread per 8 columns of a token; chunk c of the T * N/8 belongs to
-// token c / (N/8), a 32-bit division where the chunks allow it (I). (Loading
-// the rows of 4 slots ahead of their use was 12% slower.)
-template <int DT, typename I>
+// token c / (N/8), a 32-bit division. (Loading the rows of 4 slots ahead of
+// their use was 12% slower.)
+template <int DT>
 __global__ __launch_bounds__(kCThreads) void combine_kernel(const void* __restrict__ y,
                                                             const int32_t* __restrict__ row_of,
                                                             const float* __restrict__ weights,
                                                             const void* add, void* out,
-                                                            I T, int R, int topk, int N) {
-  const I nc = (I)(N >> 3);
-  const I c = (I)blockIdx.x * kCThreads + threadIdx.x;
-  const I t = c / nc;
+                                                            uint32_t T, int R, int topk, int N) {
+  const uint32_t nc = (uint32_t)N >> 3;
+  const uint32_t c = blockIdx.x * kCThreads + threadIdx.x;
+  const uint32_t t = c / nc;
   if (t >= T) return;
   const int64_t n = (int64_t)(c - t * nc) * 8;
   const int32_t* rows = row_of + (int64_t)t * topk;
@@ -94,20 +94,24 @@ __global__ __launch_bounds__(kCThreads) void combine_kernel(const void* __restri
 hipError_t launch_combine(const void* y, int dt, const int32_t* row_of, const float* weights, const void* add,
                           void* out, int64_t T, int64_t R, int64_t topk, int64_t N, hipStream_t stream) {
   if (T == 0 || N == 0) return hipSuccess;
-  const int64_t chunks = T * (N / 8);
-  const dim3 grid((unsigned)((chunks + kCThreads - 1) / kCThreads)), block(kCThreads);
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, stream, y, row_of, weights, add, out, T, (int)R, (int)topk, (int)N);
-  };
-  auto by_dt = [&](auto index) {
-    using I = decltype(index);
-    if (dt == 0) go(combine_kernel<0, I>);
-    else if (dt == 1) go(combine_kernel<1, I>);
-    else go(combine_kernel<2, I>);
-  };
-  if (chunks < ((int64_t)1 << 31)) by_dt((uint32_t)0);
-  else by_dt((int64_t)0);
-  return hipGetLastError();
+  // a launch takes fewer than 2^32 threads: past 2^31 chunks, token ranges in turn
+  const int64_t per = (((int64_t)1 << 31) - 1) / (N / 8), size = dt == 2 ? 4 : 2;
+  for (int64_t t0 = 0; t0 < T; t0 += per) {
+    const int64_t n = T - t0 < per ? T - t0 : per;
+    const dim3 grid((unsigned)((n * (N / 8) + kCThreads - 1) / kCThreads)), block(kCThreads);
+    const int64_t at = t0 * N * size;
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, block, 0, stream, y, row_of + t0 * topk, weights + t0 * topk,
+                         add ? static_cast<const char*>(add) + at : nullptr, static_cast<char*>(out) + at, (uint32_t)n,
+                         (int)R, (int)topk, (int)N);
+    };
+    if (dt == 0) go(combine_kernel<0>);
+    else if (dt == 1) go(combine_kernel<1>);
+    else go(combine_kernel<2>);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace w4

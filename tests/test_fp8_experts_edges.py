@@ -1,5 +1,5 @@
 """GPU tests of the FP8 expert path's edges: infinities and NaN on their way
-through the quantizer and the products."""
+through the quantizer and the products, and sizes past one launch's threads."""
 import numpy as np
 import pytest
 import torch
@@ -92,3 +92,20 @@ def test_infinities_reach_their_rows(dt, act, copies):
     order = torch.arange(M - 1, -1, -1, dtype=torch.int32, device=DEV)
     y = ops.w4_fp8_block_grouped_gemm(codes, scales, order, off, w, ws, out_dtype=torch.float16)
     assert torch.equal(torch.isnan(y), want.flip(0)) and torch.isfinite(y[~want.flip(0)]).all()
+
+
+# ------------------------------------------------------------------ sizes past one launch's threads (2^32)
+
+def test_combine_past_one_launch():
+    """T * N / 8 just above 2^32 (64 GiB of output): every token gets its row, none of the ranges is left out."""
+    N, R = 8192, 3
+    T = (1 << 32) // (N // 8) + 7
+    say("combine past one launch", T, N)
+    y = torch.arange(1, R * N + 1, device=DEV).remainder_(251).reshape(R, N).bfloat16()
+    table = torch.cat([torch.zeros((1, N), dtype=y.dtype, device=DEV), y])
+    row = (torch.arange(T, device=DEV) * 2654435761 >> 7).remainder_(4).to(torch.int32) - 1
+    out = torch.full((T, N), 7.0, dtype=y.dtype, device=DEV)
+    ops.w4_combine(y, row[:, None].contiguous(), torch.ones((T, 1), device=DEV), out=out)
+    for t0 in range(0, T, 1 << 18):
+        part = slice(t0, min(T, t0 + (1 << 18)))
+        assert torch.equal(out[part], table[row[part].long() + 1]), t0
