@@ -388,18 +388,24 @@ __global__ __launch_bounds__(kQThreads) void block_quant_kernel(const uint16_t* 
 
 hipError_t launch_block_quant(const void* x, bool bf16, bool swiglu, int64_t M, int64_t K, int64_t ldx, void* codes,
                               float* scales, hipStream_t stream) {
-  const int64_t KB = (K + 127) / 128, units = M * KB;
-  if (units == 0) return hipSuccess;
-  const dim3 grid((unsigned)((units + kBQUnits - 1) / kBQUnits)), block(kQThreads);
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, stream, static_cast<const uint16_t*>(x), ldx, (int)K, (uint32_t)KB, (uint32_t)units,
-                       static_cast<uint8_t*>(codes), scales);
-  };
-  if (bf16 && swiglu) go(block_quant_kernel<true, true>);
-  else if (bf16) go(block_quant_kernel<true, false>);
-  else if (swiglu) go(block_quant_kernel<false, true>);
-  else go(block_quant_kernel<false, false>);
-  return hipGetLastError();
+  if (M == 0 || K == 0) return hipSuccess;
+  // a launch takes fewer than 2^32 threads: past 2^28 blocks of 16 lanes, row ranges in turn
+  const int64_t KB = (K + 127) / 128, per = (((int64_t)1 << 28) - kBQUnits) / KB;
+  for (int64_t m0 = 0; m0 < M; m0 += per) {
+    const int64_t units = (M - m0 < per ? M - m0 : per) * KB;
+    const dim3 grid((unsigned)((units + kBQUnits - 1) / kBQUnits)), block(kQThreads);
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, block, 0, stream, static_cast<const uint16_t*>(x) + m0 * ldx, ldx, (int)K,
+                         (uint32_t)KB, (uint32_t)units, static_cast<uint8_t*>(codes) + m0 * K, scales + m0 * KB);
+    };
+    if (bf16 && swiglu) go(block_quant_kernel<true, true>);
+    else if (bf16) go(block_quant_kernel<true, false>);
+    else if (swiglu) go(block_quant_kernel<false, true>);
+    else go(block_quant_kernel<false, false>);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Test hook of the FP8 encode: the fp32 values with bit patterns first,

@@ -5,6 +5,8 @@ import pytest
 import torch
 
 from int4_weight_quantized_amd import ops
+from oracle import fp8_experts as O
+from oracle.w4_oracle import e4m3_decode
 from test_fp8_experts import DEV, DT, fp8_inputs, gpu, rng_for, say
 
 pytestmark = pytest.mark.gpu
@@ -109,3 +111,23 @@ def test_combine_past_one_launch():
     for t0 in range(0, T, 1 << 18):
         part = slice(t0, min(T, t0 + (1 << 18)))
         assert torch.equal(out[part], table[row[part].long() + 1]), t0
+
+
+def test_block_quantize_past_one_launch():
+    """More than 2^28 blocks, one per row: a pattern of 64 rows, its codes and scales repeated to the end."""
+    K, P = 8, 64
+    M = (1 << 28) + 3 * P + 5
+    say("quant past one launch", M, K)
+    g = torch.Generator(DEV).manual_seed(12)
+    rows = torch.randn((P, K), device=DEV, generator=g).bfloat16()
+    x = rows.repeat(M // P + 1, 1)[:M]
+    codes = torch.full((M, K), 0x55, dtype=torch.uint8, device=DEV)
+    scales = torch.full((M, 1), 7.0, device=DEV)
+    ops.w4_fp8_block_quantize(x, out=(codes, scales))
+    c, s = O.block_quantize(rows.float().cpu().numpy())
+    c, s = gpu(e4m3_decode(c)), gpu(s)
+    for m0 in range(0, M, 1 << 24):                              # a multiple of P
+        part = slice(m0, min(M, m0 + (1 << 24)))
+        n = part.stop - m0
+        assert torch.equal(scales[part], s.repeat(n // P + 1, 1)[:n]), m0
+        assert torch.equal(codes[part].view(torch.float8_e4m3fn).float(), c.float().repeat(n // P + 1, 1)[:n]), m0
