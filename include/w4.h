@@ -519,7 +519,7 @@ int w4_probe_mfma(int kind, int64_t iters, int32_t* sink, int64_t sink_elems, do
  *   logits    device, [T, E] with row stride ld >= E; bf16, fp16 or fp32
  *   bias      device or NULL, fp32 [E]: moves the choice, not the weights
  *   n_groups  1..64, dividing E;  topk_groups 1..n_groups;  group_top 1 or 2
- *   topk      1..min(E, 64);  E at most 1024
+ *   topk      1..min(E, 64);  E at most 1024;  T at most 2^28 - 64
  *   ids, weights  device, int32 / fp32 [T, topk]
  *   row_token device, int32 [T * topk]: token of each planned row; -1 past
  *             the last
@@ -531,7 +531,7 @@ int w4_probe_mfma(int kind, int64_t iters, int32_t* sink, int64_t sink_elems, do
  *             when that is 0), owned by the caller; calls sharing one must
  *             not overlap. Nothing in it needs to start at zero.
  * Results do not depend on timing. T == 0 writes expert_offsets only.
- * Errors: INVALID, ALIGN, GROUP, DTYPE, UNSUPPORTED (E, topk, group_top,
+ * Errors: INVALID, ALIGN, GROUP, DTYPE, UNSUPPORTED (T, E, topk, group_top,
  *         T*topk >= 2^31), HIP.
  */
 int w4_route_workspace_bytes(int64_t T, int64_t E, int64_t topk, size_t* bytes);

@@ -730,8 +730,10 @@ static int check_route_sizes(const char* fn, int64_t T, int64_t E, int64_t topk)
     return fail(W4_ERR_INVALID, "%s: sizes must be T >= 0, E > 0, topk > 0 (got T=%lld E=%lld topk=%lld)", fn,
                 (long long)T, (long long)E, (long long)topk);
   if (topk > E) return fail(W4_ERR_INVALID, "%s: topk=%lld exceeds E=%lld", fn, (long long)topk, (long long)E);
-  if (E > 1024 || topk > 64 || T > kMaxDim || T * topk >= ((int64_t)1 << 31))
-    return fail(W4_ERR_UNSUPPORTED, "%s: T=%lld E=%lld topk=%lld outside E <= 1024, topk <= 64, T*topk < 2^31", fn,
+  // 1024 threads route 64 tokens, and a launch takes fewer than 2^32 threads
+  if (E > 1024 || topk > 64 || T > ((int64_t)1 << 28) - 64 || T * topk >= ((int64_t)1 << 31))
+    return fail(W4_ERR_UNSUPPORTED,
+                "%s: T=%lld E=%lld topk=%lld outside T <= 2^28 - 64, E <= 1024, topk <= 64, T*topk < 2^31", fn,
                 (long long)T, (long long)E, (long long)topk);
   return W4_OK;
 }

@@ -131,3 +131,21 @@ def test_block_quantize_past_one_launch():
         n = part.stop - m0
         assert torch.equal(scales[part], s.repeat(n // P + 1, 1)[:n]), m0
         assert torch.equal(codes[part].view(torch.float8_e4m3fn).float(), c.float().repeat(n // P + 1, 1)[:n]), m0
+
+
+def test_route_most_tokens():
+    """The largest T: the choice, and the plan as a permutation ordered by expert, then token."""
+    T = (1 << 28) - 64
+    say("route most tokens", T)
+    x = torch.empty((T, 2), dtype=torch.bfloat16, device=DEV)
+    second = (torch.arange(T, device=DEV) * 40503 >> 9).remainder_(3) == 0
+    x[:, 0] = 0
+    x[:, 1] = torch.where(second, 1.0, -1.0)
+    ids, weights, row_token, off, row_of = ops.w4_route(x, 1)
+    ids, row_of = ids.view(-1), row_of.view(-1)
+    assert torch.equal(ids == 1, second) and int(ids.min()) == 0 and bool((weights == 1).all())
+    n0 = T - int(second.sum())
+    assert off.tolist() == [0, n0, T]
+    tokens = torch.arange(T, dtype=torch.int32, device=DEV)
+    assert torch.equal(row_token[:n0], tokens[~second]) and torch.equal(row_token[n0:], tokens[second])
+    assert torch.equal(row_token[row_of.long()], tokens)
