@@ -578,8 +578,9 @@ int w4_fp8_block_quantize(const void* x, int x_dtype, int64_t M, int64_t K, int6
  *            may be NULL when that is 0): fp32 partial tiles where few rows
  *            make the product split K, summed in a fixed order (results are
  *            reproducible). Calls sharing one must not overlap.
- * Errors: INVALID, ALIGN, DTYPE, UNSUPPORTED, HIP. M == 0 or N == 0 enqueues
- *         nothing.
+ * Errors: INVALID, ALIGN, DTYPE, UNSUPPORTED (also 2^24 output tiles and
+ *         more: 128 x 128, 64 x 128 up to 64 rows, 16 x 32 up to 16 rows),
+ *         HIP. M == 0 or N == 0 enqueues nothing.
  */
 int w4_fp8_block_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
 int w4_fp8_block_gemm(const void* a, const float* a_scale, const void* w, const float* w_scale, const void* bias,
@@ -601,8 +602,10 @@ int w4_fp8_block_gemm(const void* a, const float* a_scale, const void* w, const 
  *   out      device, [R, N] in out_dtype (bf16 or fp16)
  *   a, w and out must be 16-byte aligned; N a multiple of 8, K of 16 and at
  *   most 2^22.
- * Errors: INVALID, ALIGN, DTYPE, UNSUPPORTED (T*K >= 2^31 with row_token),
- *         HIP. Decreasing offsets are undefined behaviour.
+ * Errors: INVALID, ALIGN, DTYPE, UNSUPPORTED (T*K >= 2^31 with row_token;
+ *         tiles of 2^32 threads in all: from 2^24 of 128 x 128, or of 16 x 32
+ *         where R is at most 4 E), HIP. Decreasing offsets are undefined
+ *         behaviour.
  */
 int w4_fp8_block_grouped_gemm(const void* a, const float* a_scale, const int32_t* row_token,
                               const int32_t* expert_offsets, int64_t E, const void* w, const float* w_scale,

@@ -60,6 +60,8 @@ hipError_t launch_route(const void* x, int dt, int64_t T, int64_t E, int64_t ld,
 hipError_t launch_block_quant(const void* x, bool bf16, bool swiglu, int64_t M, int64_t K, int64_t ldx, void* codes,
                               float* scales, hipStream_t stream);
 size_t fp8_block_gemm_workspace(int64_t M, int64_t N, int64_t K);
+int64_t fp8_block_gemm_threads(int64_t M, int64_t N, int64_t K);
+int64_t fp8_block_grouped_threads(int64_t E, int64_t R, int64_t N);
 hipError_t launch_fp8_block_gemm(const void* a, const float* a_scale, const void* w, const float* w_scale,
                                  const void* bias, void* out, int out_dt, int64_t M, int64_t N, int64_t K, void* ws,
                                  hipStream_t stream);
@@ -814,10 +816,18 @@ static int check_fp8_block(const char* fn, int64_t M, int64_t N, int64_t K) {
   return W4_OK;
 }
 
+// A HIP launch takes fewer than 2^32 threads.
+static int check_threads(const char* fn, int64_t threads) {
+  if (threads >= ((int64_t)1 << 32))
+    return fail(W4_ERR_UNSUPPORTED, "%s: the output needs %lld threads, 2^32 or more", fn, (long long)threads);
+  return W4_OK;
+}
+
 int w4_fp8_block_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
   const char* fn = "w4_fp8_block_gemm_workspace_bytes";
   if (!bytes) return fail(W4_ERR_INVALID, "%s: null output pointer", fn);
   int rc = check_fp8_block(fn, M, N, K);
+  if (!rc) rc = check_threads(fn, w4::fp8_block_gemm_threads(M, N, K));
   if (rc) return rc;
   *bytes = w4::fp8_block_gemm_workspace(M, N, K);
   return ok();
@@ -830,6 +840,7 @@ int w4_fp8_block_gemm(const void* a, const float* a_scale, const void* w, const 
   const int dt = float_index(out_dtype);
   if (dt < 0) return fail(W4_ERR_DTYPE, "%s: output must be bf16, fp16 or fp32 (dtype code %d)", fn, out_dtype);
   int rc = check_fp8_block(fn, M, N, K);
+  if (!rc) rc = check_threads(fn, w4::fp8_block_gemm_threads(M, N, K));
   if (rc) return rc;
   if (M == 0 || N == 0) return ok();
   if (!a || !a_scale || !w || !w_scale || !out) return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
@@ -856,6 +867,8 @@ int w4_fp8_block_grouped_gemm(const void* a, const float* a_scale, const int32_t
   if (E < 0 || E > 65535 || T < 0)
     return fail(W4_ERR_INVALID, "%s: E=%lld T=%lld out of range", fn, (long long)E, (long long)T);
   if (R == 0 || N == 0 || E == 0) return ok();
+  rc = check_threads(fn, w4::fp8_block_grouped_threads(E, R, N));
+  if (rc) return rc;
   if (row_token && (T <= 0 || T * K >= ((int64_t)1 << 31)))
     return fail(W4_ERR_UNSUPPORTED, "%s: token count T=%lld out of range for K=%lld (T*K must be below 2^31)", fn,
                 (long long)T, (long long)K);

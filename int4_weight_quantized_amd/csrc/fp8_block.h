@@ -148,6 +148,11 @@ __device__ __forceinline__ void store_columns(const Fp8Args& p, float (&f)[C], i
   }
 }
 
+// Blocks of a grouped launch with BM x BN tiles.
+int64_t grouped_blocks(int64_t E, int64_t R, int64_t N, int64_t BM, int64_t BN);
+
 hipError_t launch_fp8_stream(const Fp8Args& p, int out_dt, hipStream_t stream);
+// Threads that it takes: dense (E = 0) or grouped.
+int64_t fp8_stream_threads(int64_t M, int64_t N, int64_t E, int64_t R);
 
 }  // namespace w4

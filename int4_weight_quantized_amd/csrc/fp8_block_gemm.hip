@@ -337,6 +337,17 @@ size_t fp8_block_gemm_workspace(int64_t M, int64_t N, int64_t K) {
   return pl.splits > 1 ? (size_t)pl.splits * (size_t)M * (size_t)N * 4 : 0;
 }
 
+// Threads of the largest launch of a product, for the host's check against a
+// launch's limit. (A dense product planned for 256 x 256 tiles takes 128 x 128
+// ones for fp32 outputs: more threads.)
+int64_t fp8_block_gemm_threads(int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || N == 0) return 0;
+  const DensePlan pl = plan_dense(M, N, K);
+  if (pl.tile == 0) return fp8_stream_threads(M, N, 0, 0);
+  const int64_t bm = pl.tile == 64 ? 64 : 128;
+  return (M + bm - 1) / bm * ((N + 127) / 128) * pl.splits * 256;
+}
+
 // f16: the fp32-exact products (fp32 results)
 template <int MI, int NJ, int WM, int WN>
 static hipError_t tile_go(Fp8Args p, bool f16, int out_dt, hipStream_t stream) {
@@ -345,8 +356,7 @@ static hipError_t tile_go(Fp8Args p, bool f16, int out_dt, hipStream_t stream) {
   const dim3 block(64 * WM * WN);
   auto go = [&](auto kernel, dim3 grid) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p); };
   if (p.offsets) {
-    const int64_t items = (p.R / BM + (p.E < p.R ? p.E : p.R)) * p.NT;
-    const dim3 grid((unsigned)((items + 7) / 8 * 8));
+    const dim3 grid((unsigned)grouped_blocks(p.E, p.R, p.N, BM, BN));
     if (out_dt == 0) go(fp8_tile_kernel<MI, NJ, WM, WN, true, false, 0>, grid);
     else go(fp8_tile_kernel<MI, NJ, WM, WN, true, false, 1>, grid);
   } else {
@@ -402,6 +412,32 @@ hipError_t launch_fp8_block_gemm(const void* a, const float* a_scale, const void
   return hipGetLastError();
 }
 
+// What the grouped product runs as: rows streamed (0), or the tile.
+static int plan_grouped(int64_t E, int64_t R, int64_t N) {
+  // by the average rows of an expert (64 experts of 2048 x 7168): 4 rows 157 us streamed, 159 in 128-row tiles; 8 rows
+  // 184 and 163; 96 rows 203 in 128-row tiles, 202 in 256-row ones; 128 rows 280 and 237
+  if (R <= 4 * E) return 0;
+  // few tiles: the smaller ones reach more CUs (4 experts, 2000 rows, 512 x 4096: 26 us, 52 in 256-row tiles; about 144
+  // tiles 38 and 56, about 160 109 and 98); 128 columns: 16384 rows 28 us, 52 in 256-wide tiles
+  const int64_t c256 = (N + 255) / 256, c128 = (N + 127) / 128;
+  if (R <= 96 * E || (R / 256 + E / 2) * c256 < 160 || !wide_pays(2 * c256, 4 * c128)) return 128;
+  return 256;
+}
+
+// Blocks of a grouped launch with BM x BN tiles: no segment's last tile is
+// shared, so at most one more than the full ones for each expert with rows;
+// a multiple of 8.
+int64_t grouped_blocks(int64_t E, int64_t R, int64_t N, int64_t BM, int64_t BN) {
+  return ((R / BM + (E < R ? E : R)) * ((N + BN - 1) / BN) + 7) / 8 * 8;
+}
+
+int64_t fp8_block_grouped_threads(int64_t E, int64_t R, int64_t N) {
+  if (R == 0 || N == 0 || E == 0) return 0;
+  const int tile = plan_grouped(E, R, N);
+  if (tile == 0) return fp8_stream_threads(0, N, E, R);
+  return grouped_blocks(E, R, N, tile, tile) * (tile == 128 ? 256 : 512);
+}
+
 hipError_t launch_fp8_block_grouped(const void* a, const float* a_scale, const int32_t* row_token,
                                     const int32_t* offsets, int64_t E, const void* w, const float* w_scale, void* out,
                                     int out_dt, int64_t T, int64_t R, int64_t N, int64_t K, hipStream_t stream) {
@@ -422,13 +458,9 @@ hipError_t launch_fp8_block_grouped(const void* a, const float* a_scale, const i
   p.KB = (int)((K + 127) / 128);
   p.NBLK = (int)((N + 127) / 128);
   p.splits = 1;
-  // by the average rows of an expert (64 experts of 2048 x 7168): 4 rows 157 us streamed, 159 in 128-row tiles; 8 rows
-  // 184 and 163; 96 rows 203 in 128-row tiles, 202 in 256-row ones; 128 rows 280 and 237
-  if (R <= 4 * E) return launch_fp8_stream(p, out_dt, stream);
-  // few tiles: the smaller ones reach more CUs (4 experts, 2000 rows, 512 x 4096: 26 us, 52 in 256-row tiles; about 144
-  // tiles 38 and 56, about 160 109 and 98); 128 columns: 16384 rows 28 us, 52 in 256-wide tiles
-  const int64_t c256 = (N + 255) / 256, c128 = (N + 127) / 128;
-  if (R <= 96 * E || (R / 256 + E / 2) * c256 < 160 || !wide_pays(2 * c256, 4 * c128)) return tile_go<4, 4, 2, 2>(p, false, out_dt, stream);
+  const int tile = plan_grouped(E, R, N);
+  if (tile == 0) return launch_fp8_stream(p, out_dt, stream);
+  if (tile == 128) return tile_go<4, 4, 2, 2>(p, false, out_dt, stream);
   return tile_go<8, 4, 2, 4>(p, false, out_dt, stream);
 }
 

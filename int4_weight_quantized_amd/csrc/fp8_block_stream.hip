@@ -121,8 +121,7 @@ static hipError_t stream_go(Fp8Args p, int out_dt, hipStream_t stream) {
   p.NT = (p.N + BN - 1) / BN;
   const dim3 block(64 * WS);
   if (p.offsets) {
-    const int64_t items = (p.R / BM + (p.E < p.R ? p.E : p.R)) * p.NT;
-    const dim3 grid((unsigned)((items + 7) / 8 * 8));
+    const dim3 grid((unsigned)grouped_blocks(p.E, p.R, p.N, BM, BN));
     if (out_dt == 0) hipLaunchKernelGGL((fp8_stream_kernel<MI, NJ, WS, U, true, false, 0>), grid, block, 0, stream, p);
     else hipLaunchKernelGGL((fp8_stream_kernel<MI, NJ, WS, U, true, false, 1>), grid, block, 0, stream, p);
   } else {
@@ -137,9 +136,16 @@ static hipError_t stream_go(Fp8Args p, int out_dt, hipStream_t stream) {
 // 32 columns a block; 16, with 16 waves along K, where the former would leave
 // CUs without a block (1 x 4096 x 14336: 11.4 us, 22.6 with 32 columns and 4
 // waves; 1 x 14336 x 4096: 11.8 us with the latter, 14.7 with the former).
+static bool narrow(bool grouped, int64_t N) { return !grouped && N < 32 * 256; }
+
 hipError_t launch_fp8_stream(const Fp8Args& p, int out_dt, hipStream_t stream) {
-  if (!p.offsets && p.N < 32 * 256) return stream_go<1, 1, 16, 2>(p, out_dt, stream);
+  if (narrow(p.offsets, p.N)) return stream_go<1, 1, 16, 2>(p, out_dt, stream);
   return stream_go<1, 2, 4, 2>(p, out_dt, stream);
+}
+
+int64_t fp8_stream_threads(int64_t M, int64_t N, int64_t E, int64_t R) {
+  if (E > 0) return grouped_blocks(E, R, N, 16, 32) * 256;
+  return (M + 15) / 16 * (narrow(false, N) ? (N + 15) / 16 * 1024 : (N + 31) / 32 * 256);
 }
 
 }  // namespace w4
