@@ -121,9 +121,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args p) {
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const uint32_t ldsw = __builtin_amdgcn_readfirstlane(lds0 + 8 * wave * kFK);
+  // m0 holds the LDS address. The compiler keeps nothing in it here, and a clobber of a reserved register is not honoured.
   auto dma = [&](const __amdgpu_buffer_rsrc_t rs, uint32_t dst, uint32_t off, uint32_t ks) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(dst), "v"(off), "s"(rs), "s"(ks) : "memory", "m0");
+                 :: "s"(dst), "v"(off), "s"(rs), "s"(ks) : "memory");
   };
   // the row of scales that this thread fetches
   const int64_t sspan = (GROUPED && p.row_token) ? p.M * p.KB : min((int64_t)BM, p.M - out0 - r0) * p.KB;
