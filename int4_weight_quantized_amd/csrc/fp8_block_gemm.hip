@@ -349,31 +349,33 @@ int64_t fp8_block_gemm_threads(int64_t M, int64_t N, int64_t K) {
   return (M + bm - 1) / bm * ((N + 127) / 128) * pl.splits * 256;
 }
 
-// f16: the fp32-exact products (fp32 results)
-template <int MI, int NJ, int WM, int WN>
-static hipError_t tile_go(Fp8Args p, bool f16, int out_dt, hipStream_t stream) {
-  constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN;
+template <int BM, int BN, int TH, typename F>
+static hipError_t grouped_go(Fp8Args p, F kernel, hipStream_t stream) {
   p.NT = (p.N + BN - 1) / BN;
-  const dim3 block(64 * WM * WN);
-  auto go = [&](auto kernel, dim3 grid) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p); };
-  if (p.offsets) {
-    const dim3 grid((unsigned)grouped_blocks(p.E, p.R, p.N, BM, BN));
-    if (out_dt == 0) go(fp8_tile_kernel<MI, NJ, WM, WN, true, false, 0>, grid);
-    else go(fp8_tile_kernel<MI, NJ, WM, WN, true, false, 1>, grid);
-  } else {
-    p.tiles = (p.M + BM - 1) / BM * p.NT;
-    const dim3 grid((unsigned)(p.tiles * p.splits));
-    if constexpr (MI * NJ <= 16) {
-      if (f16) {
-        go(fp8_tile_kernel<MI, NJ, WM, WN, false, true, 2>, grid);
-        return hipGetLastError();
-      }
-    }
-    if (out_dt == 0) go(fp8_tile_kernel<MI, NJ, WM, WN, false, false, 0>, grid);
-    else if (out_dt == 1) go(fp8_tile_kernel<MI, NJ, WM, WN, false, false, 1>, grid);
-    else go(fp8_tile_kernel<MI, NJ, WM, WN, false, false, 2>, grid);   // partial sums
-  }
+  const dim3 grid((unsigned)grouped_blocks(p.E, p.R, p.N, BM, BN)), block(TH);
+  hipLaunchKernelGGL(kernel, grid, block, 0, stream, p);
   return hipGetLastError();
+}
+
+template <int BM, int BN, int TH, typename F>
+static hipError_t dense_go(Fp8Args p, F kernel, hipStream_t stream) {
+  p.NT = (p.N + BN - 1) / BN;
+  p.tiles = (p.M + BM - 1) / BM * p.NT;
+  const dim3 grid((unsigned)(p.tiles * p.splits)), block(TH);
+  hipLaunchKernelGGL(kernel, grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
+// The tiles with K splits: fp32 outputs and partial sums among them.
+// f16: the fp32-exact products (fp32 results).
+template <int MI, int NJ>
+static hipError_t split_tile_go(const Fp8Args& p, bool f16, int out_dt, hipStream_t stream) {
+  constexpr int BM = 32 * MI, BN = 32 * NJ;
+  auto go = [&](auto kernel) { return dense_go<BM, BN, 256>(p, kernel, stream); };
+  if (f16) return go(fp8_tile_kernel<MI, NJ, 2, 2, false, true, 2>);
+  if (out_dt == 0) return go(fp8_tile_kernel<MI, NJ, 2, 2, false, false, 0>);
+  if (out_dt == 1) return go(fp8_tile_kernel<MI, NJ, 2, 2, false, false, 1>);
+  return go(fp8_tile_kernel<MI, NJ, 2, 2, false, false, 2>);   // partial sums
 }
 
 hipError_t launch_fp8_block_gemm(const void* a, const float* a_scale, const void* w, const float* w_scale,
@@ -401,9 +403,10 @@ hipError_t launch_fp8_block_gemm(const void* a, const float* a_scale, const void
   const int dt = p.splits > 1 ? 2 : out_dt;
   // (converting to fp16 in the 256 x 256 tile spills registers)
   hipError_t e;
-  if (pl.tile == 64) e = tile_go<2, 4, 2, 2>(part, out_dt == 2, dt, stream);
-  else if (pl.tile == 128 || out_dt == 2) e = tile_go<4, 4, 2, 2>(part, out_dt == 2, dt, stream);
-  else e = tile_go<8, 4, 2, 4>(part, false, dt, stream);
+  if (pl.tile == 64) e = split_tile_go<2, 4>(part, out_dt == 2, dt, stream);
+  else if (pl.tile == 128 || out_dt == 2) e = split_tile_go<4, 4>(part, out_dt == 2, dt, stream);
+  else if (dt == 0) e = dense_go<256, 256, 512>(part, fp8_tile_kernel<8, 4, 2, 4, false, false, 0>, stream);
+  else e = dense_go<256, 256, 512>(part, fp8_tile_kernel<8, 4, 2, 4, false, false, 1>, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   const dim3 grid((unsigned)((M * (N / 8) + 255) / 256)), block(256);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p, static_cast<const float*>(ws)); };
@@ -461,8 +464,11 @@ hipError_t launch_fp8_block_grouped(const void* a, const float* a_scale, const i
   p.splits = 1;
   const int tile = plan_grouped(E, R, N);
   if (tile == 0) return launch_fp8_stream(p, out_dt, stream);
-  if (tile == 128) return tile_go<4, 4, 2, 2>(p, false, out_dt, stream);
-  return tile_go<8, 4, 2, 4>(p, false, out_dt, stream);
+  if (tile == 128)
+    return out_dt == 0 ? grouped_go<128, 128, 256>(p, fp8_tile_kernel<4, 4, 2, 2, true, false, 0>, stream)
+                       : grouped_go<128, 128, 256>(p, fp8_tile_kernel<4, 4, 2, 2, true, false, 1>, stream);
+  return out_dt == 0 ? grouped_go<256, 256, 512>(p, fp8_tile_kernel<8, 4, 2, 4, true, false, 0>, stream)
+                     : grouped_go<256, 256, 512>(p, fp8_tile_kernel<8, 4, 2, 4, true, false, 1>, stream);
 }
 
 }  // namespace w4

@@ -24,8 +24,9 @@ def compiled():
     flags = [f for f in B.HIPCC_FLAGS if f != "-shared"]
     res = subprocess.run([hipcc, *flags, "--cuda-device-only", "-S", "-o", "-", SOURCE], capture_output=True, text=True)
     assert res.returncode == 0, res.stderr
+    kernels = re.findall(r"\.amdhsa_kernel (\S+)", res.stdout)
     code = [re.sub(r"\s*[;/]+.*", "", line).strip() for line in res.stdout.split("\n")]
-    return [c for c in code if c and not c.startswith(".")], res.stderr
+    return [c for c in code if c and not c.startswith(".")], res.stderr, kernels
 
 
 def scalar_registers(text):
@@ -66,3 +67,17 @@ def test_dma_statements(compiled):
             nop = re.match(r"s_nop (\d+)", code[j])
             wait += int(nop[1]) + 1 if nop else not code[j].endswith(":")
             j -= 1
+
+
+def test_instances(compiled):
+    """Every tile kernel that is built is one that a call reaches: (rows and columns of 16 a wave, waves, grouped,
+    fp16 operands, output type)."""
+    built = set()
+    for name in compiled[2]:
+        m = re.search(r"fp8_tile_kernelILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELb(\d)ELb(\d)ELi(\d)E", name)
+        if m:
+            built.add(tuple(int(v) for v in m.groups()))
+    small = {(mi, 4, 2, 2, 0, f16, out) for mi in (2, 4) for f16, out in ((0, 0), (0, 1), (0, 2), (1, 2))}
+    large = {(8, 4, 2, 4, 0, 0, out) for out in (0, 1)}
+    grouped = {(mi, 4, 2, wn, 1, 0, out) for mi, wn in ((4, 2), (8, 4)) for out in (0, 1)}
+    assert built == small | large | grouped
