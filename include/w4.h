@@ -301,8 +301,11 @@ int w4a16_gemm(const void* x, const void* w_tiled, const void* sz_tiled, int64_t
  *   a           device, E4M3 codes [T, K] (from w4a8_quantize_act)
  *   a_scale     device, fp32 [T]
  *   a_group_sums device, fp32 [T, K/group] (from w4a8_quantize_act, same group)
- *   row_token   device, int32 [R], each in [0, T)
- *   expert_offsets device, int32 [E+1], non-decreasing, [0] = 0, [E] = R
+ *   row_token   device, int32 [R], each before expert_offsets[E] in [0, T);
+ *               those past it are not read
+ *   expert_offsets device, int32 [E+1], non-decreasing, [0] = 0, [E] <= R:
+ *               output rows at or past expert_offsets[E] are not written (a
+ *               plan of w4_route with tokens that have no expert)
  *   w_tiled     device, E tiled matrices (w4_repack with batch = E)
  *   w_scale     device, fp16 [E, G, N]
  *   group       128, 256 or 512, dividing K
@@ -530,6 +533,8 @@ int w4_probe_mfma(int kind, int64_t iters, int32_t* sink, int64_t sink_elems, do
  *   workspace device, w4_route_workspace_bytes (16-byte aligned; may be NULL
  *             when that is 0), owned by the caller; calls sharing one must
  *             not overlap. Nothing in it needs to start at zero.
+ * The plan is that of w4_fp8_block_grouped_gemm and of w4a8_grouped_gemm (R =
+ * T * topk).
  * Results do not depend on timing. T == 0 writes expert_offsets only.
  * Errors: INVALID, ALIGN, GROUP, DTYPE, UNSUPPORTED (T, E, topk, group_top,
  *         T*topk >= 2^31), HIP.

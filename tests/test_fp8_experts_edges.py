@@ -1,13 +1,16 @@
 """GPU tests of the FP8 expert path's edges: infinities and NaN on their way
-through the quantizer and the products, and sizes past one launch's threads."""
+through the quantizer and the products, sizes past one launch's threads, and
+the router's plan in the int4 experts' product."""
 import numpy as np
 import pytest
 import torch
 
 from int4_weight_quantized_amd import ops
+from int4_weight_quantized_amd import workloads as W
 from oracle import fp8_experts as O
-from oracle.w4_oracle import e4m3_decode
-from test_fp8_experts import DEV, DT, fp8_inputs, gpu, rng_for, say
+from oracle.w4_oracle import bf16_bits_to_f32, e4m3_decode, grouped_fp8_reference, quantize_act_fp8
+from test_fp8_experts import DEV, DT, U, check, fp8_inputs, gpu, half_step, rng_for, say
+from test_gpu_parity import assert_close, to_f64
 
 pytestmark = pytest.mark.gpu
 
@@ -149,3 +152,35 @@ def test_route_most_tokens():
     tokens = torch.arange(T, dtype=torch.int32, device=DEV)
     assert torch.equal(row_token[:n0], tokens[~second]) and torch.equal(row_token[n0:], tokens[second])
     assert torch.equal(row_token[row_of.long()], tokens)
+
+
+# ------------------------------------------------------------------ the plan and the int4 experts
+
+@pytest.mark.parametrize("E,K,N,group,T,topk", [(8, 256, 136, 128, 300, 3), (5, 512, 72, 256, 7, 2), (3, 128, 64, 128, 1, 2)])
+def test_route_feeds_int4_experts(E, K, N, group, T, topk):
+    """route -> quantize per token -> w4a8_grouped_gemm -> combine, with tokens that have no expert, or fewer than
+    topk: their plan ends before R, the product leaves the rows past its end as they are, and combine reads none."""
+    say("int4 experts", E, K, N, group, T, topk)
+    d = W.moe_inputs(E, K, N, group, T, topk, seed=E + T)
+    x = torch.from_numpy(d["x"].view(np.int16)).view(torch.bfloat16).to(DEV)
+    r = rng_for(E, K, T)
+    logits = r.standard_normal((T, E)).astype(np.float32)
+    logits[T // 2] = -np.inf
+    logits[T // 3, 1:] = -np.inf
+    ids, weights, row_token, off, row_of = ops.w4_route(gpu(logits), topk, score="sigmoid")
+    n, R = int(off[-1]), T * topk
+    assert n < R and int(row_token[n:].max()) == -1
+    a8, s, gs = ops.w4a8_quantize_act(x, "fp8", group)
+    wt = ops.w4_repack(torch.from_numpy(d["w"]).to(DEV), ops.W4_LAYOUT_CT_NK, K, N, batch=E)
+    out = torch.full((R, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    ops.w4a8_grouped_gemm(a8, s, gs, row_token, off, wt, gpu(d["scales"]), group, N, out=out)
+    torch.cuda.synchronize()
+    assert (out[n:] == 7).all()
+    want_ids, _ = O.route(logits, topk, score="sigmoid")
+    plan = O.plan(want_ids, E)
+    rc, rs = quantize_act_fp8(bf16_bits_to_f32(d["x"]))
+    assert_close(to_f64(out[:n]), grouped_fp8_reference(rc, rs, *plan[:2], d["w"], d["scales"], group), "int4 experts")
+    y = ops.w4_combine(out, row_of, weights)
+    want, mag = O.combine(out.double().cpu().numpy(), plan[2], weights.cpu().numpy())
+    check(y, want, half_step(want, "bf16") * (1 + 1e-6) + (topk + 2) * U * mag, "combine")
+    assert not y[T // 2].any()
