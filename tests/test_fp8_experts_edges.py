@@ -1,6 +1,7 @@
 """GPU tests of the FP8 expert path's edges: infinities and NaN on their way
 through the quantizer and the products, sizes past one launch's threads, and
-the router's plan in the int4 experts' product."""
+the router's plan in the int4 experts' product, and routing by one wave per
+token."""
 import numpy as np
 import pytest
 import torch
@@ -9,7 +10,7 @@ from int4_weight_quantized_amd import ops
 from int4_weight_quantized_amd import workloads as W
 from oracle import fp8_experts as O
 from oracle.w4_oracle import bf16_bits_to_f32, e4m3_decode, grouped_fp8_reference, quantize_act_fp8
-from test_fp8_experts import DEV, DT, U, check, fp8_inputs, gpu, half_step, rng_for, say
+from test_fp8_experts import DEV, DT, U, check, check_route, fp8_inputs, gpu, half_step, rng_for, say
 from test_gpu_parity import assert_close, to_f64
 
 pytestmark = pytest.mark.gpu
@@ -184,3 +185,56 @@ def test_route_feeds_int4_experts(E, K, N, group, T, topk):
     want, mag = O.combine(out.double().cpu().numpy(), plan[2], weights.cpu().numpy())
     check(y, want, half_step(want, "bf16") * (1 + 1e-6) + (topk + 2) * U * mag, "combine")
     assert not y[T // 2].any()
+
+
+# ------------------------------------------------------------------ routing by one wave per token
+
+# more than 256 experts, or groups that do not fall on whole lanes of 16
+WAVE = [(384, 8, {}), (512, 10, dict(renorm=False)), (512, 64, dict(score="sigmoid", scale=2.5)), (1024, 64, {}),
+        (1000, 7, dict(score="sigmoid", renorm=False)), (300, 6, dict(bias=True)), (512, 5, dict(bias=True, score="sigmoid")),
+        (1024, 9, dict(bias=True)), (72, 5, dict(n_groups=3, topk_groups=2, group_top=2)),
+        (60, 4, dict(n_groups=4, topk_groups=2, group_top=1, bias=True, score="sigmoid")),
+        (300, 5, dict(n_groups=3, topk_groups=2, group_top=2, bias=True)),
+        (1024, 8, dict(n_groups=64, topk_groups=7, group_top=2, score="sigmoid"))]
+
+
+@pytest.mark.parametrize("E,topk,kw", WAVE)
+@pytest.mark.parametrize("T", [1, 63, 130])
+def test_route_wave(E, topk, kw, T):
+    kw = dict(kw)
+    r = rng_for(T, E, topk, 8)
+    x = r.standard_normal((T, E)) * 2
+    bias = (r.standard_normal(E) * 0.1).astype(np.float32) if kw.pop("bias", False) else None
+    check_route(gpu(x, DT[("f32", "bf16", "f16")[(T + E) % 3]]), topk, bias=bias, **kw)
+
+
+# 16 lanes per token, for the same masks
+LANES = [(64, 5, dict(score="sigmoid", bias=True)), (40, 6, dict(n_groups=5, topk_groups=3, group_top=2, bias=True)),
+         (256, 8, dict(score="sigmoid", n_groups=8, topk_groups=4, group_top=2, bias=True, scale=2.5)), (16, 16, {})]
+
+
+@pytest.mark.parametrize("E,topk,kw", WAVE + LANES)
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_route_masks_ties_and_bias_ends(E, topk, kw, dt):
+    """Ties everywhere, closed experts, rows with less than topk open, the type's ends, NaN, equal groups; a bias that
+    closes experts, ties others and is infinite."""
+    kw = dict(kw)
+    r = rng_for(E, topk, len(dt))
+    T = 130
+    x = r.integers(-3, 4, (T, E)).astype(np.float64)
+    x[r.random((T, E)) < 0.3] = -np.inf
+    x[3] = -np.inf
+    x[4] = np.nan
+    x[5] = torch.finfo(DT[dt]).min
+    x[6, 1:] = -np.inf
+    x[7, :4] = np.inf
+    x[8] = np.where(np.arange(E) % 2, np.nan, 1.0)
+    x[9] = torch.finfo(DT[dt]).min
+    x[9, E // 2] = torch.finfo(DT[dt]).max
+    x[10, :E - 2] = -np.inf                                      # the last group alone, and short
+    x[64:128] = 1.0
+    bias = None
+    if kw.pop("bias", False):
+        bias = (r.integers(-2, 3, E) * 0.125).astype(np.float32)
+        bias[2], bias[5], bias[E - 3] = -np.inf, np.nan, np.inf
+    check_route(gpu(x, DT[dt]), topk, bias=bias, **kw)
