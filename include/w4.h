@@ -582,7 +582,8 @@ int w4_fp8_block_quantize(const void* x, int x_dtype, int64_t M, int64_t K, int6
  *   workspace device, w4_fp8_block_gemm_workspace_bytes (16-byte aligned;
  *            may be NULL when that is 0): fp32 partial tiles where few rows
  *            make the product split K, summed in a fixed order (results are
- *            reproducible). Calls sharing one must not overlap.
+ *            reproducible). The size does not grow with M throughout: ask
+ *            for each M. Calls sharing one must not overlap.
  * Errors: INVALID, ALIGN, DTYPE, UNSUPPORTED (also 2^24 output tiles and
  *         more: 128 x 128, 64 x 128 up to 64 rows, 16 x 32 up to 16 rows),
  *         HIP. M == 0 or N == 0 enqueues nothing.
@@ -599,7 +600,8 @@ int w4_fp8_block_gemm(const void* a, const float* a_scale, const void* w, const 
  * matrix e.
  *   a        device, E4M3 [T, K];  a_scale: device, fp32 [T, ceil(K / 128)]
  *   row_token       device, int32 [R], or NULL (then T == R); a row whose
- *            token lies outside [0, T) gives zeros
+ *            token lies outside [0, T) counts as a row of zeros (with a
+ *            scale of 0)
  *   expert_offsets  device, int32 [E + 1], non-decreasing, from 0 to at most
  *            R; output rows at or past expert_offsets[E] are not written
  *   w        device, E4M3 [E, N, K];  w_scale: device, fp32

@@ -1,7 +1,7 @@
 """GPU tests of the FP8 expert path's edges: infinities and NaN on their way
 through the quantizer and the products, sizes past one launch's threads, and
-the router's plan in the int4 experts' product, and routing by one wave per
-token."""
+the router's plan in the int4 experts' product, routing by one wave per token,
+and the precision of the products' sums."""
 import numpy as np
 import pytest
 import torch
@@ -238,3 +238,115 @@ def test_route_masks_ties_and_bias_ends(E, topk, kw, dt):
         bias = (r.integers(-2, 3, E) * 0.125).astype(np.float32)
         bias[2], bias[5], bias[E - 3] = -np.inf, np.nan, np.inf
     check_route(gpu(x, DT[dt]), topk, bias=bias, **kw)
+
+
+# ------------------------------------------------------------------ the precision of the products' sums
+
+def small_ints(shape, g):
+    """E4M3 codes of whole numbers from -8 to 16."""
+    return torch.randint(-8, 17, shape, device=DEV, generator=g).float().to(torch.float8_e4m3fn)
+
+
+def halves(shape, g, unit):
+    """Scales of 1/2 and 1 units (a power of two)."""
+    return torch.randint(1, 3, shape, device=DEV, generator=g).float() * (unit / 2)
+
+
+def exact_product(a, sa, w, sw):
+    """The product in float64, where it is exact."""
+    K, N = a.shape[1], w.shape[0]
+    a = a.float() * sa.repeat_interleave(128, 1)[:, :K]
+    w = w.float() * sw.repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    return a.double() @ w.double().t()
+
+
+def assert_rounded(got, y):
+    """The output is the exact value, rounded once: every partial sum is a multiple of a quarter unit below 2^24 of them."""
+    assert torch.equal(y, y.float().double())
+    bad = got != y.float().to(got.dtype)
+    assert not bad.any(), (int(bad.sum()), bad.numel())
+
+
+PRODUCTS = [(1, 4104, 4096), (12, 8200, 2064), (40, 520, 4112), (64, 2056, 528), (200, 512, 14336), (700, 1032, 528),
+            (2305, 6152, 1152)]
+
+
+@pytest.mark.parametrize("M,N,K", PRODUCTS)
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_block_gemm_exact(M, N, K, dt):
+    """Whole numbers and scales of powers of two: no sum on the way may round, in whatever order or unit it is formed
+    (streamed, 64-, 128- and 256-row tiles, K splits), so each output is off by its own rounding alone."""
+    say("gemm exact", M, N, K, dt)
+    g = torch.Generator(DEV).manual_seed(M + N + K)
+    KB, NB = -(-K // 128), -(-N // 128)
+    unit = 2.0 ** -8 if dt == "f16" else 1.0                     # within fp16's range
+    a, w = small_ints((M, K), g), small_ints((N, K), g)
+    sa, sw = halves((M, KB), g, 1.0), halves((NB, KB), g, unit)
+    bias = torch.randint(-16, 17, (N,), device=DEV, generator=g).float() * unit
+    got = ops.w4_fp8_block_gemm(a, sa, w, sw, bias=bias.to(DT[dt]), out_dtype=DT[dt])
+    assert_rounded(got, exact_product(a, sa, w, sw) + bias.double())
+
+
+COUNTS = [[1, 0, 3, 16, 4, 2, 0, 6], [40, 0, 129, 1, 300], [700, 513, 0, 256, 31, 1100, 1, 120]]
+
+
+@pytest.mark.parametrize("counts", COUNTS)
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_grouped_gemm_exact(counts, gather, dt):
+    """The same over segments: streamed, and tiles of 128 and 256 rows."""
+    say("grouped exact", counts, gather, dt)
+    E, R, N, K = len(counts), sum(counts), 3720, 1168
+    g = torch.Generator(DEV).manual_seed(R)
+    T = 77 if gather else R
+    KB, NB = -(-K // 128), -(-N // 128)
+    a, w = small_ints((T, K), g), small_ints((E, N, K), g)
+    sa, sw = halves((T, KB), g, 1.0), halves((E, NB, KB), g, 2.0 ** -8 if dt == "f16" else 1.0)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rt = torch.randint(0, T, (R,), device=DEV, generator=g, dtype=torch.int32) if gather else None
+    got = ops.w4_fp8_block_grouped_gemm(a, sa, rt, gpu(off), w, sw, out_dtype=DT[dt])
+    for e in range(E):
+        rows = slice(int(off[e]), int(off[e + 1]))
+        pick = rt[rows].long() if gather else rows
+        assert_rounded(got[rows], exact_product(a[pick], sa[pick], w[e], sw[e]))
+
+
+def normal_codes(shape, g):
+    return (torch.randn(shape, device=DEV, generator=g) * 110).clamp_(-448, 448).to(torch.float8_e4m3fn)
+
+
+def assert_close_sums(got, y):
+    """fp16 outputs of normal data: beside the output's own rounding, the sums are off by no more than 2e-5 (rms, of the
+    result's rms), where the matrix unit's grid costs about 1e-5."""
+    rms = y.pow(2).mean()
+    own = (y.to(torch.float16).double() - y).pow(2).mean() / rms
+    err = (got.double() - y).pow(2).mean() / rms
+    assert err - own <= 2e-5 ** 2, (err.sqrt().item(), own.sqrt().item())
+
+
+@pytest.mark.parametrize("M,N,K", PRODUCTS)
+def test_block_gemm_normal_data(M, N, K):
+    g = torch.Generator(DEV).manual_seed(M + N + K)
+    a, w = normal_codes((M, K), g), normal_codes((N, K), g)
+    sa = torch.rand((M, -(-K // 128)), device=DEV, generator=g) * 0.006 + 0.003
+    sw = torch.rand((-(-N // 128), -(-K // 128)), device=DEV, generator=g) * 2e-4 + 1e-4
+    got = ops.w4_fp8_block_gemm(a, sa, w, sw, out_dtype=torch.float16)
+    assert_close_sums(got, exact_product(a, sa, w, sw))
+    again = ops.w4_fp8_block_gemm(a, sa, w, sw, out=torch.full_like(got, 7.0))
+    assert torch.equal(again.view(torch.int16), got.view(torch.int16))   # no order left to timing
+
+
+@pytest.mark.parametrize("counts", COUNTS)
+def test_grouped_gemm_normal_data(counts):
+    E, R, N, K = len(counts), sum(counts), 3720, 1168
+    g = torch.Generator(DEV).manual_seed(R + 1)
+    KB, NB = -(-K // 128), -(-N // 128)
+    a, w = normal_codes((R, K), g), normal_codes((E, N, K), g)
+    sa = torch.rand((R, KB), device=DEV, generator=g) * 0.006 + 0.003
+    sw = torch.rand((E, NB, KB), device=DEV, generator=g) * 2e-4 + 1e-4
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    got = ops.w4_fp8_block_grouped_gemm(a, sa, None, gpu(off), w, sw, out_dtype=torch.float16)
+    y = torch.cat([exact_product(a[off[e]:off[e + 1]], sa[off[e]:off[e + 1]], w[e], sw[e]) for e in range(E)])
+    assert_close_sums(got, y)
+    again = ops.w4_fp8_block_grouped_gemm(a, sa, None, gpu(off), w, sw, out=torch.full_like(got, 7.0))
+    assert torch.equal(again.view(torch.int16), got.view(torch.int16))
