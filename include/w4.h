@@ -516,8 +516,8 @@ int w4_probe_mfma(int kind, int64_t iters, int32_t* sink, int64_t sink_elems, do
  *   ids: the topk open experts of largest x (without bias) or c (with bias),
  *       in falling order; among equals (also of groups) the lowest index
  *       first; -1 where no open expert is left
- *   weights: s of the chosen, divided by their sum if renorm, times scale; 0
- *       at an id of -1. Rounded to fp32 once.
+ *   weights: s of the chosen, divided by their sum (by 1e-300 where that is
+ *       less) if renorm, times scale; 0 at an id of -1. Rounded to fp32 once.
  * Plan: the chosen (token, slot) pairs ordered by expert, then token.
  *   logits    device, [T, E] with row stride ld >= E; bf16, fp16 or fp32
  *   bias      device or NULL, fp32 [E]: moves the choice, not the weights

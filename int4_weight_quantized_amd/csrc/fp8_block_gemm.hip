@@ -34,9 +34,13 @@
 // - 256 x 256 with 8 waves is the largest tile whose accumulators (128
 //   registers a lane: vector FMAs cannot reach the other 256) leave room; it
 //   reads 3/4 of the LDS bytes per MFMA of a 64 x 64 wave tile.
-// 4096 x 14336 x 4096, bf16 out: 241 us, 2.0 PFLOP/s, the matrix units 45% busy
-// at the 2.0 GHz the power limit leaves; 65536 rows of 64 experts, 2048 x 7168:
-// 1.0 ms, 1.9 PFLOP/s. Without FMAs 5% less time, without DMA 16%.
+// 4096 x 14336 x 4096, bf16 out: 240 to 252 us, 1.9 to 2.0 PFLOP/s, the matrix
+// units 45% busy at the 2.0 GHz the power limit leaves; 65536 rows of 64
+// experts, 2048 x 7168: 1.00 to 1.05 ms, 1.8 to 1.9 PFLOP/s. From K = 1024 to
+// 8192 the time grows by 6.8 us per K step, of which the matrix units need 4.1
+// (four rounds of tiles), over 31 us for the tiles' first loads and stores.
+// Without FMAs 5% less time, without DMA 16%. With fp32 output (128 x 128
+// tiles, fp16 operands) 464 us, 1.04 PFLOP/s.
 #include "fp8_block.h"
 
 namespace w4 {

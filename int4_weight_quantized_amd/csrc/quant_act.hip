@@ -323,8 +323,9 @@ __global__ __launch_bounds__(kQThreads) void quant_act_asym_kernel(const uint16_
 // finite columns' codes are 0. Either way the product's row is NaN. A block
 // of zeros has scale 0 and codes 0.
 //
-// HBM-bound: 2 bytes in (4 with the gate) + 1 byte out per element + 4 per
-// block.
+// HBM-bound without the gate: 2 bytes in (4 with it) + 1 byte out per element
+// + 4 per block. 8192 x 14336 74 us (4.8 TB/s), 65536 x 2048 84; gated, where
+// each element takes an exponential and a full division, 180 to 186 us (3.6 TB/s).
 constexpr int kBQUnits = kQThreads / 16;             // 128-blocks per pass of a thread block
 
 template <bool BF16, bool SWIGLU>

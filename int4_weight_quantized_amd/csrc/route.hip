@@ -16,10 +16,13 @@
 // consecutive experts: the argmax rounds exchange within a row of 16 lanes,
 // by DPP, and all 64 tokens of a block go through at once. More experts, and
 // groups that do not fall on whole lanes, take one wave per token, expert
-// j * 64 + lane in register j. 16384 tokens of 256 experts in 8 groups take 35
-// us: 256 blocks run through once, 9 us of it their latency, 10 the fp64
-// scores (own exponentials over several experts at a time spilled and gained
-// nothing), 8 the argmax rounds, 7 the plan. 8192 of 64 experts take 12.5.
+// j * 64 + lane in register j. 16384 tokens of 256 experts in 8 groups take 32
+// us (26 and, for the plan's kernel, 7): 256 blocks run through once, about 8
+// us of it their latency, 10 the fp64 scores (own exponentials over several
+// experts at a time spilled and gained nothing), 8 the argmax rounds. 8192 of
+// 64 experts take 11.2. One wave per token: 16384 of 512 experts 54 us, of 1024
+// 72; with a bias and sigmoid scores 384 experts 68 us, 1024 124 (its 16 keys
+// in fp64 spill 69 registers).
 // A block takes kTok = 64 tokens, so that a token is one bit of a 64-bit mask
 // per expert: the rank of (token, expert) inside the block is the number of
 // lower bits set, which needs no sort and no order of atomics. One block does

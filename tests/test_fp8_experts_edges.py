@@ -195,7 +195,8 @@ WAVE = [(384, 8, {}), (512, 10, dict(renorm=False)), (512, 64, dict(score="sigmo
         (1024, 9, dict(bias=True)), (72, 5, dict(n_groups=3, topk_groups=2, group_top=2)),
         (60, 4, dict(n_groups=4, topk_groups=2, group_top=1, bias=True, score="sigmoid")),
         (300, 5, dict(n_groups=3, topk_groups=2, group_top=2, bias=True)),
-        (1024, 8, dict(n_groups=64, topk_groups=7, group_top=2, score="sigmoid"))]
+        (1024, 8, dict(n_groups=64, topk_groups=7, group_top=2, score="sigmoid")),
+        (1024, 64, dict(n_groups=2, topk_groups=2, group_top=1, bias=True))]
 
 
 @pytest.mark.parametrize("E,topk,kw", WAVE)
