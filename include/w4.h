@@ -633,6 +633,102 @@ int w4_fp8_block_grouped_gemm(const void* a, const float* a_scale, const int32_t
 int w4_combine(const void* y, int dtype, const int32_t* row_of, const float* weights, const void* add, void* out,
                int64_t T, int64_t R, int64_t topk, int64_t N, void* stream);
 
+/*
+ * MXFP4: 4-bit floating-point elements (E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) with one power of two (E8M0: 2^(code - 127), 255 is NaN) per
+ * 32 of them along K, the OCP Microscaling format. A [M, K] matrix is
+ *   codes   uint8 [M, K / 2], the lower column in the low nibble
+ *   scales  uint8 [M, 4 * ceil(K / 128)]: byte b is the scale of columns 32 b ..
+ *           32 b + 31; the bytes from K / 32 to the row's end are padding, which
+ *           the quantizer writes as 0 and nothing else reads
+ * K a multiple of 32. Where K is a multiple of 128 that is the plain [M, K / 32]
+ * of a checkpoint.
+ */
+
+/*
+ * Quantization to MXFP4. Per block of 32 columns, in fp32:
+ *   v = x, or with W4_ACT_SWIGLU x[:, k] * sigmoid(x[:, k]) * x[:, K + k]
+ *   scale = 2^max(floor(log2 max |v|) - 2, -127);  element = E2M1(v / scale),
+ *   nearest even, saturating at 6 (the largest lies in [4, 8))
+ * A block of zeros has the scale code 0 and codes 0 (or -0). A block with a NaN
+ * or an infinity in it has the scale NaN and codes 0, so that the products' row
+ * is NaN.
+ *   x       device, [M, K] ([M, 2K] with W4_ACT_SWIGLU), row stride ldx; bf16,
+ *           fp16 (ldx a multiple of 8) or fp32 (of 4), 16-byte aligned
+ *   codes   16-byte aligned;  scales: 4-byte aligned
+ * Errors: INVALID, ALIGN (K % 32, ldx, pointers), DTYPE, UNSUPPORTED, HIP.
+ * M == 0 or K == 0 enqueues nothing.
+ */
+int w4_mxfp4_quantize(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, int act, void* codes, void* scales,
+                      void* stream);
+
+/*
+ * The values that MXFP4 codes stand for: out = element * scale, NaN for a whole
+ * block whose scale is NaN. Exact in bf16 and fp32 (beyond the largest value:
+ * infinity); fp16 rounds to nearest even.
+ *   codes, out  16-byte aligned;  scales: 4-byte aligned;  out: [M, K]
+ * Errors: INVALID, ALIGN, DTYPE, UNSUPPORTED, HIP.
+ */
+int w4_mxfp4_dequantize(const void* codes, const void* scales, int64_t M, int64_t K, void* out, int out_dtype,
+                        void* stream);
+
+/*
+ * MXFP4 matrix product:
+ *   out[m, n] = sum_b 2^(ea[m, b] + ew[n, b]) * sum_{k in b} a[m, k] * w[n, k]  (+ bias[n])
+ * over the blocks b of 32 columns, the sums in fp32, rounded once to the output
+ * type.
+ *   a, a_scale  device, [M, K] as above;  w, w_scale: [N, K]
+ *   bias     device or NULL, [N] in the output type
+ *   out      device, [M, N] in out_dtype: bf16, fp16 or fp32
+ *   a, w and out must be 16-byte aligned, the scales 4-byte; N a multiple of 8, K
+ *   of 32 and at most 2^22.
+ *   workspace device, w4_mxfp4_gemm_workspace_bytes (16-byte aligned; may be
+ *            NULL when that is 0): fp32 partial tiles where few rows make the
+ *            product split K, summed in a fixed order (results are
+ *            reproducible). The size does not grow with M throughout: ask for
+ *            each M. Calls sharing one must not overlap.
+ * Errors: INVALID, ALIGN, DTYPE, UNSUPPORTED (also outputs that need 2^32 threads
+ *         or more), HIP. M == 0 or N == 0 enqueues nothing.
+ */
+int w4_mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int w4_mxfp4_gemm(const void* a, const void* a_scale, const void* w, const void* w_scale, const void* bias, void* out,
+                  int out_dtype, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The linear layer on MXFP4 weights, activations quantized within: the same as
+ * w4_mxfp4_quantize (without an activation) and w4_mxfp4_gemm with the output in
+ * the activations' type. Up to 16 rows are quantized by the product itself, in
+ * one launch.
+ *   x        device, [M, K] contiguous, bf16 or fp16, 16-byte aligned
+ *   workspace device, w4_mxfp4_linear_workspace_bytes (16-byte aligned; may be
+ *            NULL when that is 0), owned by the caller: codes, scales and the
+ *            product's own. Calls sharing one must not overlap.
+ *   other arguments and errors as w4_mxfp4_gemm.
+ */
+int w4_mxfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int w4_mxfp4_linear(const void* x, int x_dtype, const void* w, const void* w_scale, const void* bias, void* out,
+                    int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The product over the row segments of E experts (as w4_fp8_block_grouped_gemm):
+ * output row r of expert e's segment (expert_offsets[e] <= r <
+ * expert_offsets[e + 1]) takes activation row t = row_token[r] (t = r when
+ * row_token is NULL) and weight matrix e.
+ *   a, a_scale  device, [T, K];  w, w_scale: [E, N, K]
+ *   row_token       device, int32 [R], or NULL (then T == R); a row whose
+ *            token lies outside [0, T) counts as a row of zeros
+ *   expert_offsets  device, int32 [E + 1], non-decreasing, from 0 to at most
+ *            R; output rows at or past expert_offsets[E] are not written
+ *   out      device, [R, N] in out_dtype (bf16 or fp16)
+ *   alignments as w4_mxfp4_gemm
+ * Errors: INVALID, ALIGN, DTYPE, UNSUPPORTED (T*K >= 2^32 with row_token;
+ *         outputs that need 2^32 threads or more), HIP. Decreasing offsets are
+ *         undefined behaviour.
+ */
+int w4_mxfp4_grouped_gemm(const void* a, const void* a_scale, const int32_t* row_token, const int32_t* expert_offsets,
+                          int64_t E, const void* w, const void* w_scale, void* out, int out_dtype, int64_t T, int64_t R,
+                          int64_t N, int64_t K, void* stream);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* w4_last_error(void);
 

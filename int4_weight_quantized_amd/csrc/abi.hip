@@ -68,6 +68,21 @@ hipError_t launch_fp8_block_gemm(const void* a, const float* a_scale, const void
 hipError_t launch_fp8_block_grouped(const void* a, const float* a_scale, const int32_t* row_token,
                                     const int32_t* offsets, int64_t E, const void* w, const float* w_scale, void* out,
                                     int out_dt, int64_t T, int64_t R, int64_t N, int64_t K, hipStream_t stream);
+hipError_t launch_mx_quant(const void* x, int dt, bool swiglu, int64_t M, int64_t K, int64_t ldx, void* codes,
+                           void* scales, hipStream_t stream);
+hipError_t launch_mx_dequant(const void* codes, const void* scales, int64_t M, int64_t K, void* out, int dt,
+                             hipStream_t stream);
+size_t mx_gemm_workspace(int64_t M, int64_t N, int64_t K);
+int64_t mx_gemm_threads(int64_t M, int64_t N, int64_t K);
+int64_t mx_grouped_threads(int64_t E, int64_t R, int64_t N);
+bool mx_streams(int64_t M);
+hipError_t launch_mx_gemm(const void* a, const void* a_scale, const void* w, const void* w_scale, const void* bias,
+                          void* out, int out_dt, int64_t M, int64_t N, int64_t K, void* ws, hipStream_t stream);
+hipError_t launch_mx_linear_few(const void* x, bool bf16, const void* w, const void* w_scale, const void* bias, void* out,
+                                int64_t M, int64_t N, int64_t K, hipStream_t stream);
+hipError_t launch_mx_grouped(const void* a, const void* a_scale, const int32_t* row_token, const int32_t* offsets,
+                             int64_t E, const void* w, const void* w_scale, void* out, int out_dt, int64_t T, int64_t R,
+                             int64_t N, int64_t K, hipStream_t stream);
 hipError_t launch_combine(const void* y, int dt, const int32_t* row_of, const float* weights, const void* add,
                           void* out, int64_t T, int64_t R, int64_t topk, int64_t N, hipStream_t stream);
 }  // namespace w4
@@ -903,6 +918,184 @@ int w4_combine(const void* y, int dtype, const int32_t* row_of, const float* wei
     return fail(W4_ERR_ALIGN, "%s: y, add and out must be 16-byte aligned", fn);
   return hip_status(w4::launch_combine(y, dt, row_of, weights, add, out, T, R, topk, N,
                                        static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+// ---- MXFP4
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Scale bytes of a row: one per 32 columns, padded to whole blocks of 128.
+static int64_t mx_row_scales(int64_t K) { return (K + 127) / 128 * 4; }
+
+static int check_mx_matrix(const char* fn, int64_t M, int64_t K) {
+  if (M < 0 || K < 0) return fail(W4_ERR_INVALID, "%s: negative size M=%lld K=%lld", fn, (long long)M, (long long)K);
+  if (K % 32) return fail(W4_ERR_ALIGN, "%s: K=%lld is not a multiple of 32", fn, (long long)K);
+  if (M > kMaxDim || K > ((int64_t)1 << 24) || M * ((K + 127) / 128) >= ((int64_t)1 << 31))
+    return fail(W4_ERR_UNSUPPORTED, "%s: sizes too large (M=%lld K=%lld)", fn, (long long)M, (long long)K);
+  return W4_OK;
+}
+
+int w4_mxfp4_quantize(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, int act, void* codes, void* scales,
+                      void* stream) {
+  const char* fn = "w4_mxfp4_quantize";
+  const int dt = float_index(x_dtype);
+  if (dt < 0) return fail(W4_ERR_DTYPE, "%s: x must be bf16, fp16 or fp32 (dtype code %d)", fn, x_dtype);
+  if (act != W4_ACT_NONE && act != W4_ACT_SWIGLU) return fail(W4_ERR_INVALID, "%s: unknown activation %d", fn, act);
+  int rc = check_mx_matrix(fn, M, K);
+  if (rc) return rc;
+  const int64_t wide = act == W4_ACT_SWIGLU ? 2 * K : K, unit = dt == 2 ? 4 : 8;
+  if (ldx < wide || ldx % unit)
+    return fail(W4_ERR_ALIGN, "%s: ldx=%lld must be >= %lld and a multiple of %lld", fn, (long long)ldx, (long long)wide,
+                (long long)unit);
+  if (M == 0 || K == 0) return ok();
+  if (!x || !codes || !scales) return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
+  if (!aligned16(x) || !aligned16(codes))
+    return fail(W4_ERR_ALIGN, "%s: x and codes must be 16-byte aligned", fn);
+  if (!aligned4(scales)) return fail(W4_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
+  return hip_status(w4::launch_mx_quant(x, dt, act == W4_ACT_SWIGLU, M, K, ldx, codes, scales,
+                                        static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int w4_mxfp4_dequantize(const void* codes, const void* scales, int64_t M, int64_t K, void* out, int out_dtype,
+                        void* stream) {
+  const char* fn = "w4_mxfp4_dequantize";
+  const int dt = float_index(out_dtype);
+  if (dt < 0) return fail(W4_ERR_DTYPE, "%s: output must be bf16, fp16 or fp32 (dtype code %d)", fn, out_dtype);
+  int rc = check_mx_matrix(fn, M, K);
+  if (rc) return rc;
+  if (M == 0 || K == 0) return ok();
+  if (!codes || !scales || !out) return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
+  if (!aligned16(codes) || !aligned16(out))
+    return fail(W4_ERR_ALIGN, "%s: codes and out must be 16-byte aligned", fn);
+  if (!aligned4(scales)) return fail(W4_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
+  return hip_status(w4::launch_mx_dequant(codes, scales, M, K, out, dt, static_cast<hipStream_t>(stream)), fn);
+}
+
+static int check_mx(const char* fn, int64_t M, int64_t N, int64_t K) {
+  int rc = check_mnk(fn, M, N, K);
+  if (rc) return rc;
+  if (K % 32) return fail(W4_ERR_ALIGN, "%s: K=%lld is not a multiple of 32", fn, (long long)K);
+  // a tile's 256 rows are addressed with 32-bit offsets
+  if (K > ((int64_t)1 << 22)) return fail(W4_ERR_UNSUPPORTED, "%s: K=%lld exceeds 2^22", fn, (long long)K);
+  return W4_OK;
+}
+
+static int check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need, int64_t M, int64_t N,
+                           int64_t K) {
+  if (bytes < need || (need && !workspace))
+    return fail(W4_ERR_INVALID, "%s: workspace of %zu bytes is smaller than the %zu needed for M=%lld N=%lld K=%lld",
+                fn, bytes, need, (long long)M, (long long)N, (long long)K);
+  if (need && !aligned16(workspace)) return fail(W4_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  return W4_OK;
+}
+
+int w4_mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  const char* fn = "w4_mxfp4_gemm_workspace_bytes";
+  if (!bytes) return fail(W4_ERR_INVALID, "%s: null output pointer", fn);
+  int rc = check_mx(fn, M, N, K);
+  if (!rc) rc = check_threads(fn, w4::mx_gemm_threads(M, N, K));
+  if (rc) return rc;
+  *bytes = w4::mx_gemm_workspace(M, N, K);
+  return ok();
+}
+
+int w4_mxfp4_gemm(const void* a, const void* a_scale, const void* w, const void* w_scale, const void* bias, void* out,
+                  int out_dtype, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "w4_mxfp4_gemm";
+  const int dt = float_index(out_dtype);
+  if (dt < 0) return fail(W4_ERR_DTYPE, "%s: output must be bf16, fp16 or fp32 (dtype code %d)", fn, out_dtype);
+  int rc = check_mx(fn, M, N, K);
+  if (!rc) rc = check_threads(fn, w4::mx_gemm_threads(M, N, K));
+  if (rc) return rc;
+  if (M == 0 || N == 0) return ok();
+  if (!a || !a_scale || !w || !w_scale || !out) return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out))
+    return fail(W4_ERR_ALIGN, "%s: a, w and out must be 16-byte aligned", fn);
+  if (!aligned4(a_scale) || !aligned4(w_scale)) return fail(W4_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
+  rc = check_workspace(fn, workspace, workspace_bytes, w4::mx_gemm_workspace(M, N, K), M, N, K);
+  if (rc) return rc;
+  return hip_status(w4::launch_mx_gemm(a, a_scale, w, w_scale, bias, out, dt, M, N, K, workspace,
+                                       static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+// The quantized activations lie before the product's own workspace.
+static size_t mx_linear_codes(int64_t M, int64_t K) { return (size_t)M * (size_t)(K / 2); }
+static size_t mx_linear_scales(int64_t M, int64_t K) { return ((size_t)M * (size_t)mx_row_scales(K) + 15) & ~(size_t)15; }
+static size_t mx_linear_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || N == 0 || w4::mx_streams(M)) return 0;
+  return mx_linear_codes(M, K) + mx_linear_scales(M, K) + w4::mx_gemm_workspace(M, N, K);
+}
+
+static int check_mx_linear(const char* fn, int64_t M, int64_t N, int64_t K) {
+  int rc = check_mx(fn, M, N, K);
+  if (!rc) rc = check_threads(fn, w4::mx_gemm_threads(M, N, K));
+  return rc ? rc : check_mx_matrix(fn, M, K);
+}
+
+int w4_mxfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  const char* fn = "w4_mxfp4_linear_workspace_bytes";
+  if (!bytes) return fail(W4_ERR_INVALID, "%s: null output pointer", fn);
+  int rc = check_mx_linear(fn, M, N, K);
+  if (rc) return rc;
+  *bytes = mx_linear_workspace(M, N, K);
+  return ok();
+}
+
+int w4_mxfp4_linear(const void* x, int x_dtype, const void* w, const void* w_scale, const void* bias, void* out,
+                    int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "w4_mxfp4_linear";
+  if (x_dtype != W4_BF16 && x_dtype != W4_F16)
+    return fail(W4_ERR_DTYPE, "%s: activations must be bf16 or fp16 (dtype code %d)", fn, x_dtype);
+  int rc = check_mx_linear(fn, M, N, K);
+  if (rc) return rc;
+  if (M == 0 || N == 0) return ok();
+  if (!x || !w || !w_scale || !out) return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
+  if (!aligned16(x) || !aligned16(w) || !aligned16(out))
+    return fail(W4_ERR_ALIGN, "%s: x, w and out must be 16-byte aligned", fn);
+  if (!aligned4(w_scale)) return fail(W4_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
+  rc = check_workspace(fn, workspace, workspace_bytes, mx_linear_workspace(M, N, K), M, N, K);
+  if (rc) return rc;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool bf16 = x_dtype == W4_BF16;
+  if (w4::mx_streams(M)) return hip_status(w4::launch_mx_linear_few(x, bf16, w, w_scale, bias, out, M, N, K, s), fn);
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  uint8_t* scales = codes + mx_linear_codes(M, K);
+  const hipError_t e = w4::launch_mx_quant(x, bf16 ? 0 : 1, false, M, K, K, codes, scales, s);
+  if (e != hipSuccess) return hip_status(e, fn);
+  return hip_status(w4::launch_mx_gemm(codes, scales, w, w_scale, bias, out, bf16 ? 0 : 1, M, N, K,
+                                       scales + mx_linear_scales(M, K), s),
+                    fn);
+}
+
+int w4_mxfp4_grouped_gemm(const void* a, const void* a_scale, const int32_t* row_token, const int32_t* expert_offsets,
+                          int64_t E, const void* w, const void* w_scale, void* out, int out_dtype, int64_t T, int64_t R,
+                          int64_t N, int64_t K, void* stream) {
+  const char* fn = "w4_mxfp4_grouped_gemm";
+  if (out_dtype != W4_BF16 && out_dtype != W4_F16)
+    return fail(W4_ERR_DTYPE, "%s: output must be bf16 or fp16 (dtype code %d)", fn, out_dtype);
+  int rc = check_mx(fn, R, N, K);
+  if (rc) return rc;
+  if (E < 0 || E > 65535 || T < 0)
+    return fail(W4_ERR_INVALID, "%s: E=%lld T=%lld out of range", fn, (long long)E, (long long)T);
+  if (R == 0 || N == 0 || E == 0) return ok();
+  rc = check_threads(fn, w4::mx_grouped_threads(E, R, N));
+  if (rc) return rc;
+  if (row_token && (T <= 0 || T * K >= ((int64_t)1 << 32)))
+    return fail(W4_ERR_UNSUPPORTED, "%s: token count T=%lld out of range for K=%lld (T*K must be below 2^32)", fn,
+                (long long)T, (long long)K);
+  if (!row_token && T != R)
+    return fail(W4_ERR_INVALID, "%s: without row_token the activations need R=%lld rows, got T=%lld", fn,
+                (long long)R, (long long)T);
+  if (!a || !a_scale || !expert_offsets || !w || !w_scale || !out)
+    return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out))
+    return fail(W4_ERR_ALIGN, "%s: a, w and out must be 16-byte aligned", fn);
+  if (!aligned4(a_scale) || !aligned4(w_scale)) return fail(W4_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
+  return hip_status(w4::launch_mx_grouped(a, a_scale, row_token, expert_offsets, E, w, w_scale, out,
+                                          float_index(out_dtype), T, R, N, K, static_cast<hipStream_t>(stream)),
                     fn);
 }
 

@@ -1,5 +1,6 @@
 // Shared by the block-scaled FP8 products (fp8_block_gemm.hip: tiles through
-// LDS; fp8_block_stream.hip: few rows, weights streamed into registers).
+// LDS; fp8_block_stream.hip: few rows, weights streamed into registers) and,
+// where P is a type parameter, by the MXFP4 products.
 #pragma once
 
 #include "w4_device.h"
@@ -71,8 +72,8 @@ struct Segment {
   int64_t row0, rows;
 };
 
-template <int BM>
-__device__ __forceinline__ Segment find_segment(const Fp8Args& p) {
+template <int BM, typename P>
+__device__ __forceinline__ Segment find_segment(const P& p) {
   const int lane = threadIdx.x & 63;
   Segment s;
   s.e = -1;
@@ -119,8 +120,8 @@ __device__ __forceinline__ Segment find_segment(const Fp8Args& p) {
 }
 
 // Store C (4 or 8) consecutive columns of a row, with the bias added first.
-template <int OUT, int C>
-__device__ __forceinline__ void store_columns(const Fp8Args& p, float (&f)[C], int64_t orow, int n, bool bias) {
+template <int OUT, int C, typename P>
+__device__ __forceinline__ void store_columns(const P& p, float (&f)[C], int64_t orow, int n, bool bias) {
   if (bias) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -146,6 +147,27 @@ __device__ __forceinline__ void store_columns(const Fp8Args& p, float (&f)[C], i
     else
       *reinterpret_cast<v2i*>(o) = v2i{(int)w[0], (int)w[1]};
   }
+}
+
+// Split K: the partial sums [splits][rows][N], in order, to the output.
+template <int OUT, typename P>
+__global__ __launch_bounds__(256) void split_reduce_kernel(P p, const float* __restrict__ part) {
+  const int nc = p.N >> 3;
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= p.M * nc) return;
+  const int64_t span = p.M * p.N;
+  const float* q = part + c * 8;
+  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s, q += span) {
+    const v4f x = *reinterpret_cast<const v4f*>(q), y = *reinterpret_cast<const v4f*>(q + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] += x[e];
+      f[4 + e] += y[e];
+    }
+  }
+  store_columns<OUT, 8>(p, f, c / nc * p.N, (int)(c % nc) * 8, p.bias != nullptr);
 }
 
 // Blocks of a grouped launch with BM x BN tiles.

@@ -279,27 +279,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args p) {
   }
 }
 
-// Split K: the partial sums [splits][rows][N], in order, to the output.
-template <int OUT>
-__global__ __launch_bounds__(256) void fp8_reduce_kernel(Fp8Args p, const float* __restrict__ part) {
-  const int nc = p.N >> 3;
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.M * nc) return;
-  const int64_t span = p.M * p.N;
-  const float* q = part + c * 8;
-  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = 0; s < p.splits; ++s, q += span) {
-    const v4f x = *reinterpret_cast<const v4f*>(q), y = *reinterpret_cast<const v4f*>(q + 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[e] += x[e];
-      f[4 + e] += y[e];
-    }
-  }
-  store_columns<OUT, 8>(p, f, c / nc * p.N, (int)(c % nc) * 8, p.bias != nullptr);
-}
-
 // The 256 x 256 tile does a third more work per time than four of 128 x 128, as
 // long as its padding takes no more than that.
 static bool wide_pays(int64_t t256, int64_t t128) { return 3 * t256 <= t128; }
@@ -414,9 +393,9 @@ hipError_t launch_fp8_block_gemm(const void* a, const float* a_scale, const void
   if (e != hipSuccess || p.splits == 1) return e;
   const dim3 grid((unsigned)((M * (N / 8) + 255) / 256)), block(256);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p, static_cast<const float*>(ws)); };
-  if (out_dt == 0) go(fp8_reduce_kernel<0>);
-  else if (out_dt == 1) go(fp8_reduce_kernel<1>);
-  else go(fp8_reduce_kernel<2>);
+  if (out_dt == 0) go(split_reduce_kernel<0, Fp8Args>);
+  else if (out_dt == 1) go(split_reduce_kernel<1, Fp8Args>);
+  else go(split_reduce_kernel<2, Fp8Args>);
   return hipGetLastError();
 }
 

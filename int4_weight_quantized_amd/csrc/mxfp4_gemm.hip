@@ -1,0 +1,419 @@
+// MXFP4 matrix products: dense, and grouped over the row segments of routed
+// experts.
+//
+//   out[r, n] = sum_b 2^(ea[t, b] + ew[n, b]) * sum_{k in block b} a[t, k] * w[n, k]  (+ bias[n])
+//
+// over the blocks b of 32 columns, with t = r, or the row's token in the
+// grouped form. v_mfma_scale_f32_32x32x64_f8f6f4 takes both blocks' powers of
+// two with its operands, so its fp32 accumulators need no other arithmetic
+// (measured: 4e-8 of the absolute sum off over 128 columns, as fp32's own sums;
+// the 16x16x128 form runs at half its rate).
+//
+// Tile kernel: WM x WN waves, each with a tile of 32 MI rows x 32 NJ columns,
+// K in steps of 256 (128 bytes of a row).
+// - Both operands pass through LDS in two stages, by LDS DMA (an asm statement:
+//   with the builtin the compiler waits for all of it before the next LDS read).
+// - The matrix unit reads, from lane (row, half h), 16 bytes = one block of 32
+//   columns. MFMA c of a step takes the blocks c (h = 0) and 4 + c (h = 1), so
+//   a lane's four scales of a step are one word of LDS, byte c of it MFMA c's.
+// - The fragments of MFMA group c + 1 are read under the MFMAs of group c. The
+//   last group of a step runs behind the barrier that ends the step: its
+//   operands are in registers by then, so its stage is free for the DMA two
+//   steps ahead and the next step's first fragments are read under it.
+// - The weights are the A operand and the activations the B operand: a lane's
+//   results lie in one activation row. Row q of a weight fragment is its column
+//   16 (q / 4 % 2) + 4 (q / 8) + q % 4, which gives a lane 16 consecutive ones.
+#include "mxfp4.h"
+
+namespace w4 {
+
+constexpr int kMK = 256;                             // columns per step
+constexpr int kMB = kMK / 2;                         // bytes of a row per step
+
+__device__ __forceinline__ v8i mx_operand(v4i v) { return v8i{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+template <int C>
+__device__ __forceinline__ v16f mx_mfma(v4i w, v4i a, v16f d, int sw, int sa) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(w), mx_operand(a), d, 4, 4, C, sw, C, sa);
+}
+
+// OUT: 0 bf16, 1 fp16, 2 fp32.
+template <int WM, int WN, int MI, int NJ, bool GROUPED, int OUT>
+__global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_kernel(MxArgs p) {
+  constexpr int NW = WM * WN, TH = 64 * NW, BM = 32 * MI * WM, BN = 32 * NJ * WN;
+  constexpr int RA = BM * 8 / TH, RB = BN * 8 / TH;  // LDS DMAs of codes per thread and step
+  constexpr int RS = ((BM + BN) / 64 + NW - 1) / NW; // of scales, every second step
+  static_assert(BM % 64 == 0 && BN % 64 == 0, "a wave fetches scales of activations or of weights");
+  static_assert(RA * TH == BM * 8 && RB * TH == BN * 8, "whole DMAs");
+  constexpr int STAGE = (BM + BN) * kMB, SCALES = (BM + BN) * 16;
+  // two stages (activation rows, then weight rows), two chunks of the scales of 2 steps (16 bytes per row)
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE + 2 * SCALES];
+
+  // ---- work item
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int h = lane >> 5, l32 = lane & 31;
+  int e = 0, tn, split = 0;
+  int64_t r0, row_end, out0 = 0;                     // first row and end of this tile's rows (segment-local if grouped)
+  if constexpr (GROUPED) {
+    const Segment s = find_segment<BM>(p);
+    if (s.e < 0) return;
+    e = s.e;
+    tn = s.tn;
+    r0 = (int64_t)s.mt * BM;
+    out0 = s.row0;
+    row_end = s.rows;
+  } else {
+    const int64_t t = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+    split = (int)(t / p.tiles);
+    const int64_t tile = t - (int64_t)split * p.tiles;
+    r0 = tile / p.NT * BM;
+    tn = (int)(tile % p.NT);
+    row_end = p.M;
+  }
+  const int n0 = tn * BN;
+  const int k0 = (int)((int64_t)p.KT * split / p.splits), k1 = (int)((int64_t)p.KT * (split + 1) / p.splits);
+  const int64_t KH = p.K >> 1;                       // code bytes of a row
+
+  // ---- LDS DMA: a wave's load fills 8 rows (one KiB), lane L at row L / 8, physical 16-byte chunk L % 8. Row r holds
+  // logical chunk c at physical chunk c ^ f(r), so that 8 lanes that read one chunk of 8 rows touch 8 different ones.
+  // Rows and columns past the end get an offset past the buffer, which reads as zero.
+  const int lrow = lane >> 3, lchunk = lane & 7;
+  const bool gather = GROUPED && p.row_token;
+  const int64_t abase = gather ? 0 : out0 + r0;
+  const int64_t arows = gather ? p.M : min((int64_t)BM, p.M - abase);
+  const __amdgpu_buffer_rsrc_t arsrc = make_rsrc(p.a + abase * KH, (uint32_t)max(arows * KH, (int64_t)0));
+  const __amdgpu_buffer_rsrc_t asr = make_rsrc(p.a_scale + abase * p.KS, (uint32_t)max(arows * p.KS, (int64_t)0));
+  const int64_t wrow0 = (int64_t)e * p.N + n0;
+  const int wrows = min(BN, p.N - n0);
+  const __amdgpu_buffer_rsrc_t wrsrc = make_rsrc(p.w + wrow0 * KH, (uint32_t)(wrows * KH));
+  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(p.w_scale + wrow0 * p.KS, (uint32_t)((int64_t)wrows * p.KS));
+  auto token = [&](int r) -> int64_t {               // activation row of tile row r, relative to abase; -1: none
+    if (r0 + r >= row_end) return -1;
+    if (gather) {
+      const int t = p.row_token[out0 + r0 + r];
+      return (unsigned)t < (uint64_t)p.M ? t : -1;
+    }
+    return (!GROUPED || out0 + r0 + r < p.M) ? r : -1;
+  };
+  uint32_t a_off[RA], b_off[RB];
+  uint32_t a_dead = 0, b_dead = 0;                   // bit i: load i's chunk lies past K in the last step
+  const int klast = p.K - (p.KT - 1) * kMK;          // columns of the last step
+#pragma unroll
+  for (int i = 0; i < RA; ++i) {
+    const int r = (TH / 8) * i + 8 * wave + lrow;
+    const int c = lchunk ^ (r & 7);
+    const int64_t t = token(r);
+    a_off[i] = t >= 0 ? (uint32_t)(t * KH + 16 * c) : kPast;
+    if (32 * c >= klast) a_dead |= 1u << i;
+  }
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    const int r = (TH / 8) * i + 8 * wave + lrow;
+    const int c = lchunk ^ ((r & 3) + 4 * ((r >> 4) & 1));
+    b_off[i] = n0 + r < p.N ? (uint32_t)(r * KH + 16 * c) : kPast;
+    if (32 * c >= klast) b_dead |= 1u << i;
+  }
+  uint32_t s_off[RS];
+#pragma unroll
+  for (int i = 0; i < RS; ++i) {
+    const int r = 64 * (NW * i + wave) + lane;       // activation rows, then weight rows
+    if (64 * (NW * i + wave) < BM) {
+      const int64_t t = token(r);
+      s_off[i] = t >= 0 ? (uint32_t)(t * p.KS) : kPast;
+    } else {
+      s_off[i] = n0 + r - BM < p.N ? (uint32_t)((r - BM) * (int64_t)p.KS) : kPast;
+    }
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  const uint32_t ldsw = __builtin_amdgcn_readfirstlane(lds0 + 8 * wave * kMB);
+  // m0 holds the LDS address. The compiler keeps nothing in it here, and a clobber of a reserved register is not honoured.
+  auto dma = [&](const __amdgpu_buffer_rsrc_t rs, uint32_t dst, uint32_t off, uint32_t ks) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(dst), "v"(off), "s"(rs), "s"(ks) : "memory");
+  };
+  // DMA q of a step: the activations' RA, the weights' RB, then every second step the scales' RS
+  constexpr int ND = RA + RB + RS;
+  auto gload1 = [&](int tk, uint32_t stage, int q) {
+    if (q >= RA + RB) {
+      const int i = q - RA - RB, rel = tk - k0;
+      const int grp = NW * i + wave;                 // 64 rows
+      if ((rel & 1) || 64 * grp >= BM + BN) return;
+      const uint32_t dst = lds0 + 2 * STAGE + ((rel >> 1) & 1) * SCALES + 1024 * grp;
+      if (64 * grp < BM) dma(asr, dst, s_off[i], (uint32_t)tk * 8);
+      else dma(wsr, dst, s_off[i], (uint32_t)tk * 8);
+      return;
+    }
+    const bool act = q < RA;
+    const int i = act ? q : q - RA;
+    uint32_t off = act ? a_off[i] : b_off[i];
+    if (tk == p.KT - 1 && (((act ? a_dead : b_dead) >> i) & 1)) off = kPast;
+    dma(act ? arsrc : wrsrc, ldsw + stage + ((act ? 0 : BM) + (TH / 8) * i) * kMB, off, (uint32_t)tk * kMB);
+  };
+  auto gload = [&](int tk, uint32_t stage) {
+#pragma unroll
+    for (int q = 0; q < ND; ++q) gload1(tk, stage, q);
+  };
+
+  v16f acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  // ---- fragments
+  const int ar = 32 * MI * wm + l32;                 // + 32 i, which leaves f unchanged
+  const int br = 32 * NJ * wn + 16 * ((l32 >> 2) & 1) + 4 * (l32 >> 3) + (l32 & 3);   // + 32 j, likewise
+  const int af7 = l32 & 7, bf7 = (l32 & 3) + 4 * ((l32 >> 2) & 1);
+  auto afrag = [&](uint32_t stage, int i, int c) -> v4i {
+    return *reinterpret_cast<const v4i*>(lds + stage + (ar + 32 * i) * kMB + 16 * ((4 * h + c) ^ af7));
+  };
+  auto bfrag = [&](uint32_t stage, int j, int c) -> v4i {
+    return *reinterpret_cast<const v4i*>(lds + stage + (BM + br + 32 * j) * kMB + 16 * ((4 * h + c) ^ bf7));
+  };
+  // the four scales of a step; blocks past K (of the row's padding, or of the next row) are none
+  int smask = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (32 * (4 * h + c) < klast) smask |= 0xFF << (8 * c);
+  auto scale = [&](int tk, int row) -> int {
+    const int rel = tk - k0;
+    const uint8_t* q = lds + 2 * STAGE + ((rel >> 1) & 1) * SCALES + row * 16 + 8 * (rel & 1) + 4 * h;
+    return *reinterpret_cast<const int*>(q) & (tk == p.KT - 1 ? smask : -1);
+  };
+
+  constexpr int NM = MI * NJ;
+  if (k0 < k1) {
+    gload(k0, 0);
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    if (k0 + 1 < k1) gload(k0 + 1, STAGE);
+    if (GROUPED && r0 + 32 * MI * wm >= row_end) {   // a wave whose rows all lie past the segment only fetches
+      for (int tk = k0; tk < k1; ++tk) {
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        if (tk + 2 < k1) gload(tk + 2, ((tk - k0) & 1) * STAGE);
+      }
+      return;
+    }
+    v4i af[2][MI], bf[2][NJ];
+    int sa[MI], sb[NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      af[0][i] = afrag(0, i, 0);
+      sa[i] = scale(k0, ar + 32 * i);
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      bf[0][j] = bfrag(0, j, 0);
+      sb[j] = scale(k0, BM + br + 32 * j);
+    }
+    for (int tk = k0; tk < k1; ++tk) {
+      const uint32_t st = ((tk - k0) & 1) * STAGE;   // this step's stage
+      int sa2[MI], sb2[NJ];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int cur = c & 1, nxt = cur ^ 1;
+        if (c == 3) {
+          // every fragment of this step is in registers; once the next step's tiles have landed: swap
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        const uint32_t from = c == 3 ? STAGE - st : st;
+#pragma unroll
+        for (int n = 0; n < NM; ++n) {
+          const int i = n / NJ, j = n % NJ;
+          // the next group's fragments (at the end: of a stage whose contents are not used)
+#pragma unroll
+          for (int q = n * (MI + NJ) / NM; q < (n + 1) * (MI + NJ) / NM; ++q) {
+            if (q < NJ) bf[nxt][q] = bfrag(from, q, (c + 1) & 3);
+            else af[nxt][q - NJ] = afrag(from, q - NJ, (c + 1) & 3);
+            if (c == 3) {
+              if (q < NJ) sb2[q] = scale(tk + 1, BM + br + 32 * q);
+              else sa2[q - NJ] = scale(tk + 1, ar + 32 * (q - NJ));
+            }
+          }
+          if (c == 0) acc[i][j] = mx_mfma<0>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
+          if (c == 1) acc[i][j] = mx_mfma<1>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
+          if (c == 2) acc[i][j] = mx_mfma<2>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
+          if (c == 3) {
+            acc[i][j] = mx_mfma<3>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
+            if (tk + 2 < k1) {
+#pragma unroll
+              for (int q = n * ND / NM; q < (n + 1) * ND / NM; ++q) gload1(tk + 2, st, q);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) sa[i] = sa2[i];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) sb[j] = sb2[j];
+    }
+  }
+
+  // ---- output: lane's row per i, 16 consecutive columns per j
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t r = r0 + 32 * (MI * wm + i) + l32;
+    if (r >= row_end) continue;
+    const int64_t orow = (out0 + r + (int64_t)split * p.M) * p.N;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int n = n0 + 32 * (NJ * wn + j) + 16 * h + 8 * q;
+        if (n >= p.N) continue;
+        float f[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) f[c] = acc[i][j][8 * q + c];
+        store_columns<OUT, 8>(p, f, orow, n, !GROUPED && p.bias && p.splits == 1);
+      }
+    }
+  }
+}
+
+// What the dense product runs as: rows streamed (tile 0), or a tile and its K splits.
+struct MxPlan {
+  int tile, splits;
+};
+
+static MxPlan plan_dense(int64_t M, int64_t N, int64_t K) {
+  if (M <= 16) return {0, 1};
+  const int64_t KT = (K + kMK - 1) / kMK;
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  if (tiles(256, 256) >= 192 && 3 * tiles(256, 256) <= tiles(128, 128)) return {256, 1};
+  const int tile = M <= 64 ? 64 : 128;
+  const int64_t t = tiles(tile, 128);
+  int64_t best = 1, cost = 4000 + 900 * KT;          // ns
+  for (int64_t s = 2; s * t <= 512 && 2 * s <= KT; ++s) {
+    const int64_t c = 6000 + 900 * ((KT + s - 1) / s) + 100 * s + s * M * N * 8 / 4500;
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return {tile, (int)best};
+}
+
+size_t mx_gemm_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || N == 0) return 0;
+  const MxPlan pl = plan_dense(M, N, K);
+  return pl.splits > 1 ? (size_t)pl.splits * (size_t)M * (size_t)N * 4 : 0;
+}
+
+// Threads of the largest launch of a product, for the host's check against a launch's limit.
+int64_t mx_gemm_threads(int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || N == 0) return 0;
+  const MxPlan pl = plan_dense(M, N, K);
+  if (pl.tile == 0) return mx_stream_threads(M, N, 0, 0);
+  const int64_t bm = pl.tile, bn = pl.tile == 256 ? 256 : 128;
+  const int64_t reduce = pl.splits > 1 ? M * (N / 8) : 0, product = (M + bm - 1) / bm * ((N + bn - 1) / bn) * pl.splits * 256;
+  return product > reduce ? product : reduce;
+}
+
+bool mx_streams(int64_t M) { return M <= 16; }
+
+template <int BM, int BN, typename F>
+static hipError_t tile_go(MxArgs p, F kernel, hipStream_t stream) {
+  p.NT = (p.N + BN - 1) / BN;
+  p.tiles = (p.M + BM - 1) / BM * p.NT;
+  const dim3 grid((unsigned)(p.offsets ? grouped_blocks(p.E, p.R, p.N, BM, BN) : p.tiles * p.splits)), block(256);
+  hipLaunchKernelGGL(kernel, grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
+template <int WM, int WN, int MI, int NJ>
+static hipError_t dense_go(const MxArgs& p, int out_dt, hipStream_t stream) {
+  auto go = [&](auto kernel) { return tile_go<32 * MI * WM, 32 * NJ * WN>(p, kernel, stream); };
+  if (out_dt == 0) return go(mx_tile_kernel<WM, WN, MI, NJ, false, 0>);
+  if (out_dt == 1) return go(mx_tile_kernel<WM, WN, MI, NJ, false, 1>);
+  return go(mx_tile_kernel<WM, WN, MI, NJ, false, 2>);
+}
+
+static MxArgs mx_args(const void* a, const void* a_scale, const void* w, const void* w_scale, void* out, int64_t M,
+                      int64_t N, int64_t K) {
+  MxArgs p{};
+  p.a = static_cast<const uint8_t*>(a);
+  p.a_scale = static_cast<const uint8_t*>(a_scale);
+  p.w = static_cast<const uint8_t*>(w);
+  p.w_scale = static_cast<const uint8_t*>(w_scale);
+  p.out = out;
+  p.M = p.R = M;
+  p.E = 1;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.KS = (int)mx_scale_bytes(K);
+  p.KT = (int)((K + kMK - 1) / kMK);
+  p.splits = 1;
+  return p;
+}
+
+// Few rows of 16-bit activations, quantized on the way (a: bf16 or fp16 [M, K]).
+hipError_t launch_mx_linear_few(const void* x, bool bf16, const void* w, const void* w_scale, const void* bias, void* out,
+                                int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  if (M == 0 || N == 0) return hipSuccess;
+  MxArgs p = mx_args(x, nullptr, w, w_scale, out, M, N, K);
+  p.bias = bias;
+  return launch_mx_stream(p, bf16 ? 1 : 2, bf16 ? 0 : 1, stream);
+}
+
+hipError_t launch_mx_gemm(const void* a, const void* a_scale, const void* w, const void* w_scale, const void* bias,
+                          void* out, int out_dt, int64_t M, int64_t N, int64_t K, void* ws, hipStream_t stream) {
+  if (M == 0 || N == 0) return hipSuccess;
+  MxArgs p = mx_args(a, a_scale, w, w_scale, out, M, N, K);
+  p.bias = bias;
+  const MxPlan pl = plan_dense(M, N, K);
+  p.splits = pl.splits;
+  if (pl.tile == 0) return launch_mx_stream(p, 0, out_dt, stream);
+  MxArgs part = p;
+  if (p.splits > 1) part.out = ws;
+  const int dt = p.splits > 1 ? 2 : out_dt;
+  hipError_t e;
+  if (pl.tile == 64) e = dense_go<2, 2, 1, 2>(part, dt, stream);
+  else if (pl.tile == 128) e = dense_go<2, 2, 2, 2>(part, dt, stream);
+  else e = dense_go<2, 2, 4, 4>(part, dt, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const dim3 grid((unsigned)((M * (N / 8) + 255) / 256)), block(256);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p, static_cast<const float*>(ws)); };
+  if (out_dt == 0) go(split_reduce_kernel<0, MxArgs>);
+  else if (out_dt == 1) go(split_reduce_kernel<1, MxArgs>);
+  else go(split_reduce_kernel<2, MxArgs>);
+  return hipGetLastError();
+}
+
+// What the grouped product runs as: rows streamed (0), or the tile.
+static int plan_grouped(int64_t E, int64_t R, int64_t N) {
+  if (R <= 4 * E) return 0;
+  const int64_t c256 = (N + 255) / 256, c128 = (N + 127) / 128;
+  if (R <= 96 * E || (R / 256 + E / 2) * c256 < 160 || 3 * 2 * c256 > 4 * c128) return 128;
+  return 256;
+}
+
+int64_t mx_grouped_threads(int64_t E, int64_t R, int64_t N) {
+  if (R == 0 || N == 0 || E == 0) return 0;
+  const int tile = plan_grouped(E, R, N);
+  if (tile == 0) return mx_stream_threads(0, N, E, R);
+  return grouped_blocks(E, R, N, tile, tile) * 256;
+}
+
+hipError_t launch_mx_grouped(const void* a, const void* a_scale, const int32_t* row_token, const int32_t* offsets,
+                             int64_t E, const void* w, const void* w_scale, void* out, int out_dt, int64_t T, int64_t R,
+                             int64_t N, int64_t K, hipStream_t stream) {
+  if (R == 0 || N == 0 || E == 0) return hipSuccess;
+  MxArgs p = mx_args(a, a_scale, w, w_scale, out, T, N, K);
+  p.row_token = row_token;
+  p.offsets = offsets;
+  p.R = R;
+  p.E = (int)E;
+  const int tile = plan_grouped(E, R, N);
+  if (tile == 0) return launch_mx_stream(p, 0, out_dt, stream);
+  if (tile == 128)
+    return out_dt == 0 ? tile_go<128, 128>(p, mx_tile_kernel<2, 2, 2, 2, true, 0>, stream)
+                       : tile_go<128, 128>(p, mx_tile_kernel<2, 2, 2, 2, true, 1>, stream);
+  return out_dt == 0 ? tile_go<256, 256>(p, mx_tile_kernel<2, 2, 4, 4, true, 0>, stream)
+                     : tile_go<256, 256>(p, mx_tile_kernel<2, 2, 4, 4, true, 1>, stream);
+}
+
+}  // namespace w4

@@ -58,6 +58,13 @@ _SIGS = {
     "w4_fp8_block_gemm": [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, ctypes.c_size_t, _P],
     "w4_fp8_block_grouped_gemm": [_P, _P, _P, _P, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _P],
     "w4_combine": [_P, _I, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P],
+    "w4_mxfp4_quantize": [_P, _I, _I64, _I64, _I64, _I, _P, _P, _P],
+    "w4_mxfp4_dequantize": [_P, _P, _I64, _I64, _P, _I, _P],
+    "w4_mxfp4_gemm_workspace_bytes": [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "w4_mxfp4_gemm": [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, ctypes.c_size_t, _P],
+    "w4_mxfp4_linear_workspace_bytes": [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "w4_mxfp4_linear": [_P, _I, _P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P],
+    "w4_mxfp4_grouped_gemm": [_P, _P, _P, _P, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _P],
     "w4_last_error": [],
     "w4_version": [],
 }
@@ -604,4 +611,119 @@ def w4_combine(y, row_of, weights, add=None, out=None, stream=None):
         _ptr(y), _float_code(y.dtype), _arg(row_of, torch.int32, (T, topk), "row_of"),
         _arg(weights, torch.float32, (T, topk), "weights"), _arg(add, y.dtype, (T, N), "add"),
         _arg(out, y.dtype, (T, N), "out"), T, R, topk, N, _stream(stream))
+    return out
+
+
+# ----------------------------------------------------------------- MXFP4
+
+def _mx_row(K: int) -> int:
+    """Scale bytes of a row: one per 32 columns, padded to whole blocks of 128."""
+    return 4 * ((K + 127) // 128)
+
+
+def w4_mxfp4_quantize(x, act: str = "none", out=None, stream=None):
+    """x [M, K] ([M, 2K] = gate | up with act="swiglu") bf16/fp16/fp32, rows may be strided -> (codes uint8 [M, K / 2] of
+    E2M1 pairs, scales uint8 [M, 4 * ceil(K / 128)] of E8M0 bits, one per 32 columns, then padding)."""
+    if act not in W4_ACTS:
+        raise ValueError(f"act must be one of {sorted(W4_ACTS)}, got {act!r}")
+    M, wide = x.shape
+    if act == "swiglu" and wide % 2:
+        raise ValueError(f"swiglu takes gate and up side by side: {wide} columns cannot be halved")
+    K = wide // 2 if act == "swiglu" else wide
+    ptr, ldx = _rows_ptr(x, "x")
+    if out is None:
+        out = (_new((M, K // 2), torch.uint8, x.device, stream), _new((M, _mx_row(K)), torch.uint8, x.device, stream))
+    codes, scales = out
+    _call("w4_mxfp4_quantize",
+        ptr, _float_code(x.dtype), M, K, ldx, W4_ACTS[act], _arg(codes, torch.uint8, (M, K // 2), "codes"),
+        _arg(scales, torch.uint8, (M, _mx_row(K)), "scales"), _stream(stream))
+    return out
+
+
+def w4_mxfp4_dequantize(codes, scales, out=None, out_dtype=torch.bfloat16, stream=None):
+    """codes uint8 [M, K / 2] and scales uint8 [M, 4 * ceil(K / 128)] -> the values they stand for, [M, K]
+    bf16/fp16/fp32."""
+    M, K = codes.shape[0], 2 * codes.shape[1]
+    if out is None:
+        out = _new((M, K), out_dtype, codes.device, stream)
+    _call("w4_mxfp4_dequantize",
+        _arg(codes, torch.uint8, (M, K // 2), "codes"), _arg(scales, torch.uint8, (M, _mx_row(K)), "scales"), M, K,
+        _arg(out, out.dtype, (M, K), "out"), _float_code(out.dtype), _stream(stream))
+    return out
+
+
+def w4_mxfp4_gemm_workspace(M: int, N: int, K: int, device="cuda", stream=None) -> torch.Tensor:
+    """Device scratch for w4_mxfp4_gemm at these sizes (uint8, possibly empty), for use on `stream`."""
+    n = ctypes.c_size_t(0)
+    _check("w4_mxfp4_gemm_workspace_bytes", lib().w4_mxfp4_gemm_workspace_bytes(M, N, K, ctypes.byref(n)))
+    return _new((n.value,), torch.uint8, device, stream)
+
+
+def w4_mxfp4_gemm(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """a [M, K] and w [N, K] as MXFP4 codes (uint8 [., K / 2]) and scales (uint8 [., 4 * ceil(K / 128)]) -> out [M, N]
+    bf16/fp16/fp32 (+ bias [N] of the same type)."""
+    (M, KH), (N, Kw) = a.shape, w.shape
+    if KH != Kw:
+        raise ValueError(f"a has {2 * KH} columns, w {2 * Kw}")
+    K, KS = 2 * KH, _mx_row(2 * KH)
+    if out is None:
+        out = _new((M, N), out_dtype, a.device, stream)
+    p_a, p_as = _arg(a, torch.uint8, (M, KH), "a"), _arg(a_scale, torch.uint8, (M, KS), "a_scale")
+    p_w, p_ws = _arg(w, torch.uint8, (N, KH), "w"), _arg(w_scale, torch.uint8, (N, KS), "w_scale")
+    p_bias = _arg(bias, out.dtype, (N,), "bias")
+    p_out = _arg(out, out.dtype, (M, N), "out")
+    if workspace is None:
+        workspace = w4_mxfp4_gemm_workspace(M, N, K, a.device, stream)
+    _call("w4_mxfp4_gemm",
+        p_a, p_as, p_w, p_ws, p_bias, p_out, _float_code(out.dtype), M, N, K, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    return out
+
+
+def w4_mxfp4_linear_workspace(M: int, N: int, K: int, device="cuda", stream=None) -> torch.Tensor:
+    """Device scratch for w4_mxfp4_linear at these sizes (uint8, possibly empty), for use on `stream`."""
+    n = ctypes.c_size_t(0)
+    _check("w4_mxfp4_linear_workspace_bytes", lib().w4_mxfp4_linear_workspace_bytes(M, N, K, ctypes.byref(n)))
+    return _new((n.value,), torch.uint8, device, stream)
+
+
+def w4_mxfp4_linear(x, w, w_scale, bias=None, out=None, workspace=None, stream=None):
+    """x [M, K] bf16/fp16, quantized to MXFP4 on the way, times w [N, K] in MXFP4 (codes uint8 [N, K / 2], scales uint8
+    [N, 4 * ceil(K / 128)]) -> out [M, N] in x's type (+ bias [N])."""
+    (M, K), (N, KH) = x.shape, w.shape
+    if K != 2 * KH:
+        raise ValueError(f"x has {K} columns, w {2 * KH}")
+    if out is None:
+        out = _new((M, N), x.dtype, x.device, stream)
+    p_x = _arg(x, x.dtype, (M, K), "x")
+    p_w, p_ws = _arg(w, torch.uint8, (N, KH), "w"), _arg(w_scale, torch.uint8, (N, _mx_row(K)), "w_scale")
+    p_bias = _arg(bias, x.dtype, (N,), "bias")
+    p_out = _arg(out, x.dtype, (M, N), "out")
+    if workspace is None:
+        workspace = w4_mxfp4_linear_workspace(M, N, K, x.device, stream)
+    _call("w4_mxfp4_linear",
+        p_x, _half_code(x.dtype), p_w, p_ws, p_bias, p_out, M, N, K, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    return out
+
+
+def w4_mxfp4_grouped_gemm(a, a_scale, row_token, expert_offsets, w, w_scale, out=None, out_dtype=torch.bfloat16,
+                          stream=None):
+    """The MXFP4 product over expert segments: w [E, N, K / 2], w_scale [E, N, 4 * ceil(K / 128)]; output row r of expert
+    e (expert_offsets) takes activation row row_token[r], or row r itself with row_token None. -> out [R, N] bf16/fp16;
+    rows past expert_offsets[E] are not written."""
+    (T, KH), (E, N, Kw) = a.shape, w.shape
+    if KH != Kw:
+        raise ValueError(f"a has {2 * KH} columns, w {2 * Kw}")
+    K, KS = 2 * KH, _mx_row(2 * KH)
+    R = T if row_token is None else row_token.shape[0]
+    if out is None:
+        out = _new((R, N), out_dtype, a.device, stream)
+    p_a, p_as = _arg(a, torch.uint8, (T, KH), "a"), _arg(a_scale, torch.uint8, (T, KS), "a_scale")
+    p_token = _arg(row_token, torch.int32, (R,), "row_token")
+    p_off = _arg(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    p_w, p_ws = _arg(w, torch.uint8, (E, N, KH), "w"), _arg(w_scale, torch.uint8, (E, N, KS), "w_scale")
+    p_out = _arg(out, out.dtype, (R, N), "out")
+    _call("w4_mxfp4_grouped_gemm",
+        p_a, p_as, p_token, p_off, E, p_w, p_ws, p_out, _half_code(out.dtype), T, R, N, K, _stream(stream))
     return out
