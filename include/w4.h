@@ -729,6 +729,48 @@ int w4_mxfp4_grouped_gemm(const void* a, const void* a_scale, const int32_t* row
                           int64_t E, const void* w, const void* w_scale, void* out, int out_dtype, int64_t T, int64_t R,
                           int64_t N, int64_t K, void* stream);
 
+/* Weight formats of w4_moe_decode. */
+#define W4_MOE_FP8_BLOCK 1   /* E4M3 with fp32 scales per 128 x 128, as w4_fp8_block_grouped_gemm */
+#define W4_MOE_MXFP4     2   /* as w4_mxfp4_grouped_gemm */
+#define W4_MOE_INT4      3   /* w4_repack tiles with fp16 scales [E, G, N], as w4a8_grouped_gemm */
+
+/*
+ * The whole routed-expert layer for a few tokens (a decode step): router logits
+ * and hidden rows in, the experts' weighted sum out. Weight-only: the activations
+ * are not quantized. Per token t, with ids and weights as w4_route defines them
+ * from the same arguments:
+ *   out[t] = sum_j weights[t, j] * W2[e] (silu(W1[e] x[t]) * (W3[e] x[t]))  (+ add[t]),
+ *   e = ids[t, j]; an id of -1 adds nothing
+ * Products and sums in fp32; between the two products the gated rows (times their
+ * routing weight) are held to 16 bits of mantissa; one rounding to the output
+ * type at the end. Two kernels up to 2 tokens of 256 experts, three above.
+ *   x        device, [T, H] contiguous, bf16 or fp16;  add: device or NULL, [T, H];
+ *            out: device, [T, H], all x_dtype and 16-byte aligned; out may be add
+ *   logits .. scale  as w4_route
+ *   w13      device, [E, 2 I, H]: W1's (gate) rows, then W3's (up);  w2: [E, H, I],
+ *            in w_format, with w13_scale and w2_scale (8-byte aligned); int4: E
+ *            matrices from w4_repack (K = H, N = 2 I; K = I, N = H) with scales
+ *            [E, H / group, 2 I] and [E, I / group, H]
+ *   group    int4 only: -1 (per channel) or a multiple of 128 dividing H and I
+ *   T        at most W4_MOE_DECODE_MAX_TOKENS (more tokens: the grouped products);
+ *            H, I multiples of 32 (int4: of 128)
+ *   workspace device, w4_moe_decode_workspace_bytes (16-byte aligned), owned by
+ *            the caller; calls sharing one must not overlap. Nothing in it needs
+ *            to start at zero.
+ * Results do not depend on timing (a token's last bits may on the experts of the
+ * others, through the order of its sum; values that are not finite stay in their
+ * token's row).
+ * Errors: INVALID, ALIGN, GROUP, DTYPE, UNSUPPORTED (T, E, topk, group_top; H or I
+ *         above 2^22, T*topk*I above 2^27), HIP. T == 0 enqueues nothing.
+ */
+#define W4_MOE_DECODE_MAX_TOKENS 32
+int w4_moe_decode_workspace_bytes(int64_t T, int64_t E, int64_t topk, int64_t H, int64_t I, size_t* bytes);
+int w4_moe_decode(const void* x, int x_dtype, const void* logits, int logits_dtype, int64_t ld, int score, const float* bias,
+                  int64_t n_groups, int64_t topk_groups, int64_t group_top, int64_t topk, int renorm, double scale,
+                  int w_format, const void* w13, const void* w13_scale, const void* w2, const void* w2_scale, int64_t group,
+                  const void* add, void* out, int64_t T, int64_t E, int64_t H, int64_t I, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* w4_last_error(void);
 

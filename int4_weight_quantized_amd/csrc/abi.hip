@@ -83,6 +83,12 @@ hipError_t launch_mx_linear_few(const void* x, bool bf16, const void* w, const v
 hipError_t launch_mx_grouped(const void* a, const void* a_scale, const int32_t* row_token, const int32_t* offsets,
                              int64_t E, const void* w, const void* w_scale, void* out, int out_dt, int64_t T, int64_t R,
                              int64_t N, int64_t K, hipStream_t stream);
+size_t moe_workspace(int64_t T, int64_t E, int64_t topk, int64_t I);
+hipError_t launch_moe_decode(const void* x, bool f16, const void* logits, int dt, int64_t ld, int score, const float* bias,
+                             int64_t G, int64_t topk_groups, int64_t group_top, int64_t topk, bool renorm, double scale,
+                             int fmt, const void* w13, const void* s13, const void* w2, const void* s2, int64_t group,
+                             const void* add, void* out, int64_t T, int64_t E, int64_t H, int64_t I, void* ws,
+                             hipStream_t stream);
 hipError_t launch_combine(const void* y, int dt, const int32_t* row_of, const float* weights, const void* add,
                           void* out, int64_t T, int64_t R, int64_t topk, int64_t N, hipStream_t stream);
 }  // namespace w4
@@ -764,15 +770,8 @@ int w4_route_workspace_bytes(int64_t T, int64_t E, int64_t topk, size_t* bytes) 
   return ok();
 }
 
-int w4_route(const void* logits, int logits_dtype, int64_t T, int64_t E, int64_t ld, int score, const float* bias,
-             int64_t n_groups, int64_t topk_groups, int64_t group_top, int64_t topk, int renorm, double scale,
-             int32_t* ids, float* weights, int32_t* row_token, int32_t* expert_offsets, int32_t* row_of,
-             void* workspace, size_t workspace_bytes, void* stream) {
-  const char* fn = "w4_route";
-  const int dt = float_index(logits_dtype);
-  if (dt < 0) return fail(W4_ERR_DTYPE, "%s: logits must be bf16, fp16 or fp32 (dtype code %d)", fn, logits_dtype);
-  int rc = check_route_sizes(fn, T, E, topk);
-  if (rc) return rc;
+static int check_route_choice(const char* fn, int64_t E, int score, int64_t n_groups, int64_t topk_groups,
+                              int64_t group_top) {
   if (score != W4_SCORE_SOFTMAX && score != W4_SCORE_SIGMOID)
     return fail(W4_ERR_INVALID, "%s: unknown score %d", fn, score);
   if (n_groups <= 0 || n_groups > 64 || E % n_groups)
@@ -783,6 +782,20 @@ int w4_route(const void* logits, int logits_dtype, int64_t T, int64_t E, int64_t
                 (long long)n_groups);
   if (group_top != 1 && group_top != 2)
     return fail(W4_ERR_UNSUPPORTED, "%s: group_top=%lld must be 1 or 2", fn, (long long)group_top);
+  return W4_OK;
+}
+
+int w4_route(const void* logits, int logits_dtype, int64_t T, int64_t E, int64_t ld, int score, const float* bias,
+             int64_t n_groups, int64_t topk_groups, int64_t group_top, int64_t topk, int renorm, double scale,
+             int32_t* ids, float* weights, int32_t* row_token, int32_t* expert_offsets, int32_t* row_of,
+             void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "w4_route";
+  const int dt = float_index(logits_dtype);
+  if (dt < 0) return fail(W4_ERR_DTYPE, "%s: logits must be bf16, fp16 or fp32 (dtype code %d)", fn, logits_dtype);
+  int rc = check_route_sizes(fn, T, E, topk);
+  if (rc) return rc;
+  rc = check_route_choice(fn, E, score, n_groups, topk_groups, group_top);
+  if (rc) return rc;
   if (ld < E) return fail(W4_ERR_ALIGN, "%s: ld=%lld must be >= E=%lld", fn, (long long)ld, (long long)E);
   if (!expert_offsets || (T > 0 && (!logits || !ids || !weights || !row_token || !row_of)))
     return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
@@ -1096,6 +1109,77 @@ int w4_mxfp4_grouped_gemm(const void* a, const void* a_scale, const int32_t* row
   if (!aligned4(a_scale) || !aligned4(w_scale)) return fail(W4_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
   return hip_status(w4::launch_mx_grouped(a, a_scale, row_token, expert_offsets, E, w, w_scale, out,
                                           float_index(out_dtype), T, R, N, K, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+// ---- the whole layer for a few tokens
+
+static int check_moe_sizes(const char* fn, int64_t T, int64_t E, int64_t topk, int64_t H, int64_t I) {
+  int rc = check_route_sizes(fn, T, E, topk);
+  if (rc) return rc;
+  if (H <= 0 || I <= 0)
+    return fail(W4_ERR_INVALID, "%s: sizes must be H > 0, I > 0 (got H=%lld I=%lld)", fn, (long long)H, (long long)I);
+  if (H % 32 || I % 32)
+    return fail(W4_ERR_ALIGN, "%s: H=%lld and I=%lld must be multiples of 32", fn, (long long)H, (long long)I);
+  // the middle's rows are addressed with 32-bit offsets, and a launch takes fewer than 2^32 threads
+  if (T > W4_MOE_DECODE_MAX_TOKENS || H > ((int64_t)1 << 22) || I > ((int64_t)1 << 22) || T * topk * I > ((int64_t)1 << 27))
+    return fail(W4_ERR_UNSUPPORTED, "%s: T=%lld H=%lld I=%lld topk=%lld outside T <= %d, H, I <= 2^22, T*topk*I <= 2^27", fn,
+                (long long)T, (long long)H, (long long)I, (long long)topk, W4_MOE_DECODE_MAX_TOKENS);
+  return W4_OK;
+}
+
+int w4_moe_decode_workspace_bytes(int64_t T, int64_t E, int64_t topk, int64_t H, int64_t I, size_t* bytes) {
+  const char* fn = "w4_moe_decode_workspace_bytes";
+  if (!bytes) return fail(W4_ERR_INVALID, "%s: null output pointer", fn);
+  int rc = check_moe_sizes(fn, T, E, topk, H, I);
+  if (rc) return rc;
+  *bytes = w4::moe_workspace(T, E, topk, I);
+  return ok();
+}
+
+int w4_moe_decode(const void* x, int x_dtype, const void* logits, int logits_dtype, int64_t ld, int score, const float* bias,
+                  int64_t n_groups, int64_t topk_groups, int64_t group_top, int64_t topk, int renorm, double scale,
+                  int w_format, const void* w13, const void* w13_scale, const void* w2, const void* w2_scale, int64_t group,
+                  const void* add, void* out, int64_t T, int64_t E, int64_t H, int64_t I, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  const char* fn = "w4_moe_decode";
+  if (x_dtype != W4_BF16 && x_dtype != W4_F16)
+    return fail(W4_ERR_DTYPE, "%s: activations must be bf16 or fp16 (dtype code %d)", fn, x_dtype);
+  const int dt = float_index(logits_dtype);
+  if (dt < 0) return fail(W4_ERR_DTYPE, "%s: logits must be bf16, fp16 or fp32 (dtype code %d)", fn, logits_dtype);
+  if (w_format != W4_MOE_FP8_BLOCK && w_format != W4_MOE_MXFP4 && w_format != W4_MOE_INT4)
+    return fail(W4_ERR_INVALID, "%s: unknown weight format %d", fn, w_format);
+  int rc = check_moe_sizes(fn, T, E, topk, H, I);
+  if (!rc) rc = check_route_choice(fn, E, score, n_groups, topk_groups, group_top);
+  if (rc) return rc;
+  if (w_format == W4_MOE_INT4) {
+    if (H % 128 || I % 128)
+      return fail(W4_ERR_ALIGN, "%s: int4 weights need H=%lld and I=%lld to be multiples of 128", fn, (long long)H,
+                  (long long)I);
+    if (group != -1 && (group <= 0 || group % 128 || H % group || I % group))
+      return fail(W4_ERR_GROUP, "%s: group size %lld must be -1 (per channel) or a multiple of 128 dividing H=%lld and I=%lld",
+                  fn, (long long)group, (long long)H, (long long)I);
+  }
+  if (ld < E) return fail(W4_ERR_ALIGN, "%s: ld=%lld must be >= E=%lld", fn, (long long)ld, (long long)E);
+  if (T == 0) return ok();
+  if (!x || !logits || !w13 || !w13_scale || !w2 || !w2_scale || !out)
+    return fail(W4_ERR_INVALID, "%s: null pointer argument", fn);
+  if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(add) || !aligned16(out))
+    return fail(W4_ERR_ALIGN, "%s: x, w13, w2, add and out must be 16-byte aligned", fn);
+  if ((reinterpret_cast<uintptr_t>(w13_scale) & 7u) || (reinterpret_cast<uintptr_t>(w2_scale) & 7u))
+    return fail(W4_ERR_ALIGN, "%s: scales must be 8-byte aligned", fn);
+  if ((reinterpret_cast<uintptr_t>(logits) & (dt == 2 ? 3u : 1u)) != 0)
+    return fail(W4_ERR_ALIGN, "%s: logits must be aligned to their type", fn);
+  const size_t need = w4::moe_workspace(T, E, topk, I);
+  if (workspace_bytes < need || !workspace)
+    return fail(W4_ERR_INVALID, "%s: workspace of %zu bytes is smaller than the %zu needed for T=%lld E=%lld topk=%lld I=%lld",
+                fn, workspace_bytes, need, (long long)T, (long long)E, (long long)topk, (long long)I);
+  if (!aligned16(workspace)) return fail(W4_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  return hip_status(w4::launch_moe_decode(x, x_dtype == W4_F16, logits, dt, ld, score == W4_SCORE_SIGMOID ? 1 : 0, bias,
+                                          n_groups, topk_groups, group_top, topk, renorm != 0, scale,
+                                          w_format - W4_MOE_FP8_BLOCK, w13, w13_scale, w2, w2_scale,
+                                          w_format == W4_MOE_INT4 ? group : -1, add, out, T, E, H, I, workspace,
+                                          static_cast<hipStream_t>(stream)),
                     fn);
 }
 

@@ -32,93 +32,13 @@
 // reads passes 128 MiB a kernel between them scans the counts (64 experts: 16384
 // tokens 12 us summed, 18 scanned, 65536 36 and 52; 256 experts: 32768 tokens
 // 36 and 42, 65536 79 and 73, 131072 210 and 140).
-#include "w4_device.h"
+#include "route_token.h"
 
 namespace w4 {
 
 constexpr int kTok = 64;                 // tokens per block
 constexpr int kRThreads = 1024;
 constexpr int kRWaves = kRThreads / kWave;
-constexpr int kMaxE = 1024;
-
-struct RouteArgs {
-  const void* x;
-  const float* bias;
-  int64_t T, ld;
-  int E, topk, G, per_group, topk_groups, group_top, score, renorm;
-  double scale;
-  int32_t *ids, *row_token, *offsets, *row_of;
-  float* weights;
-  uint8_t* counts;                       // [blocks][ceil(E / 4) * 4]; null: one block
-  int32_t* prefix;                       // where the counts are scanned: those before each block [blocks][E], totals [E]
-  int vec;                               // rows of logits are aligned for whole-lane loads
-};
-
-// All lanes' best of L consecutive lanes (16: DPP inside a row of 16; 64: two
-// exchanges more), op(own, other).
-template <int CTRL>
-__device__ __forceinline__ int dpp(int v) { return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false); }
-template <int CTRL>
-__device__ __forceinline__ double dpp(double v) {
-  const long long b = __double_as_longlong(v);
-  const uint32_t lo = (uint32_t)dpp<CTRL>((int)b), hi = (uint32_t)dpp<CTRL>((int)(b >> 32));
-  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) { return __int_as_float(dpp<CTRL>(__float_as_int(v))); }
-
-template <int L, typename T, typename F>
-__device__ __forceinline__ T lanes_reduce(T v, F op) {
-  v = op(v, dpp<0xB1>(v));               // lane ^ 1
-  v = op(v, dpp<0x4E>(v));               // lane ^ 2
-  v = op(v, dpp<0x141>(v));              // mirror of 8 lanes: the other four
-  v = op(v, dpp<0x140>(v));              // mirror of 16: the other eight
-  if constexpr (L == 64) {
-    v = op(v, __shfl_xor(v, 16, kWave));
-    v = op(v, __shfl_xor(v, 32, kWave));
-  }
-  return v;
-}
-template <int L>
-__device__ __forceinline__ double lanes_sum(double v) {
-  return lanes_reduce<L>(v, [](double a, double b) { return a + b; });
-}
-
-// The best (largest key, then lowest id) of the wave.
-template <int CTRL>
-__device__ __forceinline__ void best_step(double& key, int& id) {
-  const double o = dpp<CTRL>(key);
-  const int oi = dpp<CTRL>(id);
-  if (o > key || (o == key && oi < id)) {
-    key = o;
-    id = oi;
-  }
-}
-__device__ __forceinline__ void wave_best(double& key, int& id) {
-  best_step<0xB1>(key, id);
-  best_step<0x4E>(key, id);
-  best_step<0x141>(key, id);
-  best_step<0x140>(key, id);
-#pragma unroll
-  for (int off = 16; off <= 32; off <<= 1) {
-    const double o = __shfl_xor(key, off, kWave);
-    const int oi = __shfl_xor(id, off, kWave);
-    if (o > key || (o == key && oi < id)) {
-      key = o;
-      id = oi;
-    }
-  }
-}
-
-constexpr float kF32Max = 3.40282347e38f;
-
-template <int DT>
-__device__ __forceinline__ float load_logit(const void* x, int64_t i) {
-  if constexpr (DT == 2) return static_cast<const float*>(x)[i];
-  const uint16_t v = static_cast<const uint16_t*>(x)[i];
-  return DT == 0 ? bf16_to_f32(v) : f16_to_f32(v);
-}
-
 // Inclusive sum over the wave.
 __device__ __forceinline__ int wave_scan(int v, int lane) {
 #pragma unroll
@@ -146,10 +66,6 @@ __device__ __forceinline__ int block_scan(int v, int* red, int& total) {
   __syncthreads();
   total = sum;
   return before + inc - v;
-}
-
-__device__ __forceinline__ double score_of(float x, int score, float top) {
-  return score == 0 ? exp((double)x - (double)top) : 1.0 / (1.0 + exp(-(double)x));
 }
 
 // Place the rows of this block's tokens. mask[e]: the block's tokens that
@@ -367,115 +283,13 @@ __global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * kTok;
   const int tokens = (int)min((int64_t)kTok, a.T - t0);
-  const double kLow = -__builtin_inf();
-
-  float bias[V];
-  int group[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = j * 64 + lane;
-    bias[j] = (GENERAL && a.bias && e < a.E) ? a.bias[e] : 0.f;
-    group[j] = GENERAL ? e / a.per_group : 0;
-  }
+  const LaneExperts<V, GENERAL> own(a, lane);
   for (int tl = wave; tl < tokens; tl += kRWaves) {
     const int64_t t = t0 + tl;
-    float x[V];
-    float top = -__builtin_inff();
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int e = j * 64 + lane;
-      const float v = e < a.E ? load_logit<DT>(a.x, t * a.ld + e) : -__builtin_inff();
-      x[j] = v > -__builtin_inff() ? fminf(v, kF32Max) : -__builtin_inff();   // NaN: closed
-      top = fmaxf(top, x[j]);
-    }
-    top = wave_max(top);
-    if (!(top > -__builtin_inff())) top = 0.f;         // every expert closed: no p is used
-    double sum = 1.0;
-    double key[V];
-    if (GENERAL || (a.score == 0 && !a.renorm)) {
-      double part = 0.0;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const double p = x[j] > -__builtin_inff() ? score_of(x[j], a.score, top) : 0.0;
-        key[j] = p;
-        part += p;
-      }
-      if (a.score == 0) sum = fmax(lanes_sum<64>(part), 1e-300);
-    }
-    if constexpr (GENERAL) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const double c = key[j] / sum + (double)bias[j];
-        key[j] = (x[j] > -__builtin_inff() && c > kLow) ? c : kLow;    // a NaN or -inf bias closes its expert
-      }
-      if (a.G > 1) {
-        // lane group g of LG lanes takes expert group g
-        double* mine = s_c + wave * a.E;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (j * 64 + lane < a.E) mine[j * 64 + lane] = key[j];
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_s_waitcnt(0xC07F);
-        int LG = 1;
-        while (2 * LG * a.G <= 64) LG *= 2;
-        const int g = lane / LG;
-        double b0 = kLow, b1 = kLow;
-        if (g < a.G)
-          for (int i = lane & (LG - 1); i < a.per_group; i += LG) {
-            const double c = mine[g * a.per_group + i];
-            b1 = fmax(b1, fmin(b0, c));
-            b0 = fmax(b0, c);
-          }
-        for (int off = 1; off < LG; off <<= 1) {
-          const double o0 = __shfl_xor(b0, off, kWave), o1 = __shfl_xor(b1, off, kWave);
-          b1 = fmax(fmax(b1, o1), fmin(b0, o0));
-          b0 = fmax(b0, o0);
-        }
-        const double value = (a.group_top == 2 && b1 > kLow) ? b0 + b1 : b0;
-        int before = 0;                                  // groups that rank before this lane's
-        for (int h = 0; h < a.G; ++h) {
-          const double o = __shfl(value, h * LG, kWave);
-          before += (o > value || (o == value && h < g)) ? 1 : 0;
-        }
-        const unsigned long long kept = __ballot(g < a.G && before < a.topk_groups);
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (group[j] < a.G && !((kept >> (group[j] * LG)) & 1)) key[j] = kLow;
-      }
-      if (!a.bias) {                                     // the key is the logit itself
-#pragma unroll
-        for (int j = 0; j < V; ++j) key[j] = key[j] > kLow ? (double)x[j] : kLow;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) key[j] = (double)x[j];
-    }
-    // topk rounds of argmax; lane i keeps the i-th choice
-    int my_id = -1;
-    for (int i = 0; i < a.topk; ++i) {
-      double best = kLow;
-      int id = 0x7FFFFFFF;
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (key[j] > best) {
-          best = key[j];
-          id = j * 64 + lane;
-        }
-      wave_best(best, id);
-      if (!(best > kLow)) break;                         // nothing left (uniform)
-      if (lane == i) my_id = id;
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (id == j * 64 + lane) key[j] = kLow;
-    }
-    double w = 0.0;
-    if (my_id >= 0) {
-      const float xi = fminf(load_logit<DT>(a.x, t * a.ld + my_id), kF32Max);
-      w = score_of(xi, a.score, top) / sum;
-      atomicOr(&mask[my_id], 1ull << tl);
-    }
-    if (a.renorm) w = w / fmax(lanes_sum<64>(w), 1e-300);
+    int my_id;
+    double w;
+    route_token<DT, V, GENERAL>(a, t, lane, own, s_c + wave * a.E, my_id, w);
+    if (my_id >= 0) atomicOr(&mask[my_id], 1ull << tl);
     if (lane < a.topk) {
       a.ids[t * a.topk + lane] = my_id;
       a.weights[t * a.topk + lane] = (float)(w * a.scale);
@@ -599,7 +413,7 @@ hipError_t launch_route(const void* x, int dt, int64_t T, int64_t E, int64_t ld,
   RouteArgs a;
   a.x = x; a.bias = bias; a.T = T; a.ld = ld;
   a.E = (int)E; a.topk = (int)topk; a.G = (int)G; a.per_group = (int)(E / G);
-  a.topk_groups = (int)topk_groups; a.group_top = (int)group_top; a.score = score; a.renorm = renorm ? 1 : 0;
+  a.topk_groups = (int)topk_groups; a.group_top = (int)group_top; a.score = score; a.renorm = renorm ? 1 : 0; a.dt = dt;
   a.scale = scale;
   a.ids = ids; a.row_token = row_token; a.offsets = offsets; a.row_of = row_of; a.weights = weights;
   a.counts = nb <= 1 ? nullptr : static_cast<uint8_t*>(ws);

@@ -16,16 +16,21 @@ from . import ops
 
 class Fp8Experts:
     """w13 [E, 2 I, H] (gate rows, then up rows) and w2 [E, H, I] E4M3 codes, w13_scale [E, ceil(2I/128), ceil(H/128)] and
-    w2_scale [E, ceil(H/128), ceil(I/128)] fp32. `routing` goes to ops.w4_route (score, bias, n_groups, ...)."""
+    w2_scale [E, ceil(H/128), ceil(I/128)] fp32. `routing` goes to ops.w4_route (score, bias, n_groups, ...). Up to
+    `decode_tokens` tokens (at most W4_MOE_DECODE_MAX_TOKENS) run as one call, ops.w4_moe_decode, which does not quantize
+    the activations: none unless asked for."""
 
-    def __init__(self, w13, w13_scale, w2, w2_scale, topk: int, max_tokens: int, dtype=torch.bfloat16, **routing):
+    def __init__(self, w13, w13_scale, w2, w2_scale, topk: int, max_tokens: int, dtype=torch.bfloat16,
+                 decode_tokens: int = 0, **routing):
         E, H, I = w2.shape
         if tuple(w13.shape) != (E, 2 * I, H):
             raise ValueError(f"w13 must be [{E}, {2 * I}, {H}] for w2 {tuple(w2.shape)}, got {tuple(w13.shape)}")
+        if not 0 <= decode_tokens <= ops.W4_MOE_DECODE_MAX_TOKENS:
+            raise ValueError(f"decode_tokens={decode_tokens} outside 0..{ops.W4_MOE_DECODE_MAX_TOKENS}")
         dev = w13.device
         self.w13, self.w13_scale, self.w2, self.w2_scale = w13, w13_scale, w2, w2_scale
         self.topk, self.max_tokens, self.dtype, self.routing = topk, max_tokens, dtype, routing
-        self.E, self.H, self.I = E, H, I
+        self.E, self.H, self.I, self.decode_tokens = E, H, I, min(decode_tokens, max_tokens)
         rows = max_tokens * topk
 
         def buf(*shape, dt):
@@ -38,6 +43,8 @@ class Fp8Experts:
         self._a, self._as = buf(rows, I, dt=u8), buf(rows, -(-I // 128), dt=f32)
         self._y = buf(rows, H, dt=dtype)
         self._ws = ops.w4_route_workspace(max_tokens, E, topk, device=dev)
+        if self.decode_tokens:
+            self._decode_ws = ops.w4_moe_decode_workspace(self.decode_tokens, E, topk, H, I, device=dev)
 
     def __call__(self, x, logits, add=None, out=None, stream=None):
         """x [T, H] in the layer's type, logits [T, E] -> [T, H] (+ add [T, H]). The layer's buffers are reused by the
@@ -45,6 +52,9 @@ class Fp8Experts:
         T = x.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens exceed max_tokens={self.max_tokens}")
+        if T and T <= self.decode_tokens:
+            return ops.w4_moe_decode(x, logits, self.topk, self.w13, self.w13_scale, self.w2, self.w2_scale, add=add, out=out,
+                                     workspace=self._decode_ws, stream=stream, **self.routing)
         R = T * self.topk
         plan = (self._ids[:T], self._weights[:T], self._row_token[:R], self._offsets, self._row_of[:T])
         _, weights, row_token, offsets, row_of = ops.w4_route(
@@ -73,7 +83,8 @@ def random_experts(E: int, H: int, I: int, topk: int, max_tokens: int, seed: int
 def main():
     E, H, I, topk = 64, 7168, 2048, 8
     layer = random_experts(E, H, I, topk, 8192)
-    for T in (1, 8, 64, 512, 8192):
+    decode = Fp8Experts(layer.w13, layer.w13_scale, layer.w2, layer.w2_scale, topk, 32, decode_tokens=32)
+    for layer, T in [(layer, T) for T in (1, 8, 64, 512, 8192)] + [(decode, T) for T in (1, 8, 32)]:
         x = torch.randn((T, H), device="cuda").bfloat16()
         logits = torch.randn((T, E), device="cuda")
         out = torch.empty_like(x)
@@ -85,8 +96,8 @@ def main():
             layer(x, logits, out=out)
         end.record()
         torch.cuda.synchronize()
-        print(f"{T} tokens: {start.elapsed_time(end) * 100:.0f} us  ({E} experts, hidden {H}, intermediate {I}, "
-              f"top {topk})", flush=True)
+        print(f"{T} tokens{', activations not quantized' if layer is decode else ''}: {start.elapsed_time(end) * 100:.0f} us  "
+              f"({E} experts, hidden {H}, intermediate {I}, top {topk})", flush=True)
 
 
 if __name__ == "__main__":

@@ -65,6 +65,9 @@ _SIGS = {
     "w4_mxfp4_linear_workspace_bytes": [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
     "w4_mxfp4_linear": [_P, _I, _P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P],
     "w4_mxfp4_grouped_gemm": [_P, _P, _P, _P, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _P],
+    "w4_moe_decode_workspace_bytes": [_I64, _I64, _I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "w4_moe_decode": [_P, _I, _P, _I, _I64, _I, _P, _I64, _I64, _I64, _I64, _I, ctypes.c_double, _I, _P, _P, _P, _P, _I64,
+                      _P, _P, _I64, _I64, _I64, _I64, _P, ctypes.c_size_t, _P],
     "w4_last_error": [],
     "w4_version": [],
 }
@@ -726,4 +729,73 @@ def w4_mxfp4_grouped_gemm(a, a_scale, row_token, expert_offsets, w, w_scale, out
     p_out = _arg(out, out.dtype, (R, N), "out")
     _call("w4_mxfp4_grouped_gemm",
         p_a, p_as, p_token, p_off, E, p_w, p_ws, p_out, _half_code(out.dtype), T, R, N, K, _stream(stream))
+    return out
+
+
+# ----------------------------------------------------------------- the whole layer for a few tokens
+
+W4_MOE_DECODE_MAX_TOKENS = 32            # include/w4.h
+W4_MOE_FORMATS = {"fp8_block": 1, "mxfp4": 2, "int4": 3}
+
+
+def w4_moe_decode_workspace(T: int, E: int, topk: int, H: int, I: int, device="cuda", stream=None) -> torch.Tensor:
+    """Device scratch for w4_moe_decode at these sizes (uint8, possibly empty), for use on `stream`."""
+    n = ctypes.c_size_t(0)
+    _check("w4_moe_decode_workspace_bytes", lib().w4_moe_decode_workspace_bytes(T, E, topk, H, I, ctypes.byref(n)))
+    return _new((n.value,), torch.uint8, device, stream)
+
+
+def w4_moe_decode(x, logits, topk: int, w13, w13_scale, w2, w2_scale, fmt: str = "fp8_block", score: str = "softmax",
+                  bias=None, n_groups: int = 1, topk_groups: int = 1, group_top: int = 1, renorm: bool = True,
+                  scale: float = 1.0, add=None, out=None, workspace=None, stream=None):
+    """The expert layer of at most W4_MOE_DECODE_MAX_TOKENS tokens: x [T, H] bf16/fp16 and logits [T, E] -> [T, H]
+    (+ add [T, H]); include/w4.h has the definition, w4_route the routing arguments. Weights by `fmt`:
+    "fp8_block": w13 [E, 2I, H] and w2 [E, H, I] E4M3 codes, scales fp32 [E, ceil(2I/128), ceil(H/128)] and
+    [E, ceil(H/128), ceil(I/128)];
+    "mxfp4": w13 uint8 [E, 2I, H/2], w2 uint8 [E, H, I/2], scales uint8 [E, 2I, 4 ceil(H/128)], [E, H, 4 ceil(I/128)];
+    "int4": w13 and w2 from w4_repack (batch = E), scales fp16 [E, G, 2I] and [E, G, H] with G = H / group and I / group
+    (one group of 128 m for both), or 1 and 1 per channel."""
+    if fmt not in W4_MOE_FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(W4_MOE_FORMATS)}, got {fmt!r}")
+    if score not in W4_SCORES:
+        raise ValueError(f"score must be one of {sorted(W4_SCORES)}, got {score!r}")
+    (T, H), E = x.shape, logits.shape[1]
+    ptr, ld = _rows_ptr(logits, "logits")
+    group = -1
+    if fmt == "int4":
+        I = w13_scale.shape[2] // 2
+        G13, G2 = w13_scale.shape[1], w2_scale.shape[1]
+        if (G13, G2) != (1, 1):
+            group = H // G13 if G13 else 0
+            if group <= 0 or G13 * group != H or G2 * group != I:
+                raise ValueError(f"w13_scale and w2_scale must share a group along H={H} and I={I}: got {G13} and {G2} groups")
+        p_w13 = _arg(w13, torch.uint8, (E, w4_repack_bytes(H, 2 * I)), "w13")
+        p_w2 = _arg(w2, torch.uint8, (E, w4_repack_bytes(I, H)), "w2")
+        p_s13 = _arg(w13_scale, torch.float16, (E, G13, 2 * I), "w13_scale")
+        p_s2 = _arg(w2_scale, torch.float16, (E, G2, H), "w2_scale")
+    elif fmt == "mxfp4":
+        I = 2 * w2.shape[2]
+        p_w13 = _arg(w13, torch.uint8, (E, 2 * I, H // 2), "w13")
+        p_w2 = _arg(w2, torch.uint8, (E, H, I // 2), "w2")
+        p_s13 = _arg(w13_scale, torch.uint8, (E, 2 * I, _mx_row(H)), "w13_scale")
+        p_s2 = _arg(w2_scale, torch.uint8, (E, H, _mx_row(I)), "w2_scale")
+    else:
+        I = w2.shape[2]
+        HB, IB = (H + 127) // 128, (I + 127) // 128
+        p_w13 = _arg(_e4m3_codes(w13, "w13"), w13.dtype, (E, 2 * I, H), "w13")
+        p_w2 = _arg(_e4m3_codes(w2, "w2"), w2.dtype, (E, H, I), "w2")
+        p_s13 = _arg(w13_scale, torch.float32, (E, (2 * I + 127) // 128, HB), "w13_scale")
+        p_s2 = _arg(w2_scale, torch.float32, (E, HB, IB), "w2_scale")
+    if logits.shape[0] != T:
+        raise ValueError(f"logits have {logits.shape[0]} rows, x {T}")
+    if out is None:
+        out = _new((T, H), x.dtype, x.device, stream)
+    p_bias = _arg(bias, torch.float32, (E,), "bias")
+    p_add, p_out = _arg(add, x.dtype, (T, H), "add"), _arg(out, x.dtype, (T, H), "out")
+    if workspace is None:
+        workspace = w4_moe_decode_workspace(T, E, topk, H, I, x.device, stream)
+    _call("w4_moe_decode",
+        _arg(x, x.dtype, (T, H), "x"), _half_code(x.dtype), ptr, _float_code(logits.dtype), ld, W4_SCORES[score], p_bias,
+        n_groups, topk_groups, group_top, topk, int(renorm), scale, W4_MOE_FORMATS[fmt], p_w13, p_s13, p_w2, p_s2, group,
+        p_add, p_out, T, E, H, I, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     return out

@@ -91,28 +91,33 @@ def int4_values(q, scale, group):
     return q * np.repeat(np.swapaxes(np.asarray(scale, dtype=np.float64), -1, -2), K if group == -1 else group, -1)
 
 
-def moe(x, logits, topk, w13, w2, add=None, **routing):
-    """The layer in 64 bits on weights given as values: w13 [E, 2 I, H], w2 [E, H, I]. Returns the output, and the sum of
-    the magnitudes that its tolerances count: of the middle's products and of the output's."""
+def moe(x, logits, topk, w13, w2, add=None, w13_size=None, w2_size=None, **routing):
+    """The layer in 64 bits on weights given as values: w13 [E, 2 I, H], w2 [E, H, I]. Returns the output and two
+    magnitudes for its tolerance: how far the output moves per relative error of the first products' terms, and the sum
+    of the second's terms. `w13_size`, `w2_size`: what the terms' weights count there, |w13| and |w2| if not given."""
     ids, weights = route(logits, topk, **routing)
     T, H = x.shape
-    y, mag = np.zeros((T, H)), np.zeros((T, H))
+    I = w2.shape[2]
+    y, first, second = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
     for t in range(T):
         for j in range(topk):
             e = ids[t, j]
             if e < 0:
                 continue
-            I = w2.shape[2]
+            size13 = np.abs(w13[e]) if w13_size is None else w13_size[e]
+            size2 = np.abs(w2[e]) if w2_size is None else w2_size[e]
             up = w13[e] @ x[t]
-            upm = np.abs(w13[e]) @ np.abs(x[t])
+            upm = size13 @ np.abs(x[t])
             g, u = up[:I], up[I:]
             with np.errstate(over="ignore", invalid="ignore"):
                 s = 1.0 / (1.0 + np.exp(-g))
             mid = g * s * u * weights[t, j]
-            # how far the middle moves when its factors do: |d silu| <= 1.1 |dg|
-            midm = np.abs(weights[t, j]) * (1.1 * upm[:I] * np.abs(u) + np.abs(g * s) * upm[I:])
+            # the slope of silu is at most 1.1
+            moved = np.abs(weights[t, j]) * (1.1 * upm[:I] * np.abs(u) + np.abs(g * s) * upm[I:])
             y[t] += w2[e] @ mid
-            mag[t] += np.abs(w2[e]) @ midm
+            first[t] += size2 @ moved
+            second[t] += size2 @ np.abs(mid)
     if add is not None:
         y = y + add
-    return y, mag
+        second = second + np.abs(add)
+    return y, first, second

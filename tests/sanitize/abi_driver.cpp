@@ -156,6 +156,37 @@ int main() {
   expect(w4_combine(p, W4_BF16, ip, fp, nullptr, p, 4, 8, 2, 252, nullptr), W4_ERR_ALIGN, "cb N");
   expect(w4_combine(p, W4_BF16, ip, fp, odd, p, 4, 8, 2, 256, nullptr), W4_ERR_ALIGN, "cb add");
   expect(w4_combine(nullptr, W4_BF16, nullptr, nullptr, nullptr, nullptr, 0, 8, 2, 256, nullptr), W4_OK, "cb empty");
+  // MXFP4
+  const int64_t big = (int64_t)1 << 62;
+  expect(w4_mxfp4_quantize(p, W4_I8, 4, 256, 256, W4_ACT_NONE, p, p, nullptr), W4_ERR_DTYPE, "mq dt");
+  expect(w4_mxfp4_quantize(p, W4_BF16, 4, 240, 240, W4_ACT_NONE, p, p, nullptr), W4_ERR_ALIGN, "mq K");
+  expect(w4_mxfp4_quantize(p, W4_F32, big, 256, 256, W4_ACT_NONE, p, p, nullptr), W4_ERR_UNSUPPORTED, "mq M");
+  expect(w4_mxfp4_quantize(odd, W4_BF16, 4, 256, 256, W4_ACT_NONE, p, p, nullptr), W4_ERR_ALIGN, "mq x");
+  expect(w4_mxfp4_quantize(nullptr, W4_BF16, 0, 256, 256, W4_ACT_NONE, nullptr, nullptr, nullptr), W4_OK, "mq empty");
+  expect(w4_mxfp4_dequantize(p, p, 4, 256, p, W4_I8, nullptr), W4_ERR_DTYPE, "md dt");
+  expect(w4_mxfp4_dequantize(p, p, 4, 100, p, W4_F32, nullptr), W4_ERR_ALIGN, "md K");
+  expect(w4_mxfp4_dequantize(p, nullptr, 4, 256, p, W4_F32, nullptr), W4_ERR_INVALID, "md null");
+  expect(w4_mxfp4_gemm_workspace_bytes(1, 256, 4096, nullptr), W4_ERR_INVALID, "mw null");
+  expect(w4_mxfp4_gemm_workspace_bytes(big, 256, 4096, &n), W4_ERR_UNSUPPORTED, "mw M");
+  expect(w4_mxfp4_gemm_workspace_bytes((int64_t)1 << 30, (int64_t)1 << 30, 4096, &n), W4_ERR_UNSUPPORTED, "mw threads");
+  expect(w4_mxfp4_gemm(p, p, p, p, nullptr, p, W4_I8, 4, 256, 256, nullptr, 0, nullptr), W4_ERR_DTYPE, "mg dt");
+  expect(w4_mxfp4_gemm(p, p, p, p, nullptr, p, W4_BF16, 4, 256, 272, nullptr, 0, nullptr), W4_ERR_ALIGN, "mg K");
+  expect(w4_mxfp4_gemm(p, (uint8_t*)p + 2, p, p, nullptr, p, W4_BF16, 4, 256, 256, nullptr, 0, nullptr), W4_ERR_ALIGN, "mg as");
+  expect(w4_mxfp4_gemm(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, W4_BF16, 0, 256, 256, nullptr, 0, nullptr), W4_OK, "mg empty");
+  expect(w4_mxfp4_linear_workspace_bytes(100, 256, 4096, nullptr), W4_ERR_INVALID, "mlw null");
+  expect(w4_mxfp4_linear_workspace_bytes(big, 256, 4096, &n), W4_ERR_UNSUPPORTED, "mlw M");
+  expect(w4_mxfp4_linear(p, W4_F32, p, p, nullptr, p, 4, 256, 256, nullptr, 0, nullptr), W4_ERR_DTYPE, "ml dt");
+  expect(w4_mxfp4_linear(p, W4_BF16, p, p, nullptr, p, 100, 256, 256, nullptr, 0, nullptr), W4_ERR_INVALID, "ml ws");
+  expect(w4_mxfp4_grouped_gemm(p, p, ip, ip, 4, p, p, p, W4_F32, 8, 64, 256, 256, nullptr), W4_ERR_DTYPE, "mgg dt");
+  expect(w4_mxfp4_grouped_gemm(p, p, ip, ip, 4, p, p, p, W4_BF16, 1 << 20, 64, 256, 4096, nullptr), W4_ERR_UNSUPPORTED, "mgg T*K");
+  expect(w4_mxfp4_grouped_gemm(p, p, nullptr, ip, 4, p, p, p, W4_BF16, 8, 64, 256, 256, nullptr), W4_ERR_INVALID, "mgg rows");
+  // the whole layer for a few tokens
+  expect(w4_moe_decode_workspace_bytes(1, 64, 8, 256, 256, nullptr), W4_ERR_INVALID, "mdw null");
+  expect(w4_moe_decode_workspace_bytes(1, 64, 8, big, big, &n), W4_ERR_UNSUPPORTED, "mdw H");
+  expect(w4_moe_decode(p, W4_F32, p, W4_F32, 64, W4_SCORE_SOFTMAX, nullptr, 1, 1, 1, 8, 1, 1.0, W4_MOE_MXFP4, p, p, p, p, -1, nullptr, p, 4, 64, 256, 256, p, 1 << 30, nullptr), W4_ERR_DTYPE, "moe dt");
+  expect(w4_moe_decode(p, W4_BF16, p, W4_F32, 64, W4_SCORE_SOFTMAX, nullptr, 1, 1, 1, 8, 1, 1.0, W4_MOE_INT4, p, p, p, p, 96, nullptr, p, 4, 64, 256, 256, p, 1 << 30, nullptr), W4_ERR_GROUP, "moe group");
+  expect(w4_moe_decode(p, W4_BF16, p, W4_F32, 64, W4_SCORE_SOFTMAX, nullptr, 1, 1, 1, 8, 1, 1.0, W4_MOE_MXFP4, p, p, p, p, -1, nullptr, p, 4, 64, 256, 256, p, 16, nullptr), W4_ERR_INVALID, "moe ws");
+  expect(w4_moe_decode(nullptr, W4_BF16, nullptr, W4_F32, 64, W4_SCORE_SOFTMAX, nullptr, 1, 1, 1, 8, 1, 1.0, W4_MOE_MXFP4, nullptr, nullptr, nullptr, nullptr, -1, nullptr, nullptr, 0, 64, 256, 256, nullptr, 0, nullptr), W4_OK, "moe empty");
   // the longest message paths: every argument named, sizes at their widest
   expect(w4a8_gemm((const int8_t*)p, (const float*)p, p, p, W4_F16, 128, nullptr, p, W4_BF16, 4,
                    (int64_t)1 << 62 | 4, ((int64_t)1 << 62) | 12, nullptr), W4_ERR_UNSUPPORTED, "g huge");
