@@ -761,7 +761,7 @@ int w4_mxfp4_grouped_gemm(const void* a, const void* a_scale, const int32_t* row
  * others, through the order of its sum; values that are not finite stay in their
  * token's row).
  * Errors: INVALID, ALIGN, GROUP, DTYPE, UNSUPPORTED (T, E, topk, group_top; H or I
- *         above 2^22, T*topk*I above 2^27), HIP. T == 0 enqueues nothing.
+ *         above 2^22, H*I above 2^31, T*topk*I above 2^27), HIP. T == 0 enqueues nothing.
  */
 #define W4_MOE_DECODE_MAX_TOKENS 32
 int w4_moe_decode_workspace_bytes(int64_t T, int64_t E, int64_t topk, int64_t H, int64_t I, size_t* bytes);

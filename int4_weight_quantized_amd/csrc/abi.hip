@@ -1122,8 +1122,10 @@ static int check_moe_sizes(const char* fn, int64_t T, int64_t E, int64_t topk, i
   if (H % 32 || I % 32)
     return fail(W4_ERR_ALIGN, "%s: H=%lld and I=%lld must be multiples of 32", fn, (long long)H, (long long)I);
   // the middle's rows are addressed with 32-bit offsets, and a launch takes fewer than 2^32 threads
-  if (T > W4_MOE_DECODE_MAX_TOKENS || H > ((int64_t)1 << 22) || I > ((int64_t)1 << 22) || T * topk * I > ((int64_t)1 << 27))
-    return fail(W4_ERR_UNSUPPORTED, "%s: T=%lld H=%lld I=%lld topk=%lld outside T <= %d, H, I <= 2^22, T*topk*I <= 2^27", fn,
+  if (T > W4_MOE_DECODE_MAX_TOKENS || H > ((int64_t)1 << 22) || I > ((int64_t)1 << 22) || H * I > ((int64_t)1 << 31) ||
+      T * topk * I > ((int64_t)1 << 27))
+    return fail(W4_ERR_UNSUPPORTED,
+                "%s: T=%lld H=%lld I=%lld topk=%lld outside T <= %d, H, I <= 2^22, H*I <= 2^31, T*topk*I <= 2^27", fn,
                 (long long)T, (long long)H, (long long)I, (long long)topk, W4_MOE_DECODE_MAX_TOKENS);
   return W4_OK;
 }

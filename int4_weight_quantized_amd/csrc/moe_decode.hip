@@ -6,21 +6,31 @@
 // With so few rows the time is the chosen experts' weights, each read once. Two
 // kernels: gate and up products with the activation, then the down products with
 // the sum over a token's experts. Up to kInline tokens the first one routes too,
-// every block for itself (a wave per token, a microsecond); more tokens are
-// routed by w4_route's kernel before it, once instead of once per block.
+// every block for itself (a wave per token); more tokens are routed by a block
+// before it, once instead of once per block.
 //
-// Both are streams of weights through the matrix unit, 16 weight rows as its A
-// operand, up to 16 tokens (RT times) as its B operand, nothing staged in LDS: a
-// weight byte is used by one wave only. Weights become bf16 (exactly, with MXFP4's
-// scale applied; a product with v_mfma_f32_16x16x32_bf16), or fp16 for fp16
-// activations of FP8 and int4 weights. A wave's K step is 128 columns, lane (row
-// l16, group g) holding 32 of them. FP8's and int4's scales multiply the sums of a
-// step or group.
+// The plan: pairs (token, expert) are rows, ordered by expert, then token. Tiles
+// of at most 8 (gate and up) or 4 (down) rows of an expert name it, their first
+// row and their tokens as bits.
 //
-// What lies between the two is rounded to 16 bits of mantissa: the sum of two bf16
-// numbers, each of which goes through the matrix unit (2^-17 relative, below what
-// the output's own rounding leaves visible). MXFP4 with fp16 activations takes x
-// apart in the same way, exactly (11 bits).
+// Both kernels stream weights through the matrix unit, 16 weight rows as its A
+// operand, a tile's rows as its B operand. Weights become bf16 (exactly, with
+// MXFP4's scale applied; v_mfma_f32_16x16x32_bf16), or fp16 for fp16 activations of
+// FP8 and int4 weights; FP8's and int4's scales multiply the sums of 128 columns.
+//
+// What a wave reads passes through a ring of its own in LDS, by LDS DMA: no wave
+// waits for another, and D steps are in flight without a register. Loading straight
+// into the matrix unit's layout (lane = row + 16 * column group) would touch 64
+// cache lines per load and cost the address unit 60 clocks where a DMA of 8 rows'
+// full lines costs 16 (measured); it bound such a kernel at 2 to 4 TB/s. Rows
+// lie in LDS with their 16-byte chunks permuted by the row, so that the reads of 8
+// rows touch 8 different chunks.
+//
+// What lies between the two is held to 16 bits of mantissa as the sum of two bf16
+// numbers (2^-17 relative, below what the output's own rounding leaves visible).
+// The matrix unit takes them in one go: columns 0..7 are 8 rows' first numbers,
+// columns 8..15 their second ones, added at the end. MXFP4 with fp16 activations
+// takes x apart in the same way, exactly (11 bits).
 #include <type_traits>
 
 #include "mxfp4.h"
@@ -31,13 +41,12 @@ namespace w4 {
 constexpr int kInline = 2;                           // tokens that the first kernel routes itself
 constexpr int kInlineE = 256;
 constexpr int kInlineRows = kInline * 64;
+constexpr int kUpRows = 8, kDownRows = 4;            // most rows of a tile
 enum { kFp8 = 0, kMx = 1, kInt4 = 2 };
 
-// The experts with rows: e, their first row in the plan, the mask of their tokens.
-struct MoeSlot {
-  int e, row0;
+struct MoeTile {
+  uint16_t e, row0;
   uint32_t tokens;
-  int pad;
 };
 
 struct MoeArgs {
@@ -48,14 +57,15 @@ struct MoeArgs {
   uint16_t* out;
   int T, E, topk, H, I;
   int G13, G2;                                       // int4: scale groups along K
-  int kg13, kg2;                                     // and K steps per group
+  int kg13, kg2;                                     // and steps per group
   int NT;                                            // column tiles of the launch
   int inl;                                           // the first kernel routes
   // workspace
-  int32_t* nslots;
-  MoeSlot* slots;
-  uint16_t *hi, *lo;                                 // [R][I]: the middle, as two bf16
-  RouteArgs route;                                   // ids .. row_of in the workspace too (not inl)
+  int32_t* counts;                                   // tiles of the first kernel, of the second
+  MoeTile *up, *down;
+  float* weights;                                    // of the rows
+  uint16_t* mid;                                     // [2][R][I]: the middle, as two bf16
+  RouteArgs route;
 };
 
 // 8 codes of a lane's word w as the matrix unit's operand.
@@ -80,24 +90,87 @@ __device__ __forceinline__ int cvt_fp8(int w, float scale, bool high) {
                 : __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false));
 }
 
-// The weights of a lane for one K step (16 rows x 128 columns of a wave).
-// FP8: the 16-byte chunks g and g + 4 of the row's 128 bytes; MXFP4: the row's
-// block g and the step's scale word; int4: the unit (row, g) of its tile.
+// Columns of a step: 128 bytes of a weight row (int4: two tiles).
 template <int FMT>
-struct Weights {
-  v4i q[FMT == kFp8 ? 2 : 1];
-  uint32_t s;
-};
+constexpr int kCols = FMT == kFp8 ? 128 : 256;
 
-// The lane's columns of MFMA c (0..3), as 16-byte pieces of 8 activations: FP8:
-// columns 64 (c / 2) + 16 g + 8 (c % 2) ..; MXFP4: 32 g + 8 c ..; int4: 32 g + 4 c
-// .. + 3 and 16 after them. A lane loads four pieces X[0..3]; this is MFMA c's.
+// LDS DMA of 16 or 4 bytes per lane to dst + lane * 16 (4). Memory past the buffer
+// reads as zero. m0 holds the LDS address: the compiler keeps nothing in it here, and
+// a clobber of a reserved register is not honoured.
+__device__ __forceinline__ void dma16(const __amdgpu_buffer_rsrc_t rs, uint32_t dst, uint32_t off, uint32_t ks) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :: "s"(dst), "v"(off), "s"(rs), "s"(ks) : "memory");
+}
+__device__ __forceinline__ void dma4(const __amdgpu_buffer_rsrc_t rs, uint32_t dst, uint32_t off, uint32_t ks) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :: "s"(dst), "v"(off), "s"(rs), "s"(ks) : "memory");
+}
+
+// 16 rows n .. n + 15 of weight matrix e, [N, K]: 2 KiB of LDS per step, by two DMAs.
+// FP8, MXFP4: row r, chunk c at 128 r + 16 (c ^ (r & 7)); int4: tile q, unit (r, g) at
+// 1024 q + 64 r + 16 (g ^ (r / 4 & 3)).
 template <int FMT>
-__device__ __forceinline__ int piece_column(int g, int c) {
-  return FMT == kFp8 ? 64 * (c / 2) + 16 * g + 8 * (c % 2) : 32 * g + 8 * c;
+struct Rows {
+  __amdgpu_buffer_rsrc_t w;
+  uint32_t off[2];
+  bool dead[2];                                      // the chunk lies past K in the last step
+  int kt;                                            // int4: tiles along K
+  // what depends on the lane alone, and on the matrix
+  __device__ __forceinline__ void lane(int64_t n, int64_t K, int lane) {
+    if constexpr (FMT == kInt4) {
+      kt = (int)(K / kTileK);
+      const int r = lane >> 2, g = (lane & 3) ^ (r >> 2 & 3);
+      off[0] = off[1] = (uint32_t)((n % kTileN + r) * 64 + 16 * g);
+    } else {
+      const int64_t bytes = FMT == kFp8 ? K : K / 2;
+      const int left = (int)(K - (K - 1) / kCols<FMT> * kCols<FMT>);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * i + (lane >> 3), c = (lane & 7) ^ (r & 7);
+        off[i] = (uint32_t)(r * bytes + 16 * c);
+        dead[i] = kCols<FMT> / 8 * c >= left;
+      }
+    }
+  }
+  __device__ __forceinline__ void open(const uint8_t* base, int64_t e, int64_t N, int64_t n, int64_t K) {
+    if constexpr (FMT == kInt4) {
+      const int64_t tk = K / kTileK, tiles = (N + kTileN - 1) / kTileN * tk;
+      w = make_rsrc(base + (e * tiles + n / kTileN * tk) * kTileBytes, (uint32_t)(tk * kTileBytes));
+    } else {
+      const int64_t bytes = FMT == kFp8 ? K : K / 2;
+      w = make_rsrc(base + (e * N + n) * bytes, (uint32_t)(16 * bytes));
+    }
+  }
+  __device__ __forceinline__ void fetch(int k, bool last, uint32_t dst) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (FMT == kInt4) dma16(w, dst + 1024 * i, 2 * k + i < kt ? off[i] : kPast, (uint32_t)(2 * k + i) * kTileBytes);
+      else dma16(w, dst + 1024 * i, last && dead[i] ? kPast : off[i], (uint32_t)k * 128u);
+    }
+  }
+};
+// A lane's two 16-byte pieces: FP8: columns 16 g .. and 64 + 16 g ..; MXFP4: blocks g and 4 + g; int4: units (row, g).
+template <int FMT>
+__device__ __forceinline__ v4i weight_piece(const uint8_t* at, int q, int l16, int g) {
+  return *reinterpret_cast<const v4i*>(FMT == kInt4 ? at + 1024 * q + 64 * l16 + 16 * (g ^ (l16 >> 2 & 3))
+                                                    : at + 128 * l16 + 16 * ((4 * q + g) ^ (l16 & 7)));
+}
+
+// Rows of 16-bit activations: a DMA takes kCols columns of 4 (FP8) or 2 rows; row r, chunk c at 2 kCols r + 16 (c ^ (r & 7)).
+template <int FMT>
+constexpr int kRowsPerDma = 512 / kCols<FMT>;
+template <int FMT>
+__device__ __forceinline__ int act_row(int j, int lane) { return j * kRowsPerDma<FMT> + lane / (kCols<FMT> / 8); }
+template <int FMT>
+__device__ __forceinline__ int act_column(int row, int lane) { return 8 * ((lane & (kCols<FMT> / 8 - 1)) ^ (row & 7)); }
+// MFMA c's 8 activations of a lane (of the step's half q: MXFP4 and int4 have 4 MFMAs in each): FP8: columns 64 (c / 2) +
+// 16 g + 8 (c % 2) ..; MXFP4: 128 q + 32 g + 8 c ..; int4: 128 q + 32 g + 4 c .. + 3 and 16 after them.
+template <int FMT>
+__device__ __forceinline__ v4i act_chunk(const uint8_t* at, int row, int chunk) {
+  return *reinterpret_cast<const v4i*>(at + 2 * kCols<FMT> * row + 16 * (chunk ^ (row & 7)));
 }
 template <int FMT>
-__device__ __forceinline__ v4i piece(const v4i (&X)[4], int c) {
+__device__ __forceinline__ v4i act_piece(const v4i (&X)[4], int c) {
   if constexpr (FMT == kInt4) {
     const v4i a = X[c / 2], b = X[2 + c / 2];
     return c % 2 ? v4i{a[2], a[3], b[2], b[3]} : v4i{a[0], a[1], b[0], b[1]};
@@ -106,24 +179,24 @@ __device__ __forceinline__ v4i piece(const v4i (&X)[4], int c) {
   }
 }
 
-// MFMA c's 8 weights. int4 codes come as the code itself, 0..15 (E4M3's codes 0..15
-// are 0..15 times 2^-9); the caller starts the sum from -8 sum x.
+// 8 weights for MFMA c from a lane's pieces. int4 codes come as the code itself, 0..15 (E4M3's codes 0..15 are 0..15 times
+// 2^-9); the sums start from -8 sum x.
 template <int FMT, bool F16>
-__device__ __forceinline__ typename Operand<F16>::V decode(const Weights<FMT>& w, int c, float scale) {
+__device__ __forceinline__ typename Operand<F16>::V decode(const v4i (&w)[2], int q, int c, float scale) {
   v4i r;
   if constexpr (FMT == kFp8) {
-    const int lo = w.q[c / 2][2 * (c % 2)], hi = w.q[c / 2][2 * (c % 2) + 1];
+    const int lo = w[c / 2][2 * (c % 2)], hi = w[c / 2][2 * (c % 2) + 1];
     r = v4i{cvt_fp8<F16>(lo, 1.0f, false), cvt_fp8<F16>(lo, 1.0f, true), cvt_fp8<F16>(hi, 1.0f, false),
             cvt_fp8<F16>(hi, 1.0f, true)};
   } else if constexpr (FMT == kMx) {
     static_assert(!F16, "its scales need bf16's range");
-    const uint32_t v = (uint32_t)w.q[0][c];
+    const uint32_t v = (uint32_t)w[q][c];
     r = v4i{__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 0)),
             __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 1)),
             __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 2)),
             __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 3))};
   } else {
-    const uint32_t v = (uint32_t)w.q[0][c] ^ 0x88888888u;
+    const uint32_t v = (uint32_t)w[q][c] ^ 0x88888888u;
     const int lo = (int)(v & 0x0F0F0F0Fu), hi = (int)((v >> 4) & 0x0F0F0F0Fu);
     r = v4i{cvt_fp8<F16>(lo, 512.0f, false), cvt_fp8<F16>(lo, 512.0f, true), cvt_fp8<F16>(hi, 512.0f, false),
             cvt_fp8<F16>(hi, 512.0f, true)};
@@ -131,100 +204,122 @@ __device__ __forceinline__ typename Operand<F16>::V decode(const Weights<FMT>& w
   return __builtin_bit_cast(typename Operand<F16>::V, r);
 }
 
-// 16 rows of a weight matrix: rows n .. n + 15 of [N, K] of expert e. Reads past the
-// matrix's end (its last, partial K step) give zeros.
-template <int FMT>
-struct Rows {
-  __amdgpu_buffer_rsrc_t w, s;
-  const void* scales;                                // FP8: the tile's row of block scales; int4: [G, N] at column n
-  uint32_t off, soff;
-  int N;
-  __device__ __forceinline__ Rows(const uint8_t* base, const void* sc, int64_t e, int64_t N_, int64_t n, int64_t K, int G,
-                                  int l16, int g) {
+// The scales of a step, of MATS sets of 16 rows (the second `gap` rows after the first), by one DMA. FP8: a float for each
+// set; MXFP4: 16 bytes of each row (8 are the step's); int4: half q, set m: 16 fp16.
+template <int FMT, int MATS>
+struct Scales {
+  static constexpr int kLanes = FMT == kFp8 ? MATS : 16 * MATS;
+  static constexpr int kBytes = FMT == kMx ? 256 * MATS : 64 * MATS;
+  __amdgpu_buffer_rsrc_t s;
+  uint32_t off;
+  int per, N, halves;
+  __device__ __forceinline__ void lane(int64_t N_, int64_t n, int64_t gap, int64_t K, int per_, int lane) {
+    per = per_;
     N = (int)N_;
     if constexpr (FMT == kFp8) {
-      w = make_rsrc(base + (e * N_ + n) * K, (uint32_t)(16 * K));
-      off = (uint32_t)(l16 * K + 16 * g);
-      scales = static_cast<const float*>(sc) + (e * ((N_ + 127) / 128) + n / 128) * ((K + 127) / 128);
+      off = (uint32_t)((n + lane * gap) / 128 * ((K + 127) / 128) * 4);
     } else if constexpr (FMT == kMx) {
-      w = make_rsrc(base + (e * N_ + n) * (K / 2), (uint32_t)(8 * K));
-      off = (uint32_t)(l16 * (K / 2) + 16 * g);
+      off = (uint32_t)(((lane >> 4) * gap + (lane & 15)) * mx_scale_bytes(K));
+    } else {
+      halves = (int)(K / 128);
+      off = (uint32_t)((n + (lane >> 3) % MATS * gap) * 2 + 4 * (lane & 7));
+    }
+  }
+  __device__ __forceinline__ void open(const void* base, int64_t e, int64_t N_, int64_t n, int64_t gap, int64_t K, int G) {
+    const uint8_t* b = static_cast<const uint8_t*>(base);
+    if constexpr (FMT == kFp8) {
+      const int64_t size = (K + 127) / 128 * ((N_ + 127) / 128) * 4;
+      s = make_rsrc(b + e * size, (uint32_t)size);
+    } else if constexpr (FMT == kMx) {
       const int64_t ks = mx_scale_bytes(K);
-      s = make_rsrc(static_cast<const uint8_t*>(sc) + (e * N_ + n) * ks, (uint32_t)(16 * ks));
-      soff = (uint32_t)(l16 * ks);
+      s = make_rsrc(b + (e * N_ + n) * ks, (uint32_t)(((MATS - 1) * gap + 16) * ks));
     } else {
-      // tiles [n / 128][k / 128] of 8 KiB, unit (n % 128) * 4 + g: the 16 rows are 1 KiB of each
-      const int64_t kt = K / kTileK, tiles = (N_ + kTileN - 1) / kTileN * kt;
-      w = make_rsrc(base + (e * tiles + n / kTileN * kt) * kTileBytes, (uint32_t)(kt * kTileBytes));
-      off = (uint32_t)((n % kTileN + l16) * 64 + 16 * g);
-      scales = static_cast<const uint16_t*>(sc) + e * (int64_t)G * N_ + n + 4 * g;
+      s = make_rsrc(b + e * G * N_ * 2, (uint32_t)(G * N_ * 2));
     }
   }
-  __device__ __forceinline__ Weights<FMT> load(int kb, int left, int g) const {   // left: columns from the step's first
-    Weights<FMT> r;
+  __device__ __forceinline__ void fetch(int k, uint32_t dst, int lane) const {
+    if (lane >= kLanes) return;
     if constexpr (FMT == kFp8) {
-      r.q[0] = __builtin_amdgcn_raw_buffer_load_b128(w, 16 * g < left ? off : kPast, (uint32_t)kb * 128u, 0);
-      r.q[1] = __builtin_amdgcn_raw_buffer_load_b128(w, 64 + 16 * g < left ? off + 64u : kPast, (uint32_t)kb * 128u, 0);
+      dma4(s, dst, off, (uint32_t)k * 4);
     } else if constexpr (FMT == kMx) {
-      r.q[0] = __builtin_amdgcn_raw_buffer_load_b128(w, 32 * g < left ? off : kPast, (uint32_t)kb * 64u, 0);
-      r.s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(s, 32 * g < left ? soff : kPast, (uint32_t)kb * 4u, 0);
+      dma16(s, dst, off, (uint32_t)k * 8);
     } else {
-      r.q[0] = __builtin_amdgcn_raw_buffer_load_b128(w, off, (uint32_t)kb * kTileBytes, 0);
+      // (the second half of an odd number's last step: the first's)
+      const int a = 2 * k / per * N * 2, b = min(2 * k + 1, halves - 1) / per * N * 2;
+      dma4(s, dst, off + (lane < 8 * MATS ? (uint32_t)a : (uint32_t)b), 0u);
     }
-    return r;
   }
-  // MXFP4: this lane's scale of the step
-  __device__ __forceinline__ float lane_scale(const Weights<FMT>& r, int g) const {
-    if constexpr (FMT != kMx) return 1.0f;
-    const uint32_t c = r.s >> (8 * g) & 0xFF;
-    return c == kMxNan ? __uint_as_float(0x7FC00000u) : mx_scale_value(c);
-  }
-  // what multiplies the step's sums of weight rows 4 g .. 4 g + 3
-  __device__ __forceinline__ v4f sum_scale(int kb, int per_group) const {
+  // what multiplies the sums of rows 4 g .. 4 g + 3 of set m over half q
+  static __device__ __forceinline__ v4f sums(const uint8_t* at, int m, int q, int g) {
     if constexpr (FMT == kFp8) {
-      const float v = static_cast<const float*>(scales)[kb];
+      const float v = reinterpret_cast<const float*>(at)[m];
       return v4f{v, v, v, v};
-    } else if constexpr (FMT == kInt4) {
-      const v2i v = *reinterpret_cast<const v2i*>(static_cast<const uint16_t*>(scales) + (int64_t)(kb / per_group) * N);
+    } else {
+      const v2i v = *reinterpret_cast<const v2i*>(at + 32 * (MATS * q + m) + 8 * g);
       return v4f{f16_to_f32((uint16_t)v[0]), f16_to_f32((uint16_t)((uint32_t)v[0] >> 16)), f16_to_f32((uint16_t)v[1]),
                  f16_to_f32((uint16_t)((uint32_t)v[1] >> 16))};
-    } else {
-      return v4f{1.f, 1.f, 1.f, 1.f};
     }
   }
-};
-
-// fp16 pairs as the sum of two bf16 numbers each (exact: 11 bits, and bf16's range is wider). An infinity's remainder,
-// a NaN, becomes a finite number, which changes nothing.
-__device__ __forceinline__ void split_f16(v4i x, v4i& hi, v4i& lo) {
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    const float a = f16_to_f32((uint16_t)x[d]), b = f16_to_f32((uint16_t)((uint32_t)x[d] >> 16));
-    const uint32_t ha = f32_to_bf16_rne(a), hb = f32_to_bf16_rne(b);
-    const float ra = fmaxf(a - __uint_as_float(ha << 16), -64.f), rb = fmaxf(b - __uint_as_float(hb << 16), -64.f);
-    hi[d] = (int)(ha | hb << 16);
-    lo[d] = (int)((uint32_t)f32_to_bf16_rne(ra) | (uint32_t)f32_to_bf16_rne(rb) << 16);
+  // MXFP4: a lane's scale of half q; left: the columns from the step's first to the end
+  static __device__ __forceinline__ float block(const uint8_t* at, int m, int q, int left, int l16, int g) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(at + 16 * (16 * m + l16) + 4 * q);
+    const uint32_t c = 128 * q + 32 * g < left ? w >> (8 * g) & 0xFF : 0u;   // past K: the padding, or the next row's
+    return c == kMxNan ? __uint_as_float(0x7FC00000u) : mx_scale_value(c);
   }
-}
+};
 
 __device__ __forceinline__ v8bf bf(v4i v) { return __builtin_bit_cast(v8bf, v); }
 
-// Everything a block of the first kernel has to know: its expert and the rows.
-struct MoeWork {
-  int e, row0, rows;
-};
+// fp16 pairs as the sum of two bf16 numbers each (exact: the upper 8 of 11 bits, and the
+// rest; bf16's range is wider): the first of them, or the second. An infinity's
+// remainder, a NaN, becomes a finite number, which changes nothing.
+__device__ __forceinline__ v4i part_of_f16(v4i x, uint32_t taken) {   // taken: 0, or the upper half's bits
+  v4i r;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const float a = f16_to_f32((uint16_t)x[d]), b = f16_to_f32((uint16_t)((uint32_t)x[d] >> 16));
+    const float ra = a - __uint_as_float(__float_as_uint(a) & taken), rb = b - __uint_as_float(__float_as_uint(b) & taken);
+    r[d] = (int)__builtin_amdgcn_perm(__float_as_uint(taken ? fmaxf(rb, -64.f * 1024.f) : rb),
+                                      __float_as_uint(taken ? fmaxf(ra, -64.f * 1024.f) : ra), 0x07060302u);
+  }
+  return r;
+}
 
-// The plan of up to kInline tokens in LDS, by one block: routes, orders the pairs
-// by expert and token, and lists the experts. Block 0 leaves the list in the workspace.
+// The token of a tile's i-th row (the i-th bit of its tokens), -1 past the last.
+__device__ __forceinline__ int tile_token(uint32_t tokens, int i) {
+  for (int q = 0; q < i; ++q) tokens &= tokens - 1;
+  return tokens ? __builtin_ctz(tokens) : -1;
+}
+
+// Tile i of an expert's tokens, at most `most` of them each.
+__device__ __forceinline__ MoeTile tile_of(int e, int row0, uint32_t tokens, int i, int most) {
+  for (int q = 0; q < i * most; ++q) tokens &= tokens - 1;
+  uint32_t rest = tokens;
+  for (int q = 0; q < most; ++q) rest &= rest - 1;
+  return MoeTile{(uint16_t)e, (uint16_t)(row0 + i * most), tokens ^ rest};
+}
+
+// The plan of up to kInline tokens in LDS, by every block for itself; block 0 leaves the second kernel's in the workspace.
+// (Two tokens of an expert fit one tile.)
 struct InlinePlan {
-  int t[kInlineRows];
   float w[kInlineRows];
   int raw_e[kInlineRows];
   float raw_w[kInlineRows];
-  MoeSlot slot[kInlineRows];
-  int nslots;
+  MoeTile tile[kInlineRows];
+  int tiles;
   double keys[kInline][kInlineE];
 };
+
+__device__ __forceinline__ void route_one(const RouteArgs& a, int t, int lane, double* keys, int& id, double& w) {
+  if (a.E <= 64) {
+    if (a.bias || a.G > 1) route_token<3, 1, true>(a, t, lane, LaneExperts<1, true>(a, lane), keys, id, w);
+    else route_token<3, 1, false>(a, t, lane, LaneExperts<1, false>(a, lane), keys, id, w);
+  } else {
+    constexpr int V = kInlineE / 64;
+    if (a.bias || a.G > 1) route_token<3, V, true>(a, t, lane, LaneExperts<V, true>(a, lane), keys, id, w);
+    else route_token<3, V, false>(a, t, lane, LaneExperts<V, false>(a, lane), keys, id, w);
+  }
+}
 
 __device__ __forceinline__ void plan_inline(const MoeArgs& p, InlinePlan& s) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -232,20 +327,14 @@ __device__ __forceinline__ void plan_inline(const MoeArgs& p, InlinePlan& s) {
   if (wave < p.T) {
     int id;
     double w;
-    if (a.bias || a.G > 1) {
-      const LaneExperts<kInlineE / 64, true> own(a, lane);
-      route_token<3, kInlineE / 64, true>(a, wave, lane, own, s.keys[wave], id, w);
-    } else {
-      const LaneExperts<kInlineE / 64, false> own(a, lane);
-      route_token<3, kInlineE / 64, false>(a, wave, lane, own, s.keys[wave], id, w);
-    }
+    route_one(a, wave, lane, s.keys[wave], id, w);
     if (lane < p.topk) {
       s.raw_e[wave * p.topk + lane] = id;
       s.raw_w[wave * p.topk + lane] = (float)(w * a.scale);
     }
   }
   __syncthreads();
-  // One wave: lane i holds both tokens' choice i. A pair's row counts the pairs before it, its slot the experts.
+  // One wave: lane i holds both tokens' choice i. A pair's row counts the pairs before it, its tile the experts.
   if (wave == 0) {
     const bool two = p.T == 2;
     const int e0 = lane < p.topk ? s.raw_e[lane] : -1, e1 = two && lane < p.topk ? s.raw_e[p.topk + lane] : -1;
@@ -266,315 +355,408 @@ __device__ __forceinline__ void plan_inline(const MoeArgs& p, InlinePlan& s) {
       s1 += a1 + b1 * once;
     }
     if (e0 >= 0) {
-      s.t[r0] = 0;
       s.w[r0] = s.raw_w[lane];
-      s.slot[s0] = MoeSlot{e0, r0, dup0 ? 3u : 1u, 0};
+      s.tile[s0] = MoeTile{(uint16_t)e0, (uint16_t)r0, dup0 ? 3u : 1u};
     }
     if (e1 >= 0) {
-      s.t[r1] = 1;
       s.w[r1] = s.raw_w[p.topk + lane];
-      if (!dup1) s.slot[s1] = MoeSlot{e1, r1, 2u, 0};
+      if (!dup1) s.tile[s1] = MoeTile{(uint16_t)e1, (uint16_t)r1, 2u};
     }
     const int n = __popcll(__ballot(e0 >= 0)) + __popcll(__ballot(e1 >= 0 && !dup1));
-    if (lane == 0) s.nslots = n;
+    if (lane == 0) s.tiles = n;
   }
   __syncthreads();
   if (blockIdx.x == 0) {
-    for (int i = tid; i < s.nslots; i += blockDim.x) p.slots[i] = s.slot[i];
-    if (tid == 0) *p.nslots = s.nslots;
+    for (int i = tid; i < s.tiles; i += blockDim.x) p.down[i] = s.tile[i];
+    if (tid == 0) p.counts[1] = s.tiles;
   }
 }
 
-// The list of experts from the plan's offsets, by the first block's first wave.
-__device__ __forceinline__ void list_slots(const MoeArgs& p) {
-  const int lane = threadIdx.x;
+// The plan of more tokens, by one block of its own: a wave per token; a token is one bit of a mask per expert, so that
+// rows need no sort and no order of atomics.
+constexpr int kPThreads = 1024;
+template <int V, bool GENERAL>
+__global__ __launch_bounds__(kPThreads) void moe_plan_kernel(MoeArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ uint32_t mask[kMaxE];
+  __shared__ int row0[kMaxE], part[3][kPThreads / kWave];
+  double* keys = reinterpret_cast<double*>(smem);    // (groups) the waves' choice values
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const RouteArgs& a = p.route;
-  int n = 0;
-  for (int c = 0; c < p.E; c += 64) {
-    const int e = c + lane;
-    const int r0 = e < p.E ? a.offsets[e] : 0, r1 = e < p.E ? a.offsets[e + 1] : 0;
-    const unsigned long long have = __ballot(r1 > r0);
-    if (r1 > r0) {
-      uint32_t tokens = 0;
-      for (int r = r0; r < r1; ++r) tokens |= 1u << a.row_token[r];
-      p.slots[n + __popcll(have & ((1ull << lane) - 1))] = MoeSlot{e, r0, tokens, 0};
+  mask[tid] = 0;
+  __syncthreads();
+  int id[2] = {-1, -1};
+  float w[2] = {0.f, 0.f};
+  const LaneExperts<V, GENERAL> own(a, lane);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {                      // T <= 32 = 2 x 16 waves
+    const int t = wave + 16 * q;
+    if (t < p.T) {
+      double v;
+      route_token<3, V, GENERAL>(a, t, lane, own, keys + wave * a.E, id[q], v);
+      w[q] = (float)(v * a.scale);
+      if (id[q] >= 0) atomicOr(&mask[id[q]], 1u << t);
     }
-    n += __popcll(have);
   }
-  if (lane == 0) *p.nslots = n;
+  __syncthreads();
+  // thread e: the expert's rows and tiles, and the sums of those before it
+  const uint32_t m = mask[tid];
+  const int n = __popc(m), up = (n + kUpRows - 1) / kUpRows, dn = (n + kDownRows - 1) / kDownRows;
+  int s[3] = {n, up, dn};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int o = __shfl_up(s[k], off, kWave);
+      if (lane >= off) s[k] += o;
+    }
+    if (lane == 63) part[k][wave] = s[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    for (int v = 0; v < wave; ++v) s[k] += part[k][v];
+  row0[tid] = s[0] - n;
+  for (int i = 0; i < up; ++i) p.up[s[1] - up + i] = tile_of(tid, s[0] - n, m, i, kUpRows);
+  for (int i = 0; i < dn; ++i) p.down[s[2] - dn + i] = tile_of(tid, s[0] - n, m, i, kDownRows);
+  if (tid == kPThreads - 1) {
+    p.counts[0] = s[1];
+    p.counts[1] = s[2];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    if (id[q] >= 0) p.weights[row0[id[q]] + __popc(mask[id[q]] & ((1u << (wave + 16 * q)) - 1))] = w[q];
 }
 
-// Gate and up: WS waves of a block take the K steps of 16 gate rows and the 16 up
-// rows beside them in turn.
-template <int FMT, bool XF16, int RT, int WS, int U>
+// Gate and up: WS waves of a block share the steps of 16 gate rows and the 16 up rows beside them. NX: DMAs of a step's
+// activations.
+template <int FMT, bool XF16, int NX, int WS, int D>
 __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
   constexpr bool OPF16 = XF16 && FMT != kMx;         // the operands' type
-  constexpr int PARTS = XF16 && FMT == kMx ? 2 : 1;
-  __shared__ union {
+  constexpr bool PARTS = XF16 && FMT == kMx;         // x as two numbers
+  constexpr int COLS = kCols<FMT>, HALVES = FMT == kFp8 ? 1 : 2;
+  using Op = typename Operand<OPF16>::V;
+  using S = Scales<FMT, 2>;
+  // a step in LDS: gate, up, activations, scales
+  constexpr int kX = 4096, kS = kX + 1024 * NX, kSlot = kS + S::kBytes, kDmas = 4 + NX + 1;
+  __shared__ __attribute__((aligned(16))) union {
     InlinePlan plan;
-    v4f red[WS][2 * RT][64];
+    uint8_t ring[WS][D][kSlot];
+    v4f red[WS][2][64];
   } s;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, l16 = lane & 15;
-  MoeWork k;
-  int tn = (int)blockIdx.x % p.NT;
-  int token[RT], mine[RT];                           // this lane's activation row, and that of the results it keeps
-  float weight[RT];
+  const int ti = (int)blockIdx.x / p.NT, tn = (int)blockIdx.x % p.NT;
+  MoeTile tile;
+  const int row = l16 & 7;                           // this lane's row of the tile (columns 8 and on: again, or second parts)
+  float weight = 0.f;
   if (p.inl) {
     plan_inline(p, s.plan);
-    const int sl = (int)blockIdx.x / p.NT;
-    if (sl >= s.plan.nslots) return;
-    k.e = __builtin_amdgcn_readfirstlane(s.plan.slot[sl].e);
-    k.row0 = __builtin_amdgcn_readfirstlane(s.plan.slot[sl].row0);
-    k.rows = __builtin_amdgcn_readfirstlane(__popc(s.plan.slot[sl].tokens));
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int i = 16 * r + l16;
-      token[r] = i < k.rows ? s.plan.t[k.row0 + i] : -1;
-      weight[r] = i < k.rows ? s.plan.w[k.row0 + i] : 0.f;
-      mine[r] = k.row0 + i;
-    }
-    __syncthreads();                                 // the plan's place becomes the sums'
+    if (ti >= s.plan.tiles) return;
+    tile = s.plan.tile[ti];
+    if (row < __popc(tile.tokens)) weight = s.plan.w[tile.row0 + row];
+    __syncthreads();                                 // the plan's place becomes the ring
   } else {
-    if (blockIdx.x == gridDim.x - 1 && wave == 0) list_slots(p);
-    struct { const int32_t* offsets; int E, NT; int64_t R; } f{p.route.offsets, p.E, p.NT, (int64_t)p.T * p.topk};
-    const Segment seg = find_segment<16 * RT>(f);
-    if (seg.e < 0) return;
-    k.e = seg.e;
-    k.row0 = (int)seg.row0;
-    k.rows = (int)seg.rows;
-    tn = seg.tn;
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int i = 16 * r + l16;
-      token[r] = i < k.rows ? p.route.row_token[k.row0 + i] : -1;
-      mine[r] = k.row0 + i;
-      weight[r] = 0.f;
-      if (i < k.rows)
-        for (int j = 0; j < p.topk; ++j)
-          if (p.route.row_of[token[r] * p.topk + j] == mine[r]) weight[r] = p.route.weights[token[r] * p.topk + j];
-    }
+    if (ti >= p.counts[0]) return;
+    tile = p.up[ti];
+    if (row < __popc(tile.tokens)) weight = p.weights[tile.row0 + row];
   }
-  const int KB = (p.H + 127) / 128, n0 = 16 * tn;
-  const Rows<FMT> wg(p.w13, p.s13, k.e, 2 * (int64_t)p.I, n0, p.H, p.G13, l16, g);
-  const Rows<FMT> wu(p.w13, p.s13, k.e, 2 * (int64_t)p.I, p.I + n0, p.H, p.G13, l16, g);
+  const int e = __builtin_amdgcn_readfirstlane(tile.e);
+  const int KT = (p.H + COLS - 1) / COLS, n0 = 16 * tn;
+  Rows<FMT> wg, wu;
+  wg.lane(n0, p.H, lane);
+  wu.lane(p.I + n0, p.H, lane);
+  wg.open(p.w13, e, 2 * (int64_t)p.I, n0, p.H);
+  wu.open(p.w13, e, 2 * (int64_t)p.I, p.I + n0, p.H);
+  S sc;
+  sc.lane(2 * (int64_t)p.I, n0, p.I, p.H, p.kg13, lane);
+  sc.open(p.s13, e, 2 * (int64_t)p.I, n0, p.I, p.H, p.G13);
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x, (uint32_t)(p.T * (int64_t)p.H * 2));
-  uint32_t xo[RT];
+  uint32_t xo[NX];
+  bool xdead[NX];                                    // past H in the last step
 #pragma unroll
-  for (int r = 0; r < RT; ++r) xo[r] = token[r] >= 0 ? (uint32_t)((int64_t)token[r] * p.H * 2) : kPast;
-
-  v4f ag[RT], au[RT];
+  for (int j = 0; j < NX; ++j) {
+    const int r = act_row<FMT>(j, lane), col = act_column<FMT>(r, lane), token = tile_token(tile.tokens, r);
+    xo[j] = token >= 0 ? (uint32_t)(((int64_t)token * p.H + col) * 2) : kPast;
+    xdead[j] = col >= p.H - (KT - 1) * COLS;
+  }
+  const uint32_t ring0 =
+      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&s.ring[wave][0][0]);
+  const int k0 = KT * wave / WS, k1 = KT * (wave + 1) / WS;
+  auto fetch = [&](int k, int d) {                   // past the run's end: the last step again, not used
+    k = min(k, k1 - 1);
+    const uint32_t at = ring0 + d * kSlot;
+    const bool last = k == KT - 1;
+    wg.fetch(k, last, at);
+    wu.fetch(k, last, at + 2048);
 #pragma unroll
-  for (int r = 0; r < RT; ++r) ag[r] = au[r] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int kb = wave; kb < KB; kb += WS * U) {
-    Weights<FMT> qg[U], qu[U];
-    v4i X[U][RT][4];
-    v4f sg[U], su[U];
+    for (int j = 0; j < NX; ++j) dma16(xr, at + kX + 1024 * j, last && xdead[j] ? kPast : xo[j], (uint32_t)k * (2 * COLS));
+    sc.fetch(k, at + kS, lane);
+  };
+  const uint32_t taken = l16 >= 8 ? 0xFFFF0000u : 0u;
+  v4f ag = v4f{0.f, 0.f, 0.f, 0.f}, au = ag;
+  if (k0 < k1) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kk = min(kb + WS * u, KB - 1);       // past the end: loaded again, not used
-      const int left = p.H - 128 * kk;
-      qg[u] = wg.load(kk, left, g);
-      qu[u] = wu.load(kk, left, g);
-      sg[u] = wg.sum_scale(kk, p.kg13);
-      su[u] = wu.sum_scale(kk, p.kg13);
+    for (int d = 0; d < D; ++d) fetch(k0 + d, d);
+    int d = 0;
+    for (int k = k0; k < k1; ++k) {
+      const uint8_t* at = &s.ring[wave][d][0];
+      asm volatile("s_waitcnt vmcnt(%0)" :: "n"((D - 1) * kDmas) : "memory");
+      v4i qg[2], qu[2], X[HALVES][4];
+      float lg[HALVES], lu[HALVES];
+      v4f mg[HALVES], mu[HALVES];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+      for (int q = 0; q < 2; ++q) {
+        qg[q] = weight_piece<FMT>(at, q, l16, g);
+        qu[q] = weight_piece<FMT>(at + 2048, q, l16, g);
+      }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = piece_column<FMT>(g, c);
-          X[u][r][c] = __builtin_amdgcn_raw_buffer_load_b128(xr, col < left && xo[r] != kPast ? xo[r] + 2 * col : kPast,
-                                                             256u * (uint32_t)kk, 0);
+      for (int q = 0; q < HALVES; ++q) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          X[q][c] = act_chunk<FMT>(at + kX, row & (kRowsPerDma<FMT> * NX - 1),
+                                   FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
+        if constexpr (FMT == kMx) {
+          lg[q] = S::block(at + kS, 0, q, p.H - k * COLS, l16, g);
+          lu[q] = S::block(at + kS, 1, q, p.H - k * COLS, l16, g);
+        } else {
+          mg[q] = S::sums(at + kS, 0, q, g);
+          mu[q] = S::sums(at + kS, 1, q, g);
         }
-    }
+      }
+      // the step is in registers: its place takes the one D on
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(k + D, d);
+      __builtin_amdgcn_sched_barrier(0);
+      d = d + 1 == D ? 0 : d + 1;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (kb + WS * u >= KB) break;
-      const float lg = wg.lane_scale(qg[u], g), lu = wu.lane_scale(qu[u], g);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if (16 * r >= k.rows) break;
-        v4f dg = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int q = 0; q < HALVES; ++q) {
+        v4f dg = FMT == kMx ? ag : v4f{0.f, 0.f, 0.f, 0.f}, du = FMT == kMx ? au : dg;
         if constexpr (FMT == kInt4) {                // -8 sum x
           const int m8 = OPF16 ? (int)0xC800C800 : (int)0xC100C100;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            dg = mfma16<OPF16>(__builtin_bit_cast(typename Operand<OPF16>::V, v4i{m8, m8, m8, m8}),
-                               __builtin_bit_cast(typename Operand<OPF16>::V, piece<FMT>(X[u][r], c)), dg);
+            dg = mfma16<OPF16>(__builtin_bit_cast(Op, v4i{m8, m8, m8, m8}), __builtin_bit_cast(Op, act_piece<FMT>(X[q], c)), dg);
+          du = dg;
         }
-        v4f du = dg;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const v4i xp = piece<FMT>(X[u][r], c);
-          const auto a = decode<FMT, OPF16>(qg[u], c, lg), b = decode<FMT, OPF16>(qu[u], c, lu);
-          if constexpr (PARTS == 2) {
-            v4i hi, lo;
-            split_f16(xp, hi, lo);
-            dg = mfma16<false>(a, bf(lo), dg);
-            du = mfma16<false>(b, bf(lo), du);
-            dg = mfma16<false>(a, bf(hi), dg);
-            du = mfma16<false>(b, bf(hi), du);
-          } else {
-            const auto x = __builtin_bit_cast(typename Operand<OPF16>::V, xp);
-            dg = mfma16<OPF16>(a, x, dg);
-            du = mfma16<OPF16>(b, x, du);
-          }
+          v4i xp = act_piece<FMT>(X[q], c);
+          if constexpr (PARTS) xp = part_of_f16(xp, taken);
+          dg = mfma16<OPF16>(decode<FMT, OPF16>(qg, q, c, lg[q]), __builtin_bit_cast(Op, xp), dg);
+          du = mfma16<OPF16>(decode<FMT, OPF16>(qu, q, c, lu[q]), __builtin_bit_cast(Op, xp), du);
         }
+        if constexpr (FMT == kMx) {
+          ag = dg;
+          au = du;
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          ag[r][q] = FMT == kMx ? ag[r][q] + dg[q] : fmaf(dg[q], sg[u][q], ag[r][q]);
-          au[r][q] = FMT == kMx ? au[r][q] + du[q] : fmaf(du[q], su[u][q], au[r][q]);
+          for (int i = 0; i < 4; ++i) {
+            ag[i] = fmaf(dg[i], mg[q][i], ag[i]);
+            au[i] = fmaf(du[i], mu[q][i], au[i]);
+          }
         }
       }
     }
-  }
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    s.red[wave][2 * r][lane] = ag[r];
-    s.red[wave][2 * r + 1][lane] = au[r];
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing may land in what the ring becomes
   }
   __syncthreads();
+  s.red[wave][0][lane] = ag;
+  s.red[wave][1][lane] = au;
+  __syncthreads();
   if (wave != 0) return;
+  v4f vg = s.red[0][0][lane], vu = s.red[0][1][lane];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    if (16 * r + l16 >= k.rows) break;
-    v4f vg = s.red[0][2 * r][lane], vu = s.red[0][2 * r + 1][lane];
-#pragma unroll
-    for (int w = 1; w < WS; ++w) {
-      vg += s.red[w][2 * r][lane];
-      vu += s.red[w][2 * r + 1][lane];
-    }
-    uint32_t hi[4], lo[4];
+  for (int w = 1; w < WS; ++w) {
+    vg += s.red[w][0][lane];
+    vu += s.red[w][1][lane];
+  }
+  if constexpr (PARTS) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float m = vg[q] / (1.0f + expf(-vg[q])) * vu[q] * weight[r];
-      hi[q] = f32_to_bf16_rne(m);
-      // (an infinity has no remainder)
-      const float rest = m - __uint_as_float(hi[q] << 16);
-      lo[q] = (hi[q] & 0x7F80u) != 0x7F80u ? f32_to_bf16_rne(rest) : 0u;
+      vg[q] += __shfl_xor(vg[q], 8, kWave);
+      vu[q] += __shfl_xor(vu[q], 8, kWave);
     }
-    const int64_t at = (int64_t)mine[r] * p.I + n0 + 4 * g;
-    *reinterpret_cast<v2i*>(p.hi + at) = v2i{(int)(hi[0] | hi[1] << 16), (int)(hi[2] | hi[3] << 16)};
-    *reinterpret_cast<v2i*>(p.lo + at) = v2i{(int)(lo[0] | lo[1] << 16), (int)(lo[2] | lo[3] << 16)};
   }
+  if (l16 >= 8 || row >= __popc(tile.tokens)) return;
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float m = vg[q] / (1.0f + expf(-vg[q])) * vu[q] * weight;
+    hi[q] = f32_to_bf16_rne(m);
+    const float rest = m - __uint_as_float(hi[q] << 16);
+    lo[q] = (hi[q] & 0x7F80u) != 0x7F80u ? f32_to_bf16_rne(rest) : 0u;   // (an infinity has no remainder)
+  }
+  uint16_t* o = p.mid + (int64_t)(tile.row0 + row) * p.I + n0 + 4 * g;
+  *reinterpret_cast<v2i*>(o) = v2i{(int)(hi[0] | hi[1] << 16), (int)(hi[2] | hi[3] << 16)};
+  *reinterpret_cast<v2i*>(o + (int64_t)p.T * p.topk * p.I) = v2i{(int)(lo[0] | lo[1] << 16), (int)(lo[2] | lo[3] << 16)};
 }
 
-// Down: a block owns 16 output columns of all tokens; its waves take the (expert, K
-// step) pairs in turn. The matrix unit's columns are the tokens themselves, so the
-// sum over a token's experts is the accumulator's own.
-template <int FMT, bool F16OUT, int RT, int WS, int U>
+// Down: a block owns 16 output columns of all tokens; its waves share the (tile, step) pairs, each a run of them. At a
+// tile's end a wave adds its sums to its own place in LDS by token: no token takes anything of an expert that it did not
+// choose, and the order is fixed. NM: DMAs of a step's middle (row r's first numbers as row 2 r, its second as 2 r + 1).
+template <int FMT, bool F16OUT, int NM, int WS, int D>
 __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
-  __shared__ v4f red[WS][RT][64];
+  constexpr int COLS = kCols<FMT>, HALVES = FMT == kFp8 ? 1 : 2;
+  using S = Scales<FMT, 1>;
+  constexpr int kX = 2048, kS = kX + 1024 * NM, kSlot = kS + S::kBytes, kDmas = 2 + NM + 1;
+  constexpr int kMost = kRowsPerDma<FMT> * NM / 2;   // rows that fit
+  __shared__ __attribute__((aligned(16))) uint8_t ring[WS][D][kSlot];
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  v4f* sum = reinterpret_cast<v4f*>(smem);           // [WS][T][4]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, l16 = lane & 15;
   const int n0 = 16 * (int)blockIdx.x;
-  const int KB = (p.I + 127) / 128, items = *p.nslots * KB;
-  const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.hi, (uint32_t)((int64_t)p.T * p.topk * p.I * 2));
-  const __amdgpu_buffer_rsrc_t lr = make_rsrc(p.lo, (uint32_t)((int64_t)p.T * p.topk * p.I * 2));
-  v4f acc[RT];
+  const int KT = (p.I + COLS - 1) / COLS, tiles = p.counts[1], steps = tiles * KT;
+  MoeTile* list = reinterpret_cast<MoeTile*>(sum + WS * p.T * 4);
+  for (int i = tid; i < tiles; i += 64 * WS) list[i] = p.down[i];
+  for (int i = tid; i < WS * p.T * 4; i += 64 * WS) sum[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int64_t plane = (int64_t)p.T * p.topk * p.I * 2;
+  const __amdgpu_buffer_rsrc_t mr = make_rsrc(p.mid, (uint32_t)(2 * plane));
+  __syncthreads();
+  v4f* mine = sum + wave * p.T * 4;
+  const int i0 = (int)((int64_t)steps * wave / WS), i1 = (int)((int64_t)steps * (wave + 1) / WS);
+  const uint32_t ring0 =
+      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&ring[wave][0][0]);
+  uint32_t mo[NM];
+  bool mdead[NM];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int it = wave; it < items; it += WS * U) {
-    Weights<FMT> qw[U];
-    v4i H[U][RT][4], L[U][RT][4];
-    v4f sw[U];
-    float ls[U];
-    uint32_t tokens[U];
+  for (int j = 0; j < NM; ++j) {
+    const int r = act_row<FMT>(j, lane), col = act_column<FMT>(r, lane);
+    mo[j] = (uint32_t)((int64_t)(r >> 1) * p.I * 2 + 2 * col + (r & 1) * plane);
+    mdead[j] = col >= p.I - (KT - 1) * COLS;
+  }
+  // the tile and step that are fetched next, and those that are computed
+  int ft = i0 / KT, fk = i0 - ft * KT, ct = ft, ck = fk;
+  Rows<FMT> w;
+  S sc;
+  int rows = 0;
+  uint32_t row0 = 0;
+  auto open_tile = [&]() {                           // past the last: the last again, not used
+    const MoeTile tile = list[min(ft, tiles - 1)];
+    const int e = __builtin_amdgcn_readfirstlane(tile.e);
+    rows = __popc(__builtin_amdgcn_readfirstlane(tile.tokens));
+    row0 = (uint32_t)__builtin_amdgcn_readfirstlane(tile.row0) * (uint32_t)p.I * 2u;
+    w.open(p.w2, e, p.H, n0, p.I);
+    sc.open(p.s2, e, p.H, n0, 0, p.I, p.G2);
+  };
+  auto fetch = [&](int d) {
+    const uint32_t at = ring0 + d * kSlot;
+    const bool last = fk == KT - 1;
+    w.fetch(fk, last, at);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = min(it + WS * u, items - 1);     // past the end: loaded again, not used
-      const int sl = i / KB, kb = i - sl * KB, left = p.I - 128 * kb;
-      const MoeSlot slot = p.slots[sl];
-      const Rows<FMT> w(p.w2, p.s2, slot.e, p.H, n0, p.I, p.G2, l16, g);
-      qw[u] = w.load(kb, left, g);
-      sw[u] = w.sum_scale(kb, p.kg2);
-      tokens[u] = slot.tokens;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const int t = 16 * r + l16;
-        const bool has = slot.tokens >> t & 1;
-        const uint32_t row = (uint32_t)((int64_t)(slot.row0 + __popc(slot.tokens & ((1u << t) - 1))) * p.I * 2);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = piece_column<FMT>(g, c);
-          const uint32_t off = has && col < left ? row + 2 * col : kPast;
-          H[u][r][c] = __builtin_amdgcn_raw_buffer_load_b128(hr, off, 256u * (uint32_t)kb, 0);
-          L[u][r][c] = __builtin_amdgcn_raw_buffer_load_b128(lr, off, 256u * (uint32_t)kb, 0);
-        }
-      }
-      ls[u] = w.lane_scale(qw[u], g);
+    for (int j = 0; j < NM; ++j)
+      dma16(mr, at + kX + 1024 * j, (act_row<FMT>(j, lane) >> 1) >= rows || (last && mdead[j]) ? kPast : mo[j] + row0,
+            (uint32_t)fk * (2 * COLS));
+    sc.fetch(fk, at + kS, lane);
+    if (++fk == KT) {
+      fk = 0;
+      ++ft;
+      open_tile();
     }
+  };
+  if (i0 < i1) {
+    v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+    w.lane(n0, p.I, lane);
+    sc.lane(p.H, n0, 0, p.I, p.kg2, lane);
+    open_tile();
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (it + WS * u >= items) break;
+    for (int d = 0; d < D; ++d) fetch(d);
+    const int mrow = (2 * (l16 & 7) + (l16 >> 3)) & (2 * kMost - 1);
+    int d = 0;
+    for (int i = i0; i < i1; ++i) {
+      const uint8_t* at = &ring[wave][d][0];
+      asm volatile("s_waitcnt vmcnt(%0)" :: "n"((D - 1) * kDmas) : "memory");
+      v4i qw[2], M[HALVES][4];
+      float ls[HALVES];
+      v4f ms[HALVES];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if (!(tokens[u] >> (16 * r) & 0xFFFFu)) continue;
-        v4f d = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int q = 0; q < 2; ++q) qw[q] = weight_piece<FMT>(at, q, l16, g);
+#pragma unroll
+      for (int q = 0; q < HALVES; ++q) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          M[q][c] = act_chunk<FMT>(at + kX, mrow, FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
+        if constexpr (FMT == kMx) ls[q] = S::block(at + kS, 0, q, p.I - ck * COLS, l16, g);
+        else ms[q] = S::sums(at + kS, 0, q, g);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(d);
+      __builtin_amdgcn_sched_barrier(0);
+      d = d + 1 == D ? 0 : d + 1;
+#pragma unroll
+      for (int q = 0; q < HALVES; ++q) {
+        v4f v = FMT == kMx ? acc : v4f{0.f, 0.f, 0.f, 0.f};
         if constexpr (FMT == kInt4) {
           const int m8 = (int)0xC100C100;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            d = mfma16<false>(bf(v4i{m8, m8, m8, m8}), bf(piece<FMT>(L[u][r], c)), d);
-            d = mfma16<false>(bf(v4i{m8, m8, m8, m8}), bf(piece<FMT>(H[u][r], c)), d);
-          }
+          for (int c = 0; c < 4; ++c) v = mfma16<false>(bf(v4i{m8, m8, m8, m8}), bf(act_piece<FMT>(M[q], c)), v);
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const v8bf a = decode<FMT, false>(qw[u], c, ls[u]);
-          d = mfma16<false>(a, bf(piece<FMT>(L[u][r], c)), d);
-          d = mfma16<false>(a, bf(piece<FMT>(H[u][r], c)), d);
-        }
-        // a token that did not choose this expert takes nothing of it, not even NaN
-        const bool has = tokens[u] >> (16 * r + l16) & 1;
+        for (int c = 0; c < 4; ++c) v = mfma16<false>(decode<FMT, false>(qw, q, c, ls[q]), bf(act_piece<FMT>(M[q], c)), v);
+        if constexpr (FMT == kMx) {
+          acc = v;
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float v = FMT == kMx ? acc[r][q] + d[q] : fmaf(d[q], sw[u][q], acc[r][q]);
-          acc[r][q] = has ? v : acc[r][q];
+          for (int c = 0; c < 4; ++c) acc[c] = fmaf(v[c], ms[q][c], acc[c]);
         }
       }
+      if (++ck == KT || i == i1 - 1) {               // the tile's last step here
+        const MoeTile tile = list[ct];
+        const int token = tile_token(tile.tokens, l16 & 7);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] += __shfl_xor(acc[c], 8, kWave);
+        if (l16 < 8 && token >= 0) mine[token * 4 + g] += acc;
+        acc = v4f{0.f, 0.f, 0.f, 0.f};
+        ck = 0;
+        ++ct;
+      }
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // what was fetched past the end has landed
   }
-#pragma unroll
-  for (int r = 0; r < RT; ++r) red[wave][r][lane] = acc[r];
   __syncthreads();
-  if (wave != 0) return;
+  for (int i = tid; i < p.T * 4; i += 64 * WS) {
+    v4f v = sum[i];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int t = 16 * r + l16;
-    if (t >= p.T) break;
-    v4f v = red[0][r][lane];
+    for (int w = 1; w < WS; ++w) v += sum[w * p.T * 4 + i];
+    const int64_t at = (int64_t)(i / 4) * p.H + n0 + 4 * (i % 4);
+    if (p.add) {
+      const v2i a = *reinterpret_cast<const v2i*>(p.add + at);
 #pragma unroll
-    for (int w = 1; w < WS; ++w) v += red[w][r][lane];
-    const int64_t at = (int64_t)t * p.H + n0 + 4 * g;
+      for (int q = 0; q < 4; ++q) {
+        const uint16_t b = (uint16_t)((uint32_t)a[q / 2] >> (16 * (q % 2)));
+        v[q] += F16OUT ? f16_to_f32(b) : bf16_to_f32(b);
+      }
+    }
     uint32_t o[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (p.add) v[q] += F16OUT ? f16_to_f32(p.add[at + q]) : bf16_to_f32(p.add[at + q]);
       o[q] = F16OUT ? f32_to_f16_rne(v[q]) : f32_to_bf16_rne(v[q]);
     }
     *reinterpret_cast<v2i*>(p.out + at) = v2i{(int)(o[0] | o[1] << 16), (int)(o[2] | o[3] << 16)};
   }
 }
 
-// ---- workspace: the list of experts, the middle, then (not routed inline) the route's own
+// ---- workspace: the tiles, the rows' weights, the middle
 static size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
+// Most tiles of `most` rows: one partial one for each expert with rows.
+static int64_t most_tiles(int64_t E, int64_t R, int64_t most) { return R / most + (E < R ? E : R); }
+
 struct MoeSpace {
-  size_t slots, hi, lo, ids, weights, row_token, offsets, row_of, end;
+  size_t up, down, weights, mid, end;
 };
 static MoeSpace moe_space(int64_t T, int64_t E, int64_t topk, int64_t I) {
-  const size_t R = (size_t)(T * topk);
+  const int64_t R = T * topk;
   MoeSpace s;
-  s.slots = 16;
-  s.hi = s.slots + sizeof(MoeSlot) * (size_t)(E < (int64_t)R ? E : (int64_t)R);
-  s.lo = s.hi + up16(R * (size_t)I * 2);
-  s.ids = s.lo + up16(R * (size_t)I * 2);
-  s.weights = s.ids + up16(R * 4);
-  s.row_token = s.weights + up16(R * 4);
-  s.offsets = s.row_token + up16(R * 4);
-  s.row_of = s.offsets + up16((size_t)(E + 1) * 4);
-  s.end = s.row_of + up16(R * 4);
+  s.up = 16;
+  s.down = s.up + up16(sizeof(MoeTile) * (size_t)most_tiles(E, R, kUpRows));
+  s.weights = s.down + up16(sizeof(MoeTile) * (size_t)most_tiles(E, R, kDownRows));
+  s.mid = s.weights + up16((size_t)R * 4);
+  s.end = s.mid + up16((size_t)(2 * R * I) * 2);
   return s;
 }
 
@@ -582,23 +764,35 @@ size_t moe_workspace(int64_t T, int64_t E, int64_t topk, int64_t I) {
   return T == 0 ? 0 : moe_space(T, E, topk, I).end;
 }
 
-hipError_t launch_route(const void* x, int dt, int64_t T, int64_t E, int64_t ld, int score, const float* bias,
-                        int64_t G, int64_t topk_groups, int64_t group_top, int64_t topk, bool renorm, double scale,
-                        int32_t* ids, float* weights, int32_t* row_token, int32_t* offsets, int32_t* row_of,
-                        void* ws, hipStream_t stream);
+template <int FMT, bool F16, int NX, int NM>
+static hipError_t moe_stream(const MoeArgs& p, int64_t tiles, hipStream_t stream) {
+  constexpr int WU = 4, DU = 2, WD = 8, DD = 2;
+  hipLaunchKernelGGL((moe_up_kernel<FMT, F16, NX, WU, DU>), dim3((unsigned)(tiles * p.NT)), dim3(64 * WU), 0, stream, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((moe_down_kernel<FMT, F16, NM, WD, DD>), dim3((unsigned)(p.H / 16)), dim3(64 * WD),
+                     (size_t)WD * p.T * 64 + sizeof(MoeTile) * (size_t)most_tiles(p.E, (int64_t)p.T * p.topk, kDownRows), stream, p);
+  return hipGetLastError();
+}
 
-template <int FMT, bool F16, int RT>
+template <int FMT, bool F16>
 static hipError_t moe_go(MoeArgs& p, hipStream_t stream) {
-  constexpr int WU = 4, WD = 8;
   const int64_t R = (int64_t)p.T * p.topk;
   p.NT = p.I / 16;
-  const int64_t blocks = p.inl ? (R < p.E ? R : p.E) * p.NT : grouped_blocks(p.E, R, p.I, 16 * RT, 16);
-  hipLaunchKernelGGL((moe_up_kernel<FMT, F16, RT, WU, 2>), dim3((unsigned)blocks), dim3(64 * WU), 0, stream, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down_kernel<FMT, F16, RT, WD, RT == 1 ? 2 : 1>), dim3((unsigned)(p.H / 16)), dim3(64 * WD), 0,
-                     stream, p);
-  return hipGetLastError();
+  if (!p.inl) {
+    const bool general = p.route.bias || p.route.G > 1;
+    const size_t keys = p.route.G > 1 ? (size_t)8 * p.E * (kPThreads / kWave) : 0;
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(1), dim3(kPThreads), keys, stream, p); };
+    if (p.E <= 64) general ? go(moe_plan_kernel<1, true>) : go(moe_plan_kernel<1, false>);
+    else if (p.E <= 256) general ? go(moe_plan_kernel<4, true>) : go(moe_plan_kernel<4, false>);
+    else general ? go(moe_plan_kernel<16, true>) : go(moe_plan_kernel<16, false>);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  // up to 2 tokens tiles have at most 2 rows
+  constexpr int C = kCols<FMT> / 128;
+  return p.T <= 2 ? moe_stream<FMT, F16, 1, C>(p, p.inl ? (R < p.E ? R : p.E) : most_tiles(p.E, R, kUpRows), stream)
+                  : moe_stream<FMT, F16, 2 * C, 2 * C>(p, most_tiles(p.E, R, kUpRows), stream);
 }
 
 // fmt: 0 FP8 with block scales, 1 MXFP4, 2 int4 tiles (group: 128 m, or -1).
@@ -623,35 +817,20 @@ hipError_t launch_moe_decode(const void* x, bool f16, const void* logits, int dt
   p.G2 = group == -1 ? 1 : (int)(I / group);
   p.kg13 = (int)((group == -1 ? H : group) / 128);
   p.kg2 = (int)((group == -1 ? I : group) / 128);
-  p.nslots = reinterpret_cast<int32_t*>(base);
-  p.slots = reinterpret_cast<MoeSlot*>(base + sp.slots);
-  p.hi = reinterpret_cast<uint16_t*>(base + sp.hi);
-  p.lo = reinterpret_cast<uint16_t*>(base + sp.lo);
+  p.counts = reinterpret_cast<int32_t*>(base);
+  p.up = reinterpret_cast<MoeTile*>(base + sp.up);
+  p.down = reinterpret_cast<MoeTile*>(base + sp.down);
+  p.weights = reinterpret_cast<float*>(base + sp.weights);
+  p.mid = reinterpret_cast<uint16_t*>(base + sp.mid);
   RouteArgs& a = p.route;
   a.x = logits; a.bias = bias; a.T = T; a.ld = ld; a.dt = dt;
   a.E = (int)E; a.topk = (int)topk; a.G = (int)G; a.per_group = (int)(E / G);
   a.topk_groups = (int)topk_groups; a.group_top = (int)group_top; a.score = score; a.renorm = renorm ? 1 : 0;
   a.scale = scale;
-  a.ids = reinterpret_cast<int32_t*>(base + sp.ids);
-  a.weights = reinterpret_cast<float*>(base + sp.weights);
-  a.row_token = reinterpret_cast<int32_t*>(base + sp.row_token);
-  a.offsets = reinterpret_cast<int32_t*>(base + sp.offsets);
-  a.row_of = reinterpret_cast<int32_t*>(base + sp.row_of);
   p.inl = T <= kInline && E <= kInlineE;
-  if (!p.inl) {
-    const hipError_t e = launch_route(logits, dt, T, E, ld, score, bias, G, topk_groups, group_top, topk, renorm, scale,
-                                      a.ids, a.weights, a.row_token, a.offsets, a.row_of, nullptr, stream);
-    if (e != hipSuccess) return e;
-  }
-  auto by_rows = [&](auto f, auto h) {
-    constexpr int F = decltype(f)::value;
-    constexpr bool X = decltype(h)::value;
-    return T <= 16 ? moe_go<F, X, 1>(p, stream) : moe_go<F, X, 2>(p, stream);
-  };
-  auto by_type = [&](auto f) { return f16 ? by_rows(f, std::true_type{}) : by_rows(f, std::false_type{}); };
-  if (fmt == kFp8) return by_type(std::integral_constant<int, kFp8>{});
-  if (fmt == kMx) return by_type(std::integral_constant<int, kMx>{});
-  return by_type(std::integral_constant<int, kInt4>{});
+  if (fmt == kFp8) return f16 ? moe_go<kFp8, true>(p, stream) : moe_go<kFp8, false>(p, stream);
+  if (fmt == kMx) return f16 ? moe_go<kMx, true>(p, stream) : moe_go<kMx, false>(p, stream);
+  return f16 ? moe_go<kInt4, true>(p, stream) : moe_go<kInt4, false>(p, stream);
 }
 
 }  // namespace w4

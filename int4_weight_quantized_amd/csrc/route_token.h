@@ -52,30 +52,17 @@ __device__ __forceinline__ double lanes_sum(double v) {
   return lanes_reduce<L>(v, [](double a, double b) { return a + b; });
 }
 
-// The best (largest key, then lowest id) of the wave.
-template <int CTRL>
-__device__ __forceinline__ void best_step(double& key, int& id) {
-  const double o = dpp<CTRL>(key);
-  const int oi = dpp<CTRL>(id);
-  if (o > key || (o == key && oi < id)) {
-    key = o;
-    id = oi;
-  }
-}
-__device__ __forceinline__ void wave_best(double& key, int& id) {
-  best_step<0xB1>(key, id);
-  best_step<0x4E>(key, id);
-  best_step<0x141>(key, id);
-  best_step<0x140>(key, id);
+// The wave's largest key, the same in every lane: within rows of 16 lanes by DPP, the four rows' through scalar registers.
+__device__ __forceinline__ double wave_max64(double v) {
+  v = lanes_reduce<16>(v, [](double a, double b) { return fmax(a, b); });
+  const long long b = __double_as_longlong(v);
+  double r[4];
 #pragma unroll
-  for (int off = 16; off <= 32; off <<= 1) {
-    const double o = __shfl_xor(key, off, kWave);
-    const int oi = __shfl_xor(id, off, kWave);
-    if (o > key || (o == key && oi < id)) {
-      key = o;
-      id = oi;
-    }
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)b, 16 * i), hi = (uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), 16 * i);
+    r[i] = __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
   }
+  return fmax(fmax(r[0], r[1]), fmax(r[2], r[3]));
 }
 
 constexpr float kF32Max = 3.40282347e38f;
@@ -92,7 +79,28 @@ __device__ __forceinline__ float load_logit(const void* x, int64_t i) {
 template <int DT>
 __device__ __forceinline__ float logit_of(const RouteArgs& a, int64_t i) {
   if constexpr (DT < 3) return load_logit<DT>(a.x, i);
-  return a.dt == 0 ? load_logit<0>(a.x, i) : (a.dt == 1 ? load_logit<1>(a.x, i) : load_logit<2>(a.x, i));
+  if (a.dt == 2) return load_logit<2>(a.x, i);
+  const uint16_t v = static_cast<const uint16_t*>(a.x)[i];
+  return a.dt == 0 ? bf16_to_f32(v) : f16_to_f32(v);
+}
+
+// A lane's V logits of token t, -inf past the last expert.
+template <int DT, int V>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, int lane, float (&x)[V]) {
+  constexpr float kClosed = -__builtin_inff();
+  if constexpr (DT < 3) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = j * 64 + lane < a.E ? load_logit<DT>(a.x, t * a.ld + j * 64 + lane) : kClosed;
+  } else if (a.dt == 2) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = j * 64 + lane < a.E ? load_logit<2>(a.x, t * a.ld + j * 64 + lane) : kClosed;
+  } else {
+    uint16_t h[V];                                   // all loads, then one look at the type
+#pragma unroll
+    for (int j = 0; j < V; ++j) h[j] = j * 64 + lane < a.E ? static_cast<const uint16_t*>(a.x)[t * a.ld + j * 64 + lane] : 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = j * 64 + lane < a.E ? (a.dt == 0 ? bf16_to_f32(h[j]) : f16_to_f32(h[j])) : kClosed;
+  }
 }
 
 __device__ __forceinline__ double score_of(float x, int score, float top) {
@@ -123,11 +131,11 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
                                             double* mine, int& my_id, double& w) {
   const double kLow = -__builtin_inf();
   float x[V];
+  load_logits<DT>(a, t, lane, x);
   float top = -__builtin_inff();
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int e = j * 64 + lane;
-    const float v = e < a.E ? logit_of<DT>(a, t * a.ld + e) : -__builtin_inff();
+    const float v = x[j];
     x[j] = v > -__builtin_inff() ? fminf(v, kF32Max) : -__builtin_inff();   // NaN: closed
     top = fmaxf(top, x[j]);
   }
@@ -197,15 +205,16 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
   my_id = -1;
   for (int i = 0; i < a.topk; ++i) {
     double best = kLow;
-    int id = 0x7FFFFFFF;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        id = j * 64 + lane;
-      }
-    wave_best(best, id);
+    for (int j = 0; j < V; ++j) best = fmax(best, key[j]);
+    best = wave_max64(best);
     if (!(best > kLow)) break;                         // nothing left (uniform)
+    int id = 0;                                        // the lowest expert that holds it
+#pragma unroll
+    for (int j = V - 1; j >= 0; --j) {
+      const unsigned long long hit = __ballot(key[j] == best);
+      id = hit ? j * 64 + __ffsll(hit) - 1 : id;
+    }
     if (lane == i) my_id = id;
 #pragma unroll
     for (int j = 0; j < V; ++j)
