@@ -204,22 +204,28 @@ __device__ __forceinline__ typename Operand<F16>::V decode(const v4i (&w)[2], in
   return __builtin_bit_cast(typename Operand<F16>::V, r);
 }
 
-// The scales of a step, of MATS sets of 16 rows (the second `gap` rows after the first), by one DMA. FP8: a float for each
-// set; MXFP4: 16 bytes of each row (8 are the step's); int4: half q, set m: 16 fp16.
+// The scales of MATS sets of 16 rows (the second `gap` rows after the first). FP8 and MXFP4: of 8 steps at a time, with the
+// first of them (steps one by one would ask for a cache line that is still on its way, which holds up the whole cache: 46 us
+// of one token's gate and up products where 8 at a time take $UP): FP8 8 floats of each set; MXFP4 64 bytes of each row,
+// piece c of row r at 64 r + 16 (c ^ (r / 4 & 3)). int4: of each step: half q, set m: 16 fp16.
 template <int FMT, int MATS>
 struct Scales {
-  static constexpr int kLanes = FMT == kFp8 ? MATS : 16 * MATS;
-  static constexpr int kBytes = FMT == kMx ? 256 * MATS : 64 * MATS;
+  static constexpr int kSteps = FMT == kInt4 ? 1 : 8;
+  static constexpr int kDmas = FMT == kMx ? MATS : 1;
+  static constexpr int kLanes = FMT == kMx ? 64 : (FMT == kFp8 ? 8 : 16) * MATS;
+  static constexpr int kBytes = FMT == kMx ? 1024 * MATS : 64 * MATS;
   __amdgpu_buffer_rsrc_t s;
-  uint32_t off;
+  uint32_t off, next;                                // next: from set to set
   int per, N, halves;
   __device__ __forceinline__ void lane(int64_t N_, int64_t n, int64_t gap, int64_t K, int per_, int lane) {
     per = per_;
     N = (int)N_;
     if constexpr (FMT == kFp8) {
-      off = (uint32_t)((n + lane * gap) / 128 * ((K + 127) / 128) * 4);
+      off = (uint32_t)((n + (lane >> 3) * gap) / 128 * ((K + 127) / 128) * 4 + 4 * (lane & 7));
     } else if constexpr (FMT == kMx) {
-      off = (uint32_t)(((lane >> 4) * gap + (lane & 15)) * mx_scale_bytes(K));
+      const int r = lane >> 2;
+      off = (uint32_t)(r * mx_scale_bytes(K) + 16 * ((lane & 3) ^ (r >> 2 & 3)));
+      next = (uint32_t)(gap * mx_scale_bytes(K));
     } else {
       halves = (int)(K / 128);
       off = (uint32_t)((n + (lane >> 3) % MATS * gap) * 2 + 4 * (lane & 7));
@@ -237,22 +243,26 @@ struct Scales {
       s = make_rsrc(b + e * G * N_ * 2, (uint32_t)(G * N_ * 2));
     }
   }
+  // begins: whether a step's scales come with it (a run's first step, and every kSteps)
+  static __device__ __forceinline__ bool begins(int k) { return k % kSteps == 0; }
   __device__ __forceinline__ void fetch(int k, uint32_t dst, int lane) const {
+    dst = __builtin_amdgcn_readfirstlane(dst);       // (the compiler does not see that it is uniform)
     if (lane >= kLanes) return;
     if constexpr (FMT == kFp8) {
-      dma4(s, dst, off, (uint32_t)k * 4);
+      dma4(s, dst, off, (uint32_t)(k & ~7) * 4);
     } else if constexpr (FMT == kMx) {
-      dma16(s, dst, off, (uint32_t)k * 8);
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) dma16(s, dst + 1024 * m, off + m * next, (uint32_t)(k & ~7) * 8);
     } else {
       // (the second half of an odd number's last step: the first's)
       const int a = 2 * k / per * N * 2, b = min(2 * k + 1, halves - 1) / per * N * 2;
       dma4(s, dst, off + (lane < 8 * MATS ? (uint32_t)a : (uint32_t)b), 0u);
     }
   }
-  // what multiplies the sums of rows 4 g .. 4 g + 3 of set m over half q
-  static __device__ __forceinline__ v4f sums(const uint8_t* at, int m, int q, int g) {
+  // what multiplies the sums of rows 4 g .. 4 g + 3 of set m over half q of step k
+  static __device__ __forceinline__ v4f sums(const uint8_t* at, int k, int m, int q, int g) {
     if constexpr (FMT == kFp8) {
-      const float v = reinterpret_cast<const float*>(at)[m];
+      const float v = reinterpret_cast<const float*>(at)[8 * m + (k & 7)];
       return v4f{v, v, v, v};
     } else {
       const v2i v = *reinterpret_cast<const v2i*>(at + 32 * (MATS * q + m) + 8 * g);
@@ -260,9 +270,10 @@ struct Scales {
                  f16_to_f32((uint16_t)((uint32_t)v[1] >> 16))};
     }
   }
-  // MXFP4: a lane's scale of half q; left: the columns from the step's first to the end
-  static __device__ __forceinline__ float block(const uint8_t* at, int m, int q, int left, int l16, int g) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(at + 16 * (16 * m + l16) + 4 * q);
+  // MXFP4: a lane's scale of half q of step k; left: the columns from the step's first to the end
+  static __device__ __forceinline__ float block(const uint8_t* at, int k, int m, int q, int left, int l16, int g) {
+    const int piece = (k & 7) >> 1 ^ (l16 >> 2 & 3);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(at + 1024 * m + 64 * l16 + 16 * piece + 8 * (k & 1) + 4 * q);
     const uint32_t c = 128 * q + 32 * g < left ? w >> (8 * g) & 0xFF : 0u;   // past K: the padding, or the next row's
     return c == kMxNan ? __uint_as_float(0x7FC00000u) : mx_scale_value(c);
   }
@@ -438,11 +449,13 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
   constexpr int COLS = kCols<FMT>, HALVES = FMT == kFp8 ? 1 : 2;
   using Op = typename Operand<OPF16>::V;
   using S = Scales<FMT, 2>;
-  // a step in LDS: gate, up, activations, scales
-  constexpr int kX = 4096, kS = kX + 1024 * NX, kSlot = kS + S::kBytes, kDmas = 4 + NX + 1;
+  // a step in LDS: gate, up, activations; and the scales in places of their own. kDmas: the fewest of a step
+  constexpr int kX = 4096, kSlot = kX + 1024 * NX, kDmas = 4 + NX + (S::kSteps == 1 ? S::kDmas : 0);
   __shared__ __attribute__((aligned(16))) union {
     InlinePlan plan;
-    uint8_t ring[WS][D][kSlot];
+    struct {
+      uint8_t ring[WS][D][kSlot], scales[WS][D][S::kBytes];
+    } r;
     v4f red[WS][2][64];
   } s;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -482,9 +495,13 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
     xdead[j] = col >= p.H - (KT - 1) * COLS;
   }
   const uint32_t ring0 =
-      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&s.ring[wave][0][0]);
+      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&s.r.ring[wave][0][0]);
+  const uint32_t scales0 =
+      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&s.r.scales[wave][0][0]);
   const int k0 = KT * wave / WS, k1 = KT * (wave + 1) / WS;
+  int fs = -1, cs = -1;                              // the scales' places that were fetched and are used last
   auto fetch = [&](int k, int d) {                   // past the run's end: the last step again, not used
+    const bool begins = k == k0 || (k < k1 && S::begins(k));
     k = min(k, k1 - 1);
     const uint32_t at = ring0 + d * kSlot;
     const bool last = k == KT - 1;
@@ -492,7 +509,10 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
     wu.fetch(k, last, at + 2048);
 #pragma unroll
     for (int j = 0; j < NX; ++j) dma16(xr, at + kX + 1024 * j, last && xdead[j] ? kPast : xo[j], (uint32_t)k * (2 * COLS));
-    sc.fetch(k, at + kS, lane);
+    if (begins || S::kSteps == 1) {
+      fs = fs + 1 == D ? 0 : fs + 1;
+      sc.fetch(k, scales0 + fs * S::kBytes, lane);
+    }
   };
   const uint32_t taken = l16 >= 8 ? 0xFFFF0000u : 0u;
   v4f ag = v4f{0.f, 0.f, 0.f, 0.f}, au = ag;
@@ -501,7 +521,9 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
     for (int d = 0; d < D; ++d) fetch(k0 + d, d);
     int d = 0;
     for (int k = k0; k < k1; ++k) {
-      const uint8_t* at = &s.ring[wave][d][0];
+      const uint8_t* at = &s.r.ring[wave][d][0];
+      if (k == k0 || S::begins(k)) cs = cs + 1 == D ? 0 : cs + 1;
+      const uint8_t* as = &s.r.scales[wave][cs][0];
       asm volatile("s_waitcnt vmcnt(%0)" :: "n"((D - 1) * kDmas) : "memory");
       v4i qg[2], qu[2], X[HALVES][4];
       float lg[HALVES], lu[HALVES];
@@ -518,11 +540,11 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
           X[q][c] = act_chunk<FMT>(at + kX, row & (kRowsPerDma<FMT> * NX - 1),
                                    FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
         if constexpr (FMT == kMx) {
-          lg[q] = S::block(at + kS, 0, q, p.H - k * COLS, l16, g);
-          lu[q] = S::block(at + kS, 1, q, p.H - k * COLS, l16, g);
+          lg[q] = S::block(as, k, 0, q, p.H - k * COLS, l16, g);
+          lu[q] = S::block(as, k, 1, q, p.H - k * COLS, l16, g);
         } else {
-          mg[q] = S::sums(at + kS, 0, q, g);
-          mu[q] = S::sums(at + kS, 1, q, g);
+          mg[q] = S::sums(as, k, 0, q, g);
+          mu[q] = S::sums(as, k, 1, q, g);
         }
       }
       // the step is in registers: its place takes the one D on
@@ -601,9 +623,9 @@ template <int FMT, bool F16OUT, int NM, int WS, int D>
 __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
   constexpr int COLS = kCols<FMT>, HALVES = FMT == kFp8 ? 1 : 2;
   using S = Scales<FMT, 1>;
-  constexpr int kX = 2048, kS = kX + 1024 * NM, kSlot = kS + S::kBytes, kDmas = 2 + NM + 1;
+  constexpr int kX = 2048, kSlot = kX + 1024 * NM, kDmas = 2 + NM + (S::kSteps == 1 ? S::kDmas : 0);
   constexpr int kMost = kRowsPerDma<FMT> * NM / 2;   // rows that fit
-  __shared__ __attribute__((aligned(16))) uint8_t ring[WS][D][kSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t ring[WS][D][kSlot], scales[WS][D][S::kBytes];
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   v4f* sum = reinterpret_cast<v4f*>(smem);           // [WS][T][4]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -620,6 +642,8 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
   const int i0 = (int)((int64_t)steps * wave / WS), i1 = (int)((int64_t)steps * (wave + 1) / WS);
   const uint32_t ring0 =
       __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&ring[wave][0][0]);
+  const uint32_t scales0 =
+      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&scales[wave][0][0]);
   uint32_t mo[NM];
   bool mdead[NM];
 #pragma unroll
@@ -630,6 +654,7 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
   }
   // the tile and step that are fetched next, and those that are computed
   int ft = i0 / KT, fk = i0 - ft * KT, ct = ft, ck = fk;
+  int fs = -1, cs = -1;                              // the scales' places that were fetched and are used last
   Rows<FMT> w;
   S sc;
   int rows = 0;
@@ -642,7 +667,7 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
     w.open(p.w2, e, p.H, n0, p.I);
     sc.open(p.s2, e, p.H, n0, 0, p.I, p.G2);
   };
-  auto fetch = [&](int d) {
+  auto fetch = [&](int d, bool first) {
     const uint32_t at = ring0 + d * kSlot;
     const bool last = fk == KT - 1;
     w.fetch(fk, last, at);
@@ -650,7 +675,10 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
     for (int j = 0; j < NM; ++j)
       dma16(mr, at + kX + 1024 * j, (act_row<FMT>(j, lane) >> 1) >= rows || (last && mdead[j]) ? kPast : mo[j] + row0,
             (uint32_t)fk * (2 * COLS));
-    sc.fetch(fk, at + kS, lane);
+    if (first || S::begins(fk)) {
+      fs = fs + 1 == D ? 0 : fs + 1;
+      sc.fetch(fk, scales0 + fs * S::kBytes, lane);
+    }
     if (++fk == KT) {
       fk = 0;
       ++ft;
@@ -663,11 +691,13 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
     sc.lane(p.H, n0, 0, p.I, p.kg2, lane);
     open_tile();
 #pragma unroll
-    for (int d = 0; d < D; ++d) fetch(d);
+    for (int d = 0; d < D; ++d) fetch(d, d == 0);
     const int mrow = (2 * (l16 & 7) + (l16 >> 3)) & (2 * kMost - 1);
     int d = 0;
     for (int i = i0; i < i1; ++i) {
       const uint8_t* at = &ring[wave][d][0];
+      if (i == i0 || S::begins(ck)) cs = cs + 1 == D ? 0 : cs + 1;
+      const uint8_t* as = &scales[wave][cs][0];
       asm volatile("s_waitcnt vmcnt(%0)" :: "n"((D - 1) * kDmas) : "memory");
       v4i qw[2], M[HALVES][4];
       float ls[HALVES];
@@ -679,12 +709,12 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           M[q][c] = act_chunk<FMT>(at + kX, mrow, FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
-        if constexpr (FMT == kMx) ls[q] = S::block(at + kS, 0, q, p.I - ck * COLS, l16, g);
-        else ms[q] = S::sums(at + kS, 0, q, g);
+        if constexpr (FMT == kMx) ls[q] = S::block(as, ck, 0, q, p.I - ck * COLS, l16, g);
+        else ms[q] = S::sums(as, ck, 0, q, g);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      fetch(d);
+      fetch(d, false);
       __builtin_amdgcn_sched_barrier(0);
       d = d + 1 == D ? 0 : d + 1;
 #pragma unroll
