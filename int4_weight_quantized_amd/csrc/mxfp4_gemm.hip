@@ -23,6 +23,8 @@
 // - The weights are the A operand and the activations the B operand: a lane's
 //   results lie in one activation row. Row q of a weight fragment is its column
 //   16 (q / 4 % 2) + 4 (q / 8) + q % 4, which gives a lane 16 consecutive ones.
+#include <type_traits>
+
 #include "mxfp4.h"
 
 namespace w4 {
@@ -67,8 +69,11 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
     const int64_t t = xcd_remap((int)blockIdx.x, (int)gridDim.x);
     split = (int)(t / p.tiles);
     const int64_t tile = t - (int64_t)split * p.tiles;
-    r0 = tile / p.NT * BM;
-    tn = (int)(tile % p.NT);
+    // four row tiles at a time, column by column: the tiles that an XCD holds at once share rows and columns
+    const int64_t MT = p.tiles / p.NT, grp = tile / (4 * p.NT);
+    const int rows = (int)min((int64_t)4, MT - 4 * grp), in = (int)(tile - grp * 4 * p.NT);
+    r0 = (4 * grp + in % rows) * BM;
+    tn = in / rows;
     row_end = p.M;
   }
   const int n0 = tn * BN;
@@ -102,7 +107,7 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
 #pragma unroll
   for (int i = 0; i < RA; ++i) {
     const int r = (TH / 8) * i + 8 * wave + lrow;
-    const int c = lchunk ^ (r & 7);
+    const int c = lchunk ^ ((r >> 1) & 7);
     const int64_t t = token(r);
     a_off[i] = t >= 0 ? (uint32_t)(t * KH + 16 * c) : kPast;
     if (32 * c >= klast) a_dead |= 1u << i;
@@ -110,7 +115,7 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
     const int r = (TH / 8) * i + 8 * wave + lrow;
-    const int c = lchunk ^ ((r & 3) + 4 * ((r >> 4) & 1));
+    const int c = lchunk ^ (((r >> 1) & 3) + 4 * ((r >> 4) & 1));
     b_off[i] = n0 + r < p.N ? (uint32_t)(r * KH + 16 * c) : kPast;
     if (32 * c >= klast) b_dead |= 1u << i;
   }
@@ -132,27 +137,25 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(dst), "v"(off), "s"(rs), "s"(ks) : "memory");
   };
-  // DMA q of a step: the activations' RA, the weights' RB, then every second step the scales' RS
+  // DMA q of a step: the activations' RA, the weights' RB, then with every second step the scales' RS (of steps past K:
+  // whatever follows, not used). Steps past the split's end read no memory.
   constexpr int ND = RA + RB + RS;
-  auto gload1 = [&](int tk, uint32_t stage, int q) {
+  auto gload1 = [&](int tk, uint32_t stage, int q) __attribute__((always_inline)) {
     if (q >= RA + RB) {
-      const int i = q - RA - RB, rel = tk - k0;
+      const int i = q - RA - RB;
       const int grp = NW * i + wave;                 // 64 rows
-      if ((rel & 1) || 64 * grp >= BM + BN) return;
-      const uint32_t dst = lds0 + 2 * STAGE + ((rel >> 1) & 1) * SCALES + 1024 * grp;
-      if (64 * grp < BM) dma(asr, dst, s_off[i], (uint32_t)tk * 8);
-      else dma(wsr, dst, s_off[i], (uint32_t)tk * 8);
+      if (64 * grp >= BM + BN) return;
+      const uint32_t dst = lds0 + 2 * STAGE + (((tk - k0) >> 1) & 1) * SCALES + 1024 * grp;
+      const uint32_t off = tk < k1 ? s_off[i] : kPast;
+      if (64 * grp < BM) dma(asr, dst, off, (uint32_t)tk * 8);
+      else dma(wsr, dst, off, (uint32_t)tk * 8);
       return;
     }
     const bool act = q < RA;
     const int i = act ? q : q - RA;
     uint32_t off = act ? a_off[i] : b_off[i];
-    if (tk == p.KT - 1 && (((act ? a_dead : b_dead) >> i) & 1)) off = kPast;
+    if (tk >= k1 || (tk == p.KT - 1 && (((act ? a_dead : b_dead) >> i) & 1))) off = kPast;
     dma(act ? arsrc : wrsrc, ldsw + stage + ((act ? 0 : BM) + (TH / 8) * i) * kMB, off, (uint32_t)tk * kMB);
-  };
-  auto gload = [&](int tk, uint32_t stage) {
-#pragma unroll
-    for (int q = 0; q < ND; ++q) gload1(tk, stage, q);
   };
 
   v16f acc[MI][NJ];
@@ -166,7 +169,7 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
   // ---- fragments
   const int ar = 32 * MI * wm + l32;                 // + 32 i, which leaves f unchanged
   const int br = 32 * NJ * wn + 16 * ((l32 >> 2) & 1) + 4 * (l32 >> 3) + (l32 & 3);   // + 32 j, likewise
-  const int af7 = l32 & 7, bf7 = (l32 & 3) + 4 * ((l32 >> 2) & 1);
+  const int af7 = (l32 >> 1) & 7, bf7 = ((br >> 1) & 3) + 4 * ((br >> 4) & 1);
   auto afrag = [&](uint32_t stage, int i, int c) -> v4i {
     return *reinterpret_cast<const v4i*>(lds + stage + (ar + 32 * i) * kMB + 16 * ((4 * h + c) ^ af7));
   };
@@ -181,76 +184,99 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
   auto scale = [&](int tk, int row) -> int {
     const int rel = tk - k0;
     const uint8_t* q = lds + 2 * STAGE + ((rel >> 1) & 1) * SCALES + row * 16 + 8 * (rel & 1) + 4 * h;
-    return *reinterpret_cast<const int*>(q) & (tk == p.KT - 1 ? smask : -1);
+    return *reinterpret_cast<const int*>(q) & (tk < k1 ? (tk == p.KT - 1 ? smask : -1) : 0);
   };
 
   constexpr int NM = MI * NJ;
   if (k0 < k1) {
-    gload(k0, 0);
+#pragma unroll
+    for (int q = 0; q < ND; ++q) gload1(k0, 0, q);
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    if (k0 + 1 < k1) gload(k0 + 1, STAGE);
+#pragma unroll
+    for (int q = 0; q < RA + RB; ++q) gload1(k0 + 1, STAGE, q);
     if (GROUPED && r0 + 32 * MI * wm >= row_end) {   // a wave whose rows all lie past the segment only fetches
-      for (int tk = k0; tk < k1; ++tk) {
-        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-        if (tk + 2 < k1) gload(tk + 2, ((tk - k0) & 1) * STAGE);
+      for (int tk = k0; tk < k1 + ((k1 - k0) & 1); ++tk) {   // as many barriers as the others
+        asm volatile("s_barrier" ::: "memory");
+        const bool odd = (tk - k0) & 1;
+#pragma unroll
+        for (int q = 0; q < ND; ++q)
+          if (q < RA + RB || !odd) gload1(tk + 2, odd * STAGE, q);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"(RA + RB) : "memory");
       }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       return;
     }
-    v4i af[2][MI], bf[2][NJ];
-    int sa[MI], sb[NJ];
+    v4i af[4][MI], bf[4][NJ];
+    int sa[2][MI], sb[2][NJ];                        // by the step's parity
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       af[0][i] = afrag(0, i, 0);
-      sa[i] = scale(k0, ar + 32 * i);
+      sa[0][i] = scale(k0, ar + 32 * i);
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       bf[0][j] = bfrag(0, j, 0);
-      sb[j] = scale(k0, BM + br + 32 * j);
+      sb[0][j] = scale(k0, BM + br + 32 * j);
     }
-    for (int tk = k0; tk < k1; ++tk) {
-      const uint32_t st = ((tk - k0) & 1) * STAGE;   // this step's stage
-      int sa2[MI], sb2[NJ];
+    // One step; P: its parity, and so its stage. No branch inside, and every MFMA is pinned where it stands (the empty
+    // statement names its result): left alone the compiler sinks all 64 behind the barrier and reads every fragment first.
+    auto step = [&](auto parity, int tk) __attribute__((always_inline)) {
+      constexpr int P = decltype(parity)::value;
+      constexpr uint32_t st = P * STAGE;
+      constexpr int NF = MI + NJ;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int cur = c & 1, nxt = cur ^ 1;
-        if (c == 3) {
-          // every fragment of this step is in registers; once the next step's tiles have landed: swap
-          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (c == 1) {
+          // every fragment of this step is in every wave's registers: its stage is free
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
           __builtin_amdgcn_sched_barrier(0);
         }
-        const uint32_t from = c == 3 ? STAGE - st : st;
+        if (c == 3) {
+          // the next step's tiles have landed (what was issued since is the step after's)
+          asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"(RA + RB + (P == 0 && NW * 64 * RS == BM + BN ? RS : 0)) : "memory");
+          __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int n = 0; n < NM; ++n) {
           const int i = n / NJ, j = n % NJ;
-          // the next group's fragments (at the end: of a stage whose contents are not used)
+          if (c == 0) {                              // groups 1 to 3's fragments
 #pragma unroll
-          for (int q = n * (MI + NJ) / NM; q < (n + 1) * (MI + NJ) / NM; ++q) {
-            if (q < NJ) bf[nxt][q] = bfrag(from, q, (c + 1) & 3);
-            else af[nxt][q - NJ] = afrag(from, q - NJ, (c + 1) & 3);
-            if (c == 3) {
-              if (q < NJ) sb2[q] = scale(tk + 1, BM + br + 32 * q);
-              else sa2[q - NJ] = scale(tk + 1, ar + 32 * (q - NJ));
+            for (int q = n * 3 * NF / NM; q < (n + 1) * 3 * NF / NM; ++q) {
+              if (q % NF < NJ) bf[1 + q / NF][q % NF] = bfrag(st, q % NF, 1 + q / NF);
+              else af[1 + q / NF][q % NF - NJ] = afrag(st, q % NF - NJ, 1 + q / NF);
             }
           }
-          if (c == 0) acc[i][j] = mx_mfma<0>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
-          if (c == 1) acc[i][j] = mx_mfma<1>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
-          if (c == 2) acc[i][j] = mx_mfma<2>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
-          if (c == 3) {
-            acc[i][j] = mx_mfma<3>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
-            if (tk + 2 < k1) {
+          if (c == 3) {                              // the next step's group 0 (at the end: of a stage whose contents are not used)
 #pragma unroll
-              for (int q = n * ND / NM; q < (n + 1) * ND / NM; ++q) gload1(tk + 2, st, q);
+            for (int q = n * NF / NM; q < (n + 1) * NF / NM; ++q) {
+              if (q < NJ) {
+                bf[0][q] = bfrag(STAGE - st, q, 0);
+                sb[1 - P][q] = scale(tk + 1, BM + br + 32 * q);
+              } else {
+                af[0][q - NJ] = afrag(STAGE - st, q - NJ, 0);
+                sa[1 - P][q - NJ] = scale(tk + 1, ar + 32 * (q - NJ));
+              }
             }
+          }
+          if (c == 0) acc[i][j] = mx_mfma<0>(bf[0][j], af[0][i], acc[i][j], sb[P][j], sa[P][i]);
+          if (c == 1) acc[i][j] = mx_mfma<1>(bf[1][j], af[1][i], acc[i][j], sb[P][j], sa[P][i]);
+          if (c == 2) acc[i][j] = mx_mfma<2>(bf[2][j], af[2][i], acc[i][j], sb[P][j], sa[P][i]);
+          if (c == 3) acc[i][j] = mx_mfma<3>(bf[3][j], af[3][i], acc[i][j], sb[P][j], sa[P][i]);
+          asm volatile("" : "+a"(acc[i][j]));
+          if (c == 1) {
+            constexpr int NDP = P == 0 ? ND : RA + RB;
+#pragma unroll
+            for (int q = n * NDP / NM; q < (n + 1) * NDP / NM; ++q) gload1(tk + 2, st, q);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-#pragma unroll
-      for (int i = 0; i < MI; ++i) sa[i] = sa2[i];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) sb[j] = sb2[j];
+    };
+    for (int tk = k0; tk < k1; tk += 2) {            // an odd number's last step adds zeros
+      step(std::integral_constant<int, 0>{}, tk);
+      step(std::integral_constant<int, 1>{}, tk + 1);
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
 
   // ---- output: lane's row per i, 16 consecutive columns per j
