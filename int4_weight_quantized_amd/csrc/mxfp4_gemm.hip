@@ -279,23 +279,57 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
 
-  // ---- output: lane's row per i, 16 consecutive columns per j
+  // ---- output. A lane's results are 16 columns of one row, which as stores would be half a cache line from each of 32
+  // rows; 32 rows at a time go through the wave's own LDS and leave as whole rows. Chunk c (16 bytes) of row r lies at c ^
+  // f(r), so that 16 lanes that write one chunk of 16 rows, or read 16 of a row, fill the banks.
+  constexpr int SZ = OUT == 2 ? 4 : 2, CH = 32 * NJ * SZ / 16, PER = 16 / SZ;   // chunks of a row, columns of a chunk
+  static_assert(CH >= 8 && NW * 32 * CH * 16 <= 2 * STAGE, "the waves' rows fit the stages");
+  auto swizzle = [](int r) { return CH == 8 ? (r >> 1) & 7 : r & 15; };
+  __syncthreads();                                   // no wave's tiles are on their way any more
+  uint8_t* mine = lds + wave * (32 * CH * 16);
+  const int nw = n0 + 32 * NJ * wn;
+  const int col = nw + PER * (lane % CH), row = lane / CH;
+  constexpr int RPI = 64 / CH;                       // rows of a store
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int64_t r = r0 + 32 * (MI * wm + i) + l32;
-    if (r >= row_end) continue;
-    const int64_t orow = (out0 + r + (int64_t)split * p.M) * p.N;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
+      float f[16];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int n = n0 + 32 * (NJ * wn + j) + 16 * h + 8 * q;
-        if (n >= p.N) continue;
-        float f[8];
+      for (int c = 0; c < 16; ++c) f[c] = acc[i][j][c];
+      if (!GROUPED && p.bias && p.splits == 1) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) f[c] = acc[i][j][8 * q + c];
-        store_columns<OUT, 8>(p, f, orow, n, !GROUPED && p.bias && p.splits == 1);
+        for (int c = 0; c < 16; ++c) {
+          const int n = min(nw + 32 * j + 16 * h + c, p.N - 1);
+          f[c] += OUT == 2 ? static_cast<const float*>(p.bias)[n]
+                           : (OUT == 0 ? bf16_to_f32(static_cast<const uint16_t*>(p.bias)[n])
+                                       : f16_to_f32(static_cast<const uint16_t*>(p.bias)[n]));
+        }
       }
+#pragma unroll
+      for (int q = 0; q < SZ; ++q) {                 // SZ chunks of the lane's 16 columns
+        v4i w;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if constexpr (OUT == 2) {
+            w[c] = __float_as_int(f[4 * q + c]);
+          } else {
+            const float x = f[8 * q + 2 * c], y = f[8 * q + 2 * c + 1];
+            w[c] = (int)(OUT == 0 ? f32_to_bf16_rne(x) | (uint32_t)f32_to_bf16_rne(y) << 16
+                                  : f32_to_f16_rne(x) | (uint32_t)f32_to_f16_rne(y) << 16);
+          }
+        }
+        *reinterpret_cast<v4i*>(mine + (l32 * CH + ((2 * j + h) * SZ + q ^ swizzle(l32))) * 16) = w;
+      }
+    }
+    const int64_t r = r0 + 32 * (MI * wm + i) + row;
+    uint8_t* o = static_cast<uint8_t*>(p.out) + ((out0 + r + (int64_t)split * p.M) * p.N + col) * SZ;
+#pragma unroll
+    for (int k = 0; k < 32 / RPI; ++k) {
+      const int rr = row + RPI * k;
+      const v4i w = *reinterpret_cast<const v4i*>(mine + (rr * CH + (lane % CH ^ swizzle(rr))) * 16);
+      if (r + RPI * k < row_end && col < p.N) *reinterpret_cast<v4i*>(o) = w;
+      o += (int64_t)RPI * p.N * SZ;
     }
   }
 }
