@@ -39,6 +39,14 @@ __device__ __forceinline__ v16f mx_mfma(v4i w, v4i a, v16f d, int sw, int sa) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(w), mx_operand(a), d, 4, 4, C, sw, C, sa);
 }
 
+// Two results as bf16 (OUT 0) or fp16, nearest even.
+template <int OUT>
+__device__ __forceinline__ int pack16(float x, float y) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  if constexpr (OUT == 0) return __builtin_bit_cast(int, __builtin_convertvector(v2f{x, y}, v2bf));
+  else return __builtin_bit_cast(int, __builtin_convertvector(v2f{x, y}, v2h));
+}
+
 // OUT: 0 bf16, 1 fp16, 2 fp32.
 template <int WM, int WN, int MI, int NJ, bool GROUPED, int OUT>
 __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_kernel(MxArgs p) {
@@ -66,18 +74,18 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
     out0 = s.row0;
     row_end = s.rows;
   } else {
-    const int64_t t = xcd_remap((int)blockIdx.x, (int)gridDim.x);
-    split = (int)(t / p.tiles);
-    const int64_t tile = t - (int64_t)split * p.tiles;
+    const int t = xcd_remap((int)blockIdx.x, (int)gridDim.x), tiles = (int)p.tiles;   // below 2^24
+    split = t / tiles;
+    const int tile = t - split * tiles;
     // four row tiles at a time, column by column: the tiles that an XCD holds at once share rows and columns
-    const int64_t MT = p.tiles / p.NT, grp = tile / (4 * p.NT);
-    const int rows = (int)min((int64_t)4, MT - 4 * grp), in = (int)(tile - grp * 4 * p.NT);
-    r0 = (4 * grp + in % rows) * BM;
+    const int MT = tiles / p.NT, grp = tile / (4 * p.NT);
+    const int rows = min(4, MT - 4 * grp), in = tile - grp * 4 * p.NT;
+    r0 = (int64_t)(4 * grp + in % rows) * BM;
     tn = in / rows;
     row_end = p.M;
   }
   const int n0 = tn * BN;
-  const int k0 = (int)((int64_t)p.KT * split / p.splits), k1 = (int)((int64_t)p.KT * (split + 1) / p.splits);
+  const int k0 = p.KT * split / p.splits, k1 = p.KT * (split + 1) / p.splits;   // KT at most 2^14, splits 2^9
   const int64_t KH = p.K >> 1;                       // code bytes of a row
 
   // ---- LDS DMA: a wave's load fills 8 rows (one KiB), lane L at row L / 8, physical 16-byte chunk L % 8. Row r holds
@@ -158,13 +166,16 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
     dma(act ? arsrc : wrsrc, ldsw + stage + ((act ? 0 : BM) + (TH / 8) * i) * kMB, off, (uint32_t)tk * kMB);
   };
 
-  v16f acc[MI][NJ];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
+  // the accumulators start from the bias, of 16 consecutive columns each (without one an empty buffer, which reads as zero)
+  constexpr int SZ = OUT == 2 ? 4 : 2;               // bytes of a result
+  v4i bias[NJ][SZ];
+  if constexpr (!GROUPED) {
+    const __amdgpu_buffer_rsrc_t brs = make_rsrc(p.bias, p.bias && p.splits == 1 ? (uint32_t)p.N * SZ : 0u);
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+      for (int q = 0; q < SZ; ++q) bias[j][q] = buffer_load16(brs, (uint32_t)(n0 + 32 * (NJ * wn + j) + 16 * h) * SZ + 16 * q);
+  }
 
   // ---- fragments
   const int ar = 32 * MI * wm + l32;                 // + 32 i, which leaves f unchanged
@@ -191,6 +202,24 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
   if (k0 < k1) {
 #pragma unroll
     for (int q = 0; q < ND; ++q) gload1(k0, 0, q);
+  }
+  v16f acc[MI][NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    v16f f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      if constexpr (GROUPED) f[c] = 0.f;
+      else if constexpr (OUT == 2) f[c] = __int_as_float(bias[j][c / 4][c % 4]);
+      else {
+        const uint16_t b = (uint16_t)((uint32_t)bias[j][c / 8][c % 8 / 2] >> (16 * (c % 2)));
+        f[c] = OUT == 0 ? bf16_to_f32(b) : f16_to_f32(b);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) acc[i][j] = f;
+  }
+  if (k0 < k1) {
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
     for (int q = 0; q < RA + RB; ++q) gload1(k0 + 1, STAGE, q);
@@ -282,7 +311,7 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
   // ---- output. A lane's results are 16 columns of one row, which as stores would be half a cache line from each of 32
   // rows; 32 rows at a time go through the wave's own LDS and leave as whole rows. Chunk c (16 bytes) of row r lies at c ^
   // f(r), so that 16 lanes that write one chunk of 16 rows, or read 16 of a row, fill the banks.
-  constexpr int SZ = OUT == 2 ? 4 : 2, CH = 32 * NJ * SZ / 16, PER = 16 / SZ;   // chunks of a row, columns of a chunk
+  constexpr int CH = 32 * NJ * SZ / 16, PER = 16 / SZ;   // chunks of a row, columns of a chunk
   static_assert(CH >= 8 && NW * 32 * CH * 16 <= 2 * STAGE, "the waves' rows fit the stages");
   auto swizzle = [](int r) { return CH == 8 ? (r >> 1) & 7 : r & 15; };
   __syncthreads();                                   // no wave's tiles are on their way any more
@@ -290,45 +319,29 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
   const int nw = n0 + 32 * NJ * wn;
   const int col = nw + PER * (lane % CH), row = lane / CH;
   constexpr int RPI = 64 / CH;                       // rows of a store
+  const int left = col < p.N ? (int)min((int64_t)BM, row_end - r0) : 0;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      float f[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) f[c] = acc[i][j][c];
-      if (!GROUPED && p.bias && p.splits == 1) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const int n = min(nw + 32 * j + 16 * h + c, p.N - 1);
-          f[c] += OUT == 2 ? static_cast<const float*>(p.bias)[n]
-                           : (OUT == 0 ? bf16_to_f32(static_cast<const uint16_t*>(p.bias)[n])
-                                       : f16_to_f32(static_cast<const uint16_t*>(p.bias)[n]));
-        }
-      }
 #pragma unroll
       for (int q = 0; q < SZ; ++q) {                 // SZ chunks of the lane's 16 columns
         v4i w;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          if constexpr (OUT == 2) {
-            w[c] = __float_as_int(f[4 * q + c]);
-          } else {
-            const float x = f[8 * q + 2 * c], y = f[8 * q + 2 * c + 1];
-            w[c] = (int)(OUT == 0 ? f32_to_bf16_rne(x) | (uint32_t)f32_to_bf16_rne(y) << 16
-                                  : f32_to_f16_rne(x) | (uint32_t)f32_to_f16_rne(y) << 16);
-          }
+          if constexpr (OUT == 2) w[c] = __float_as_int(acc[i][j][4 * q + c]);
+          else w[c] = pack16<OUT>(acc[i][j][8 * q + 2 * c], acc[i][j][8 * q + 2 * c + 1]);
         }
         *reinterpret_cast<v4i*>(mine + (l32 * CH + ((2 * j + h) * SZ + q ^ swizzle(l32))) * 16) = w;
       }
     }
-    const int64_t r = r0 + 32 * (MI * wm + i) + row;
-    uint8_t* o = static_cast<uint8_t*>(p.out) + ((out0 + r + (int64_t)split * p.M) * p.N + col) * SZ;
+    const int first = 32 * (MI * wm + i) + row;      // of the tile's rows
+    uint8_t* o = static_cast<uint8_t*>(p.out) + ((out0 + r0 + first + (int64_t)split * p.M) * p.N + col) * SZ;
 #pragma unroll
     for (int k = 0; k < 32 / RPI; ++k) {
       const int rr = row + RPI * k;
       const v4i w = *reinterpret_cast<const v4i*>(mine + (rr * CH + (lane % CH ^ swizzle(rr))) * 16);
-      if (r + RPI * k < row_end && col < p.N) *reinterpret_cast<v4i*>(o) = w;
+      if (first + RPI * k < left) *reinterpret_cast<v4i*>(o) = w;
       o += (int64_t)RPI * p.N * SZ;
     }
   }
