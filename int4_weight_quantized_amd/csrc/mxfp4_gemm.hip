@@ -88,55 +88,45 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
   const int k0 = p.KT * split / p.splits, k1 = p.KT * (split + 1) / p.splits;   // KT at most 2^14, splits 2^9
   const int64_t KH = p.K >> 1;                       // code bytes of a row
 
-  // ---- LDS DMA: a wave's load fills 8 rows (one KiB), lane L at row L / 8, physical 16-byte chunk L % 8. Row r holds
-  // logical chunk c at physical chunk c ^ f(r), so that 8 lanes that read one chunk of 8 rows touch 8 different ones.
-  // Rows and columns past the end get an offset past the buffer, which reads as zero.
+  // ---- LDS DMA: a wave's load fills 8 rows (one KiB), lane L at row L / 8, physical 16-byte chunk L % 8. Row r holds logical
+  // chunk c at physical chunk c ^ f(r), so that the 16 rows that a read touches at a time fill two rows' width of banks.
+  // f repeats every TH / 8 rows. Rows past the end lie past the buffer, which reads as zero; so do gathered rows without a
+  // token, and chunks past K, by an offset of their own. (The scalar part of an address never passes the buffer's size.)
   const int lrow = lane >> 3, lchunk = lane & 7;
   const bool gather = GROUPED && p.row_token;
   const int64_t abase = gather ? 0 : out0 + r0;
-  const int64_t arows = gather ? p.M : min((int64_t)BM, p.M - abase);
+  const int64_t arows = gather ? p.M : (GROUPED ? min(min((int64_t)BM, row_end - r0), p.M - abase) : min((int64_t)BM, p.M - abase));
   const __amdgpu_buffer_rsrc_t arsrc = make_rsrc(p.a + abase * KH, (uint32_t)max(arows * KH, (int64_t)0));
   const __amdgpu_buffer_rsrc_t asr = make_rsrc(p.a_scale + abase * p.KS, (uint32_t)max(arows * p.KS, (int64_t)0));
   const int64_t wrow0 = (int64_t)e * p.N + n0;
   const int wrows = min(BN, p.N - n0);
   const __amdgpu_buffer_rsrc_t wrsrc = make_rsrc(p.w + wrow0 * KH, (uint32_t)(wrows * KH));
   const __amdgpu_buffer_rsrc_t wsr = make_rsrc(p.w_scale + wrow0 * p.KS, (uint32_t)((int64_t)wrows * p.KS));
-  auto token = [&](int r) -> int64_t {               // activation row of tile row r, relative to abase; -1: none
+  auto token = [&](int r) -> int {                   // gathered: activation row of tile row r; -1: none
     if (r0 + r >= row_end) return -1;
-    if (gather) {
-      const int t = p.row_token[out0 + r0 + r];
-      return (unsigned)t < (uint64_t)p.M ? t : -1;
-    }
-    return (!GROUPED || out0 + r0 + r < p.M) ? r : -1;
+    const int t = p.row_token[out0 + r0 + r];
+    return (unsigned)t < (uint64_t)p.M ? t : -1;
   };
-  uint32_t a_off[RA], b_off[RB];
-  uint32_t a_dead = 0, b_dead = 0;                   // bit i: load i's chunk lies past K in the last step
+  const int drow = 8 * wave + lrow;                  // + TH / 8 per load
+  const int ca = lchunk ^ ((drow >> 1) & 7), cb = lchunk ^ (((drow >> 1) & 3) + 4 * ((drow >> 4) & 1));
+  static_assert(TH / 8 % 32 == 0, "f repeats");
+  const uint32_t KHu = (uint32_t)KH;
   const int klast = p.K - (p.KT - 1) * kMK;          // columns of the last step
+  const bool a_dead = 32 * ca >= klast, b_dead = 32 * cb >= klast;   // the lane's chunk lies past K there
+  uint32_t a_off[RA], b_off[RB];
 #pragma unroll
   for (int i = 0; i < RA; ++i) {
-    const int r = (TH / 8) * i + 8 * wave + lrow;
-    const int c = lchunk ^ ((r >> 1) & 7);
-    const int64_t t = token(r);
-    a_off[i] = t >= 0 ? (uint32_t)(t * KH + 16 * c) : kPast;
-    if (32 * c >= klast) a_dead |= 1u << i;
+    const int t = gather ? token((TH / 8) * i + drow) : (TH / 8) * i + drow;
+    a_off[i] = t >= 0 ? (uint32_t)t * KHu + 16 * ca : kPast;
   }
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    const int r = (TH / 8) * i + 8 * wave + lrow;
-    const int c = lchunk ^ (((r >> 1) & 3) + 4 * ((r >> 4) & 1));
-    b_off[i] = n0 + r < p.N ? (uint32_t)(r * KH + 16 * c) : kPast;
-    if (32 * c >= klast) b_dead |= 1u << i;
-  }
+  for (int i = 0; i < RB; ++i) b_off[i] = (uint32_t)((TH / 8) * i + drow) * KHu + 16 * cb;
   uint32_t s_off[RS];
 #pragma unroll
   for (int i = 0; i < RS; ++i) {
     const int r = 64 * (NW * i + wave) + lane;       // activation rows, then weight rows
-    if (64 * (NW * i + wave) < BM) {
-      const int64_t t = token(r);
-      s_off[i] = t >= 0 ? (uint32_t)(t * p.KS) : kPast;
-    } else {
-      s_off[i] = n0 + r - BM < p.N ? (uint32_t)((r - BM) * (int64_t)p.KS) : kPast;
-    }
+    const int t = 64 * (NW * i + wave) >= BM ? r - BM : (gather ? token(r) : r);
+    s_off[i] = t >= 0 ? (uint32_t)t * (uint32_t)p.KS : kPast;
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const uint32_t ldsw = __builtin_amdgcn_readfirstlane(lds0 + 8 * wave * kMB);
@@ -154,16 +144,15 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
       const int grp = NW * i + wave;                 // 64 rows
       if (64 * grp >= BM + BN) return;
       const uint32_t dst = lds0 + 2 * STAGE + (((tk - k0) >> 1) & 1) * SCALES + 1024 * grp;
-      const uint32_t off = tk < k1 ? s_off[i] : kPast;
-      if (64 * grp < BM) dma(asr, dst, off, (uint32_t)tk * 8);
-      else dma(wsr, dst, off, (uint32_t)tk * 8);
+      const uint32_t off = tk < k1 ? s_off[i] : kPast, ks = tk < k1 ? (uint32_t)tk * 8 : 0u;
+      if (64 * grp < BM) dma(asr, dst, off, ks);
+      else dma(wsr, dst, off, ks);
       return;
     }
-    const bool act = q < RA;
-    const int i = act ? q : q - RA;
-    uint32_t off = act ? a_off[i] : b_off[i];
-    if (tk >= k1 || (tk == p.KT - 1 && (((act ? a_dead : b_dead) >> i) & 1))) off = kPast;
-    dma(act ? arsrc : wrsrc, ldsw + stage + ((act ? 0 : BM) + (TH / 8) * i) * kMB, off, (uint32_t)tk * kMB);
+    const uint32_t ks = tk < k1 ? (uint32_t)tk * kMB : 0u;
+    const bool last = tk == p.KT - 1;
+    if (q < RA) dma(arsrc, ldsw + stage + (TH / 8) * q * kMB, tk >= k1 || (last && a_dead) ? kPast : a_off[q], ks);
+    else dma(wrsrc, ldsw + stage + (BM + (TH / 8) * (q - RA)) * kMB, tk >= k1 || (last && b_dead) ? kPast : b_off[q - RA], ks);
   };
 
   // the accumulators start from the bias, of 16 consecutive columns each (without one an empty buffer, which reads as zero)
