@@ -18,13 +18,8 @@
 // MXFP4's scale applied; v_mfma_f32_16x16x32_bf16), or fp16 for fp16 activations of
 // FP8 and int4 weights; FP8's and int4's scales multiply the sums of 128 columns.
 //
-// What a wave reads passes through a ring of its own in LDS, by LDS DMA: no wave
-// waits for another, and D steps are in flight without a register. Loading straight
-// into the matrix unit's layout (lane = row + 16 * column group) would touch 64
-// cache lines per load and cost the address unit 60 clocks where a DMA of 8 rows'
-// full lines costs 16 (measured); it bound such a kernel at 2 to 4 TB/s. Rows
-// lie in LDS with their 16-byte chunks permuted by the row, so that the reads of 8
-// rows touch 8 different chunks.
+// What a wave reads passes through LDS of its own (lds_weights.h): rows lie there with their 16-byte chunks permuted by the
+// row, so that the reads of 8 rows touch 8 different chunks.
 //
 // What lies between the two is held to 16 bits of mantissa as the sum of two bf16
 // numbers (2^-17 relative, below what the output's own rounding leaves visible).
@@ -33,7 +28,7 @@
 // takes x apart in the same way, exactly (11 bits).
 #include <type_traits>
 
-#include "mxfp4.h"
+#include "lds_weights.h"
 #include "route_token.h"
 
 namespace w4 {
@@ -42,7 +37,6 @@ constexpr int kInline = 2;                           // tokens that the first ke
 constexpr int kInlineE = 256;
 constexpr int kInlineRows = kInline * 64;
 constexpr int kUpRows = 8, kDownRows = 4;            // most rows of a tile
-enum { kFp8 = 0, kMx = 1, kInt4 = 2 };
 
 struct MoeTile {
   uint16_t e, row0;
@@ -88,72 +82,6 @@ __device__ __forceinline__ int cvt_fp8(int w, float scale, bool high) {
   else
     return high ? __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true))
                 : __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false));
-}
-
-// Columns of a step: 128 bytes of a weight row (int4: two tiles).
-template <int FMT>
-constexpr int kCols = FMT == kFp8 ? 128 : 256;
-
-// LDS DMA of 16 or 4 bytes per lane to dst + lane * 16 (4). Memory past the buffer
-// reads as zero. m0 holds the LDS address: the compiler keeps nothing in it here, and
-// a clobber of a reserved register is not honoured.
-__device__ __forceinline__ void dma16(const __amdgpu_buffer_rsrc_t rs, uint32_t dst, uint32_t off, uint32_t ks) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :: "s"(dst), "v"(off), "s"(rs), "s"(ks) : "memory");
-}
-__device__ __forceinline__ void dma4(const __amdgpu_buffer_rsrc_t rs, uint32_t dst, uint32_t off, uint32_t ks) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-               :: "s"(dst), "v"(off), "s"(rs), "s"(ks) : "memory");
-}
-
-// 16 rows n .. n + 15 of weight matrix e, [N, K]: 2 KiB of LDS per step, by two DMAs.
-// FP8, MXFP4: row r, chunk c at 128 r + 16 (c ^ (r & 7)); int4: tile q, unit (r, g) at
-// 1024 q + 64 r + 16 (g ^ (r / 4 & 3)).
-template <int FMT>
-struct Rows {
-  __amdgpu_buffer_rsrc_t w;
-  uint32_t off[2];
-  bool dead[2];                                      // the chunk lies past K in the last step
-  int kt;                                            // int4: tiles along K
-  // what depends on the lane alone, and on the matrix
-  __device__ __forceinline__ void lane(int64_t n, int64_t K, int lane) {
-    if constexpr (FMT == kInt4) {
-      kt = (int)(K / kTileK);
-      const int r = lane >> 2, g = (lane & 3) ^ (r >> 2 & 3);
-      off[0] = off[1] = (uint32_t)((n % kTileN + r) * 64 + 16 * g);
-    } else {
-      const int64_t bytes = FMT == kFp8 ? K : K / 2;
-      const int left = (int)(K - (K - 1) / kCols<FMT> * kCols<FMT>);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 8 * i + (lane >> 3), c = (lane & 7) ^ (r & 7);
-        off[i] = (uint32_t)(r * bytes + 16 * c);
-        dead[i] = kCols<FMT> / 8 * c >= left;
-      }
-    }
-  }
-  __device__ __forceinline__ void open(const uint8_t* base, int64_t e, int64_t N, int64_t n, int64_t K) {
-    if constexpr (FMT == kInt4) {
-      const int64_t tk = K / kTileK, tiles = (N + kTileN - 1) / kTileN * tk;
-      w = make_rsrc(base + (e * tiles + n / kTileN * tk) * kTileBytes, (uint32_t)(tk * kTileBytes));
-    } else {
-      const int64_t bytes = FMT == kFp8 ? K : K / 2;
-      w = make_rsrc(base + (e * N + n) * bytes, (uint32_t)(16 * bytes));
-    }
-  }
-  __device__ __forceinline__ void fetch(int k, bool last, uint32_t dst) const {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if constexpr (FMT == kInt4) dma16(w, dst + 1024 * i, 2 * k + i < kt ? off[i] : kPast, (uint32_t)(2 * k + i) * kTileBytes);
-      else dma16(w, dst + 1024 * i, last && dead[i] ? kPast : off[i], (uint32_t)k * 128u);
-    }
-  }
-};
-// A lane's two 16-byte pieces: FP8: columns 16 g .. and 64 + 16 g ..; MXFP4: blocks g and 4 + g; int4: units (row, g).
-template <int FMT>
-__device__ __forceinline__ v4i weight_piece(const uint8_t* at, int q, int l16, int g) {
-  return *reinterpret_cast<const v4i*>(FMT == kInt4 ? at + 1024 * q + 64 * l16 + 16 * (g ^ (l16 >> 2 & 3))
-                                                    : at + 128 * l16 + 16 * ((4 * q + g) ^ (l16 & 7)));
 }
 
 // Rows of 16-bit activations: a DMA takes kCols columns of 4 (FP8) or 2 rows; row r, chunk c at 2 kCols r + 16 (c ^ (r & 7)).
@@ -203,81 +131,6 @@ __device__ __forceinline__ typename Operand<F16>::V decode(const v4i (&w)[2], in
   }
   return __builtin_bit_cast(typename Operand<F16>::V, r);
 }
-
-// The scales of MATS sets of 16 rows (the second `gap` rows after the first). FP8 and MXFP4: of 8 steps at a time, with the
-// first of them (steps one by one would ask for a cache line that is still on its way, which holds up the whole cache: 46 us
-// of one token's gate and up products where 8 at a time take $UP): FP8 8 floats of each set; MXFP4 64 bytes of each row,
-// piece c of row r at 64 r + 16 (c ^ (r / 4 & 3)). int4: of each step: half q, set m: 16 fp16.
-template <int FMT, int MATS>
-struct Scales {
-  static constexpr int kSteps = FMT == kInt4 ? 1 : 8;
-  static constexpr int kDmas = FMT == kMx ? MATS : 1;
-  static constexpr int kLanes = FMT == kMx ? 64 : (FMT == kFp8 ? 8 : 16) * MATS;
-  static constexpr int kBytes = FMT == kMx ? 1024 * MATS : 64 * MATS;
-  __amdgpu_buffer_rsrc_t s;
-  uint32_t off, next;                                // next: from set to set
-  int per, N, halves;
-  __device__ __forceinline__ void lane(int64_t N_, int64_t n, int64_t gap, int64_t K, int per_, int lane) {
-    per = per_;
-    N = (int)N_;
-    if constexpr (FMT == kFp8) {
-      off = (uint32_t)((n + (lane >> 3) * gap) / 128 * ((K + 127) / 128) * 4 + 4 * (lane & 7));
-    } else if constexpr (FMT == kMx) {
-      const int r = lane >> 2;
-      off = (uint32_t)(r * mx_scale_bytes(K) + 16 * ((lane & 3) ^ (r >> 2 & 3)));
-      next = (uint32_t)(gap * mx_scale_bytes(K));
-    } else {
-      halves = (int)(K / 128);
-      off = (uint32_t)((n + (lane >> 3) % MATS * gap) * 2 + 4 * (lane & 7));
-    }
-  }
-  __device__ __forceinline__ void open(const void* base, int64_t e, int64_t N_, int64_t n, int64_t gap, int64_t K, int G) {
-    const uint8_t* b = static_cast<const uint8_t*>(base);
-    if constexpr (FMT == kFp8) {
-      const int64_t size = (K + 127) / 128 * ((N_ + 127) / 128) * 4;
-      s = make_rsrc(b + e * size, (uint32_t)size);
-    } else if constexpr (FMT == kMx) {
-      const int64_t ks = mx_scale_bytes(K);
-      s = make_rsrc(b + (e * N_ + n) * ks, (uint32_t)(((MATS - 1) * gap + 16) * ks));
-    } else {
-      s = make_rsrc(b + e * G * N_ * 2, (uint32_t)(G * N_ * 2));
-    }
-  }
-  // begins: whether a step's scales come with it (a run's first step, and every kSteps)
-  static __device__ __forceinline__ bool begins(int k) { return k % kSteps == 0; }
-  __device__ __forceinline__ void fetch(int k, uint32_t dst, int lane) const {
-    dst = __builtin_amdgcn_readfirstlane(dst);       // (the compiler does not see that it is uniform)
-    if (lane >= kLanes) return;
-    if constexpr (FMT == kFp8) {
-      dma4(s, dst, off, (uint32_t)(k & ~7) * 4);
-    } else if constexpr (FMT == kMx) {
-#pragma unroll
-      for (int m = 0; m < MATS; ++m) dma16(s, dst + 1024 * m, off + m * next, (uint32_t)(k & ~7) * 8);
-    } else {
-      // (the second half of an odd number's last step: the first's)
-      const int a = 2 * k / per * N * 2, b = min(2 * k + 1, halves - 1) / per * N * 2;
-      dma4(s, dst, off + (lane < 8 * MATS ? (uint32_t)a : (uint32_t)b), 0u);
-    }
-  }
-  // what multiplies the sums of rows 4 g .. 4 g + 3 of set m over half q of step k
-  static __device__ __forceinline__ v4f sums(const uint8_t* at, int k, int m, int q, int g) {
-    if constexpr (FMT == kFp8) {
-      const float v = reinterpret_cast<const float*>(at)[8 * m + (k & 7)];
-      return v4f{v, v, v, v};
-    } else {
-      const v2i v = *reinterpret_cast<const v2i*>(at + 32 * (MATS * q + m) + 8 * g);
-      return v4f{f16_to_f32((uint16_t)v[0]), f16_to_f32((uint16_t)((uint32_t)v[0] >> 16)), f16_to_f32((uint16_t)v[1]),
-                 f16_to_f32((uint16_t)((uint32_t)v[1] >> 16))};
-    }
-  }
-  // MXFP4: a lane's scale of half q of step k; left: the columns from the step's first to the end
-  static __device__ __forceinline__ float block(const uint8_t* at, int k, int m, int q, int left, int l16, int g) {
-    const int piece = (k & 7) >> 1 ^ (l16 >> 2 & 3);
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(at + 1024 * m + 64 * l16 + 16 * piece + 8 * (k & 1) + 4 * q);
-    const uint32_t c = 128 * q + 32 * g < left ? w >> (8 * g) & 0xFF : 0u;   // past K: the padding, or the next row's
-    return c == kMxNan ? __uint_as_float(0x7FC00000u) : mx_scale_value(c);
-  }
-};
 
 __device__ __forceinline__ v8bf bf(v4i v) { return __builtin_bit_cast(v8bf, v); }
 
@@ -442,19 +295,18 @@ __global__ __launch_bounds__(kPThreads) void moe_plan_kernel(MoeArgs p) {
 
 // Gate and up: WS waves of a block share the steps of 16 gate rows and the 16 up rows beside them. NX: DMAs of a step's
 // activations.
-template <int FMT, bool XF16, int NX, int WS, int D>
+template <int FMT, bool XF16, int NX, int WS>
 __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
   constexpr bool OPF16 = XF16 && FMT != kMx;         // the operands' type
   constexpr bool PARTS = XF16 && FMT == kMx;         // x as two numbers
   constexpr int COLS = kCols<FMT>, HALVES = FMT == kFp8 ? 1 : 2;
   using Op = typename Operand<OPF16>::V;
   using S = Scales<FMT, 2>;
-  // a step in LDS: gate, up, activations; and the scales in places of their own. kDmas: the fewest of a step
-  constexpr int kX = 4096, kSlot = kX + 1024 * NX, kDmas = 4 + NX + (S::kSteps == 1 ? S::kDmas : 0);
+  constexpr int kX = 4096, kSlot = kX + 1024 * NX;   // a step in LDS: gate, up, activations
   __shared__ __attribute__((aligned(16))) union {
     InlinePlan plan;
     struct {
-      uint8_t ring[WS][D][kSlot], scales[WS][D][S::kBytes];
+      uint8_t step[WS][kSlot], scales[WS][S::kBytes];
     } r;
     v4f red[WS][2][64];
   } s;
@@ -469,7 +321,7 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
     if (ti >= s.plan.tiles) return;
     tile = s.plan.tile[ti];
     if (row < __popc(tile.tokens)) weight = s.plan.w[tile.row0 + row];
-    __syncthreads();                                 // the plan's place becomes the ring
+    __syncthreads();                                 // the plan's place takes the steps
   } else {
     if (ti >= p.counts[0]) return;
     tile = p.up[ti];
@@ -494,65 +346,50 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
     xo[j] = token >= 0 ? (uint32_t)(((int64_t)token * p.H + col) * 2) : kPast;
     xdead[j] = col >= p.H - (KT - 1) * COLS;
   }
-  const uint32_t ring0 =
-      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&s.r.ring[wave][0][0]);
-  const uint32_t scales0 =
-      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&s.r.scales[wave][0][0]);
+  const uint8_t *step = &s.r.step[wave][0], *scales = &s.r.scales[wave][0];
+  const uint32_t to = lds_address(step), to_scales = lds_address(scales);
   const int k0 = KT * wave / WS, k1 = KT * (wave + 1) / WS;
-  int fs = -1, cs = -1;                              // the scales' places that were fetched and are used last
-  auto fetch = [&](int k, int d) {                   // past the run's end: the last step again, not used
-    const bool begins = k == k0 || (k < k1 && S::begins(k));
-    k = min(k, k1 - 1);
-    const uint32_t at = ring0 + d * kSlot;
+  auto fetch = [&](int k) {
     const bool last = k == KT - 1;
-    wg.fetch(k, last, at);
-    wu.fetch(k, last, at + 2048);
+    wg.fetch(k, last, to);
+    wu.fetch(k, last, to + 2048);
 #pragma unroll
-    for (int j = 0; j < NX; ++j) dma16(xr, at + kX + 1024 * j, last && xdead[j] ? kPast : xo[j], (uint32_t)k * (2 * COLS));
-    if (begins || S::kSteps == 1) {
-      fs = fs + 1 == D ? 0 : fs + 1;
-      sc.fetch(k, scales0 + fs * S::kBytes, lane);
-    }
+    for (int j = 0; j < NX; ++j) dma16(xr, to + kX + 1024 * j, last && xdead[j] ? kPast : xo[j], (uint32_t)k * (2 * COLS));
+    if (k == k0 || S::begins(k)) sc.fetch(k, to_scales, lane);
   };
   const uint32_t taken = l16 >= 8 ? 0xFFFF0000u : 0u;
   v4f ag = v4f{0.f, 0.f, 0.f, 0.f}, au = ag;
   if (k0 < k1) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) fetch(k0 + d, d);
-    int d = 0;
+    fetch(k0);
     for (int k = k0; k < k1; ++k) {
-      const uint8_t* at = &s.r.ring[wave][d][0];
-      if (k == k0 || S::begins(k)) cs = cs + 1 == D ? 0 : cs + 1;
-      const uint8_t* as = &s.r.scales[wave][cs][0];
-      asm volatile("s_waitcnt vmcnt(%0)" :: "n"((D - 1) * kDmas) : "memory");
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       v4i qg[2], qu[2], X[HALVES][4];
       float lg[HALVES], lu[HALVES];
       v4f mg[HALVES], mu[HALVES];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        qg[q] = weight_piece<FMT>(at, q, l16, g);
-        qu[q] = weight_piece<FMT>(at + 2048, q, l16, g);
+        qg[q] = weight_piece<FMT>(step, q, l16, g);
+        qu[q] = weight_piece<FMT>(step + 2048, q, l16, g);
       }
 #pragma unroll
       for (int q = 0; q < HALVES; ++q) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          X[q][c] = act_chunk<FMT>(at + kX, row & (kRowsPerDma<FMT> * NX - 1),
+          X[q][c] = act_chunk<FMT>(step + kX, row & (kRowsPerDma<FMT> * NX - 1),
                                    FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
         if constexpr (FMT == kMx) {
-          lg[q] = S::block(as, k, 0, q, p.H - k * COLS, l16, g);
-          lu[q] = S::block(as, k, 1, q, p.H - k * COLS, l16, g);
+          lg[q] = S::block(scales, k, 0, q, p.H - k * COLS, l16, g);
+          lu[q] = S::block(scales, k, 1, q, p.H - k * COLS, l16, g);
         } else {
-          mg[q] = S::sums(as, k, 0, q, g);
-          mu[q] = S::sums(as, k, 1, q, g);
+          mg[q] = S::sums(scales, k, 0, q, g);
+          mu[q] = S::sums(scales, k, 1, q, g);
         }
       }
-      // the step is in registers: its place takes the one D on
+      // the step is in registers: its place takes the next
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      fetch(k + D, d);
+      if (k + 1 < k1) fetch(k + 1);
       __builtin_amdgcn_sched_barrier(0);
-      d = d + 1 == D ? 0 : d + 1;
 #pragma unroll
       for (int q = 0; q < HALVES; ++q) {
         v4f dg = FMT == kMx ? ag : v4f{0.f, 0.f, 0.f, 0.f}, du = FMT == kMx ? au : dg;
@@ -582,9 +419,8 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
         }
       }
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing may land in what the ring becomes
   }
-  __syncthreads();
+  __syncthreads();                                   // nothing is on its way into what takes the sums
   s.red[wave][0][lane] = ag;
   s.red[wave][1][lane] = au;
   __syncthreads();
@@ -619,13 +455,13 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
 // Down: a block owns 16 output columns of all tokens; its waves share the (tile, step) pairs, each a run of them. At a
 // tile's end a wave adds its sums to its own place in LDS by token: no token takes anything of an expert that it did not
 // choose, and the order is fixed. NM: DMAs of a step's middle (row r's first numbers as row 2 r, its second as 2 r + 1).
-template <int FMT, bool F16OUT, int NM, int WS, int D>
+template <int FMT, bool F16OUT, int NM, int WS>
 __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
   constexpr int COLS = kCols<FMT>, HALVES = FMT == kFp8 ? 1 : 2;
   using S = Scales<FMT, 1>;
-  constexpr int kX = 2048, kSlot = kX + 1024 * NM, kDmas = 2 + NM + (S::kSteps == 1 ? S::kDmas : 0);
+  constexpr int kX = 2048, kSlot = kX + 1024 * NM;
   constexpr int kMost = kRowsPerDma<FMT> * NM / 2;   // rows that fit
-  __shared__ __attribute__((aligned(16))) uint8_t ring[WS][D][kSlot], scales[WS][D][S::kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t room[WS][kSlot], room_scales[WS][S::kBytes];
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   v4f* sum = reinterpret_cast<v4f*>(smem);           // [WS][T][4]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -640,10 +476,8 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
   __syncthreads();
   v4f* mine = sum + wave * p.T * 4;
   const int i0 = (int)((int64_t)steps * wave / WS), i1 = (int)((int64_t)steps * (wave + 1) / WS);
-  const uint32_t ring0 =
-      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&ring[wave][0][0]);
-  const uint32_t scales0 =
-      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&scales[wave][0][0]);
+  const uint8_t *step = &room[wave][0], *scales = &room_scales[wave][0];
+  const uint32_t to = lds_address(step), to_scales = lds_address(scales);
   uint32_t mo[NM];
   bool mdead[NM];
 #pragma unroll
@@ -654,7 +488,6 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
   }
   // the tile and step that are fetched next, and those that are computed
   int ft = i0 / KT, fk = i0 - ft * KT, ct = ft, ck = fk;
-  int fs = -1, cs = -1;                              // the scales' places that were fetched and are used last
   Rows<FMT> w;
   S sc;
   int rows = 0;
@@ -667,18 +500,14 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
     w.open(p.w2, e, p.H, n0, p.I);
     sc.open(p.s2, e, p.H, n0, 0, p.I, p.G2);
   };
-  auto fetch = [&](int d, bool first) {
-    const uint32_t at = ring0 + d * kSlot;
+  auto fetch = [&](bool first) {
     const bool last = fk == KT - 1;
-    w.fetch(fk, last, at);
+    w.fetch(fk, last, to);
 #pragma unroll
     for (int j = 0; j < NM; ++j)
-      dma16(mr, at + kX + 1024 * j, (act_row<FMT>(j, lane) >> 1) >= rows || (last && mdead[j]) ? kPast : mo[j] + row0,
+      dma16(mr, to + kX + 1024 * j, (act_row<FMT>(j, lane) >> 1) >= rows || (last && mdead[j]) ? kPast : mo[j] + row0,
             (uint32_t)fk * (2 * COLS));
-    if (first || S::begins(fk)) {
-      fs = fs + 1 == D ? 0 : fs + 1;
-      sc.fetch(fk, scales0 + fs * S::kBytes, lane);
-    }
+    if (first || S::begins(fk)) sc.fetch(fk, to_scales, lane);
     if (++fk == KT) {
       fk = 0;
       ++ft;
@@ -690,33 +519,27 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
     w.lane(n0, p.I, lane);
     sc.lane(p.H, n0, 0, p.I, p.kg2, lane);
     open_tile();
-#pragma unroll
-    for (int d = 0; d < D; ++d) fetch(d, d == 0);
+    fetch(true);
     const int mrow = (2 * (l16 & 7) + (l16 >> 3)) & (2 * kMost - 1);
-    int d = 0;
     for (int i = i0; i < i1; ++i) {
-      const uint8_t* at = &ring[wave][d][0];
-      if (i == i0 || S::begins(ck)) cs = cs + 1 == D ? 0 : cs + 1;
-      const uint8_t* as = &scales[wave][cs][0];
-      asm volatile("s_waitcnt vmcnt(%0)" :: "n"((D - 1) * kDmas) : "memory");
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       v4i qw[2], M[HALVES][4];
       float ls[HALVES];
       v4f ms[HALVES];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) qw[q] = weight_piece<FMT>(at, q, l16, g);
+      for (int q = 0; q < 2; ++q) qw[q] = weight_piece<FMT>(step, q, l16, g);
 #pragma unroll
       for (int q = 0; q < HALVES; ++q) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          M[q][c] = act_chunk<FMT>(at + kX, mrow, FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
-        if constexpr (FMT == kMx) ls[q] = S::block(as, ck, 0, q, p.I - ck * COLS, l16, g);
-        else ms[q] = S::sums(as, ck, 0, q, g);
+          M[q][c] = act_chunk<FMT>(step + kX, mrow, FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
+        if constexpr (FMT == kMx) ls[q] = S::block(scales, ck, 0, q, p.I - ck * COLS, l16, g);
+        else ms[q] = S::sums(scales, ck, 0, q, g);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      fetch(d, false);
+      if (i + 1 < i1) fetch(false);
       __builtin_amdgcn_sched_barrier(0);
-      d = d + 1 == D ? 0 : d + 1;
 #pragma unroll
       for (int q = 0; q < HALVES; ++q) {
         v4f v = FMT == kMx ? acc : v4f{0.f, 0.f, 0.f, 0.f};
@@ -745,7 +568,6 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
         ++ct;
       }
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // what was fetched past the end has landed
   }
   __syncthreads();
   for (int i = tid; i < p.T * 4; i += 64 * WS) {
@@ -796,11 +618,11 @@ size_t moe_workspace(int64_t T, int64_t E, int64_t topk, int64_t I) {
 
 template <int FMT, bool F16, int NX, int NM>
 static hipError_t moe_stream(const MoeArgs& p, int64_t tiles, hipStream_t stream) {
-  constexpr int WU = 4, DU = 2, WD = 8, DD = 2;
-  hipLaunchKernelGGL((moe_up_kernel<FMT, F16, NX, WU, DU>), dim3((unsigned)(tiles * p.NT)), dim3(64 * WU), 0, stream, p);
+  constexpr int WU = 4, WD = 8;
+  hipLaunchKernelGGL((moe_up_kernel<FMT, F16, NX, WU>), dim3((unsigned)(tiles * p.NT)), dim3(64 * WU), 0, stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down_kernel<FMT, F16, NM, WD, DD>), dim3((unsigned)(p.H / 16)), dim3(64 * WD),
+  hipLaunchKernelGGL((moe_down_kernel<FMT, F16, NM, WD>), dim3((unsigned)(p.H / 16)), dim3(64 * WD),
                      (size_t)WD * p.T * 64 + sizeof(MoeTile) * (size_t)most_tiles(p.E, (int64_t)p.T * p.topk, kDownRows), stream, p);
   return hipGetLastError();
 }

@@ -375,7 +375,7 @@ int64_t mx_gemm_threads(int64_t M, int64_t N, int64_t K) {
   return product > reduce ? product : reduce;
 }
 
-bool mx_streams(int64_t M) { return M <= 16; }
+bool mx_inline(int64_t M, int64_t K) { return M <= 16 && M * K <= 65536; }
 
 template <int BM, int BN, typename F>
 static hipError_t tile_go(MxArgs p, F kernel, hipStream_t stream) {
