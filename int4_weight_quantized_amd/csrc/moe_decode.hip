@@ -36,7 +36,7 @@ namespace w4 {
 constexpr int kInline = 2;                           // tokens that the first kernel routes itself
 constexpr int kInlineE = 256;
 constexpr int kInlineRows = kInline * 64;
-constexpr int kUpRows = 8, kDownRows = 4;            // most rows of a tile
+constexpr int kUpRows = 8, kFewRows = 4;             // most rows of a tile (down: kUpRows where experts hold many)
 
 struct MoeTile {
   uint16_t e, row0;
@@ -54,6 +54,7 @@ struct MoeArgs {
   int kg13, kg2;                                     // and steps per group
   int NT;                                            // column tiles of the launch
   int inl;                                           // the first kernel routes
+  int down_rows;                                     // most rows of a tile of the second
   // workspace
   int32_t* counts;                                   // tiles of the first kernel, of the second
   MoeTile *up, *down;
@@ -167,10 +168,12 @@ __device__ __forceinline__ MoeTile tile_of(int e, int row0, uint32_t tokens, int
 // (Two tokens of an expert fit one tile.)
 struct InlinePlan {
   float w[kInlineRows];
-  int raw_e[kInlineRows];
-  float raw_w[kInlineRows];
   MoeTile tile[kInlineRows];
   int tiles;
+};
+struct InlineScratch {
+  int raw_e[kInlineRows];
+  float raw_w[kInlineRows];
   double keys[kInline][kInlineE];
 };
 
@@ -185,32 +188,32 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, int lane, d
   }
 }
 
-__device__ __forceinline__ void plan_inline(const MoeArgs& p, InlinePlan& s) {
+__device__ __forceinline__ void plan_inline(const MoeArgs& p, InlinePlan& s, InlineScratch& x) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const RouteArgs& a = p.route;
   if (wave < p.T) {
     int id;
     double w;
-    route_one(a, wave, lane, s.keys[wave], id, w);
+    route_one(a, wave, lane, x.keys[wave], id, w);
     if (lane < p.topk) {
-      s.raw_e[wave * p.topk + lane] = id;
-      s.raw_w[wave * p.topk + lane] = (float)(w * a.scale);
+      x.raw_e[wave * p.topk + lane] = id;
+      x.raw_w[wave * p.topk + lane] = (float)(w * a.scale);
     }
   }
   __syncthreads();
   // One wave: lane i holds both tokens' choice i. A pair's row counts the pairs before it, its tile the experts.
   if (wave == 0) {
     const bool two = p.T == 2;
-    const int e0 = lane < p.topk ? s.raw_e[lane] : -1, e1 = two && lane < p.topk ? s.raw_e[p.topk + lane] : -1;
+    const int e0 = lane < p.topk ? x.raw_e[lane] : -1, e1 = two && lane < p.topk ? x.raw_e[p.topk + lane] : -1;
     bool dup0 = false, dup1 = false;                 // the other token chose it too
     for (int q = 0; q < p.topk; ++q) {
-      dup1 = dup1 || (e1 >= 0 && s.raw_e[q] == e1);
-      dup0 = dup0 || (two && e0 >= 0 && s.raw_e[p.topk + q] == e0);
+      dup1 = dup1 || (e1 >= 0 && x.raw_e[q] == e1);
+      dup0 = dup0 || (two && e0 >= 0 && x.raw_e[p.topk + q] == e0);
     }
     const unsigned long long dups = __ballot(dup1);
     int r0 = 0, r1 = dup1 ? 1 : 0, s0 = 0, s1 = 0;
     for (int q = 0; q < p.topk; ++q) {
-      const int a = s.raw_e[q], b = two ? s.raw_e[p.topk + q] : -1;
+      const int a = x.raw_e[q], b = two ? x.raw_e[p.topk + q] : -1;
       const int a0 = a >= 0 && a < e0, a1 = a >= 0 && a < e1, b0 = b >= 0 && b < e0, b1 = b >= 0 && b < e1;
       const int once = (dups >> q & 1) ? 0 : 1;
       r0 += a0 + b0;
@@ -219,11 +222,11 @@ __device__ __forceinline__ void plan_inline(const MoeArgs& p, InlinePlan& s) {
       s1 += a1 + b1 * once;
     }
     if (e0 >= 0) {
-      s.w[r0] = s.raw_w[lane];
+      s.w[r0] = x.raw_w[lane];
       s.tile[s0] = MoeTile{(uint16_t)e0, (uint16_t)r0, dup0 ? 3u : 1u};
     }
     if (e1 >= 0) {
-      s.w[r1] = s.raw_w[p.topk + lane];
+      s.w[r1] = x.raw_w[p.topk + lane];
       if (!dup1) s.tile[s1] = MoeTile{(uint16_t)e1, (uint16_t)r1, 2u};
     }
     const int n = __popcll(__ballot(e0 >= 0)) + __popcll(__ballot(e1 >= 0 && !dup1));
@@ -265,7 +268,7 @@ __global__ __launch_bounds__(kPThreads) void moe_plan_kernel(MoeArgs p) {
   __syncthreads();
   // thread e: the expert's rows and tiles, and the sums of those before it
   const uint32_t m = mask[tid];
-  const int n = __popc(m), up = (n + kUpRows - 1) / kUpRows, dn = (n + kDownRows - 1) / kDownRows;
+  const int n = __popc(m), up = (n + kUpRows - 1) / kUpRows, dn = (n + p.down_rows - 1) / p.down_rows;
   int s[3] = {n, up, dn};
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
@@ -282,7 +285,7 @@ __global__ __launch_bounds__(kPThreads) void moe_plan_kernel(MoeArgs p) {
     for (int v = 0; v < wave; ++v) s[k] += part[k][v];
   row0[tid] = s[0] - n;
   for (int i = 0; i < up; ++i) p.up[s[1] - up + i] = tile_of(tid, s[0] - n, m, i, kUpRows);
-  for (int i = 0; i < dn; ++i) p.down[s[2] - dn + i] = tile_of(tid, s[0] - n, m, i, kDownRows);
+  for (int i = 0; i < dn; ++i) p.down[s[2] - dn + i] = tile_of(tid, s[0] - n, m, i, p.down_rows);
   if (tid == kPThreads - 1) {
     p.counts[0] = s[1];
     p.counts[1] = s[2];
@@ -299,157 +302,158 @@ template <int FMT, bool XF16, int NX, int WS>
 __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
   constexpr bool OPF16 = XF16 && FMT != kMx;         // the operands' type
   constexpr bool PARTS = XF16 && FMT == kMx;         // x as two numbers
+  constexpr bool FEW = kRowsPerDma<FMT> * NX < kUpRows;   // up to kInline tokens
   constexpr int COLS = kCols<FMT>, HALVES = FMT == kFp8 ? 1 : 2;
   using Op = typename Operand<OPF16>::V;
   using S = Scales<FMT, 2>;
   constexpr int kX = 4096, kSlot = kX + 1024 * NX;   // a step in LDS: gate, up, activations
   __shared__ __attribute__((aligned(16))) union {
-    InlinePlan plan;
+    InlineScratch route;
     struct {
       uint8_t step[WS][kSlot], scales[WS][S::kBytes];
     } r;
     v4f red[WS][2][64];
   } s;
+  __shared__ InlinePlan plan;                        // (takes no place where FEW is false)
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, l16 = lane & 15;
-  const int ti = (int)blockIdx.x / p.NT, tn = (int)blockIdx.x % p.NT;
-  MoeTile tile;
-  const int row = l16 & 7;                           // this lane's row of the tile (columns 8 and on: again, or second parts)
-  float weight = 0.f;
-  if (p.inl) {
-    plan_inline(p, s.plan);
-    if (ti >= s.plan.tiles) return;
-    tile = s.plan.tile[ti];
-    if (row < __popc(tile.tokens)) weight = s.plan.w[tile.row0 + row];
-    __syncthreads();                                 // the plan's place takes the steps
-  } else {
-    if (ti >= p.counts[0]) return;
-    tile = p.up[ti];
-    if (row < __popc(tile.tokens)) weight = p.weights[tile.row0 + row];
-  }
-  const int e = __builtin_amdgcn_readfirstlane(tile.e);
-  const int KT = (p.H + COLS - 1) / COLS, n0 = 16 * tn;
-  Rows<FMT> wg, wu;
-  wg.lane(n0, p.H, lane);
-  wu.lane(p.I + n0, p.H, lane);
-  wg.open(p.w13, e, 2 * (int64_t)p.I, n0, p.H);
-  wu.open(p.w13, e, 2 * (int64_t)p.I, p.I + n0, p.H);
-  S sc;
-  sc.lane(2 * (int64_t)p.I, n0, p.I, p.H, p.kg13, lane);
-  sc.open(p.s13, e, 2 * (int64_t)p.I, n0, p.I, p.H, p.G13);
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x, (uint32_t)(p.T * (int64_t)p.H * 2));
-  uint32_t xo[NX];
-  bool xdead[NX];                                    // past H in the last step
+  const int row = l16 & 7;                           // this lane's row of a tile (columns 8 and on: again, or second parts)
+  const bool inl = FEW && p.inl;
+  if (inl) plan_inline(p, plan, s.route);
+  const int items = __builtin_amdgcn_readfirstlane(inl ? plan.tiles : p.counts[0]) * p.NT;
+  for (int item = (int)blockIdx.x; item < items; item += (int)gridDim.x) {
+    const int ti = item / p.NT, tn = item - ti * p.NT;
+    const MoeTile tile = inl ? plan.tile[ti] : p.up[ti];
+    const int rows = __popc(__builtin_amdgcn_readfirstlane(tile.tokens));
+    const bool mine = row < rows;
+    const float weight = mine ? (inl ? plan.w[tile.row0 + row] : p.weights[tile.row0 + row]) : 0.f;
+    __syncthreads();                                   // the last item's sums were read (or the plan's scratch)
+    const int e = __builtin_amdgcn_readfirstlane(tile.e);
+    const int KT = (p.H + COLS - 1) / COLS, n0 = 16 * tn;
+    Rows<FMT> wg, wu;
+    wg.lane(n0, p.H, lane);
+    wu.lane(p.I + n0, p.H, lane);
+    wg.open(p.w13, e, 2 * (int64_t)p.I, n0, p.H);
+    wu.open(p.w13, e, 2 * (int64_t)p.I, p.I + n0, p.H);
+    S sc;
+    sc.lane(2 * (int64_t)p.I, n0, p.I, p.H, p.kg13, lane);
+    sc.open(p.s13, e, 2 * (int64_t)p.I, n0, p.I, p.H, p.G13);
+    const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x, (uint32_t)(p.T * (int64_t)p.H * 2));
+    uint32_t xo[NX];
+    bool xdead[NX];                                    // past H in the last step
 #pragma unroll
-  for (int j = 0; j < NX; ++j) {
-    const int r = act_row<FMT>(j, lane), col = act_column<FMT>(r, lane), token = tile_token(tile.tokens, r);
-    xo[j] = token >= 0 ? (uint32_t)(((int64_t)token * p.H + col) * 2) : kPast;
-    xdead[j] = col >= p.H - (KT - 1) * COLS;
-  }
-  const uint8_t *step = &s.r.step[wave][0], *scales = &s.r.scales[wave][0];
-  const uint32_t to = lds_address(step), to_scales = lds_address(scales);
-  const int k0 = KT * wave / WS, k1 = KT * (wave + 1) / WS;
-  auto fetch = [&](int k) {
-    const bool last = k == KT - 1;
-    wg.fetch(k, last, to);
-    wu.fetch(k, last, to + 2048);
+    for (int j = 0; j < NX; ++j) {
+      const int r = act_row<FMT>(j, lane), col = act_column<FMT>(r, lane), token = tile_token(tile.tokens, r);
+      xo[j] = token >= 0 ? (uint32_t)(((int64_t)token * p.H + col) * 2) : kPast;
+      xdead[j] = col >= p.H - (KT - 1) * COLS;
+    }
+    const uint8_t *step = &s.r.step[wave][0], *scales = &s.r.scales[wave][0];
+    const uint32_t to = lds_address(step), to_scales = lds_address(scales);
+    const int k0 = KT * wave / WS, k1 = KT * (wave + 1) / WS;
+    auto fetch = [&](int k) {
+      const bool last = k == KT - 1;
+      wg.fetch(k, last, to);
+      wu.fetch(k, last, to + 2048);
 #pragma unroll
-    for (int j = 0; j < NX; ++j) dma16(xr, to + kX + 1024 * j, last && xdead[j] ? kPast : xo[j], (uint32_t)k * (2 * COLS));
-    if (k == k0 || S::begins(k)) sc.fetch(k, to_scales, lane);
-  };
-  const uint32_t taken = l16 >= 8 ? 0xFFFF0000u : 0u;
-  v4f ag = v4f{0.f, 0.f, 0.f, 0.f}, au = ag;
-  if (k0 < k1) {
-    fetch(k0);
-    for (int k = k0; k < k1; ++k) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      v4i qg[2], qu[2], X[HALVES][4];
-      float lg[HALVES], lu[HALVES];
-      v4f mg[HALVES], mu[HALVES];
+      for (int j = 0; j < NX; ++j)                   // (rows that the tile does not have: whatever lies there, not stored)
+        if (kRowsPerDma<FMT> * j < rows)
+          dma16(xr, to + kX + 1024 * j, last && xdead[j] ? kPast : xo[j], (uint32_t)k * (2 * COLS));
+      if (k == k0 || S::begins(k)) sc.fetch(k, to_scales, lane);
+    };
+    const uint32_t taken = l16 >= 8 ? 0xFFFF0000u : 0u;
+    v4f ag = v4f{0.f, 0.f, 0.f, 0.f}, au = ag;
+    if (k0 < k1) {
+      fetch(k0);
+      for (int k = k0; k < k1; ++k) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        v4i qg[2], qu[2], X[HALVES][4];
+        float lg[HALVES], lu[HALVES];
+        v4f mg[HALVES], mu[HALVES];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        qg[q] = weight_piece<FMT>(step, q, l16, g);
-        qu[q] = weight_piece<FMT>(step + 2048, q, l16, g);
-      }
-#pragma unroll
-      for (int q = 0; q < HALVES; ++q) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          X[q][c] = act_chunk<FMT>(step + kX, row & (kRowsPerDma<FMT> * NX - 1),
-                                   FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
-        if constexpr (FMT == kMx) {
-          lg[q] = S::block(scales, k, 0, q, p.H - k * COLS, l16, g);
-          lu[q] = S::block(scales, k, 1, q, p.H - k * COLS, l16, g);
-        } else {
-          mg[q] = S::sums(scales, k, 0, q, g);
-          mu[q] = S::sums(scales, k, 1, q, g);
+        for (int q = 0; q < 2; ++q) {
+          qg[q] = weight_piece<FMT>(step, q, l16, g);
+          qu[q] = weight_piece<FMT>(step + 2048, q, l16, g);
         }
-      }
-      // the step is in registers: its place takes the next
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
-      if (k + 1 < k1) fetch(k + 1);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int q = 0; q < HALVES; ++q) {
-        v4f dg = FMT == kMx ? ag : v4f{0.f, 0.f, 0.f, 0.f}, du = FMT == kMx ? au : dg;
-        if constexpr (FMT == kInt4) {                // -8 sum x
-          const int m8 = OPF16 ? (int)0xC800C800 : (int)0xC100C100;
+        for (int q = 0; q < HALVES; ++q) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            dg = mfma16<OPF16>(__builtin_bit_cast(Op, v4i{m8, m8, m8, m8}), __builtin_bit_cast(Op, act_piece<FMT>(X[q], c)), dg);
-          du = dg;
+            X[q][c] = act_chunk<FMT>(step + kX, row & (kRowsPerDma<FMT> * NX - 1),
+                                     FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
+          if constexpr (FMT == kMx) {
+            lg[q] = S::block(scales, k, 0, q, p.H - k * COLS, l16, g);
+            lu[q] = S::block(scales, k, 1, q, p.H - k * COLS, l16, g);
+          } else {
+            mg[q] = S::sums(scales, k, 0, q, g);
+            mu[q] = S::sums(scales, k, 1, q, g);
+          }
         }
+        // the step is in registers: its place takes the next
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if (k + 1 < k1) fetch(k + 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          v4i xp = act_piece<FMT>(X[q], c);
-          if constexpr (PARTS) xp = part_of_f16(xp, taken);
-          dg = mfma16<OPF16>(decode<FMT, OPF16>(qg, q, c, lg[q]), __builtin_bit_cast(Op, xp), dg);
-          du = mfma16<OPF16>(decode<FMT, OPF16>(qu, q, c, lu[q]), __builtin_bit_cast(Op, xp), du);
-        }
-        if constexpr (FMT == kMx) {
-          ag = dg;
-          au = du;
-        } else {
+        for (int q = 0; q < HALVES; ++q) {
+          v4f dg = FMT == kMx ? ag : v4f{0.f, 0.f, 0.f, 0.f}, du = FMT == kMx ? au : dg;
+          if constexpr (FMT == kInt4) {                // -8 sum x
+            const int m8 = OPF16 ? (int)0xC800C800 : (int)0xC100C100;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            ag[i] = fmaf(dg[i], mg[q][i], ag[i]);
-            au[i] = fmaf(du[i], mu[q][i], au[i]);
+            for (int c = 0; c < 4; ++c)
+              dg = mfma16<OPF16>(__builtin_bit_cast(Op, v4i{m8, m8, m8, m8}), __builtin_bit_cast(Op, act_piece<FMT>(X[q], c)), dg);
+            du = dg;
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            v4i xp = act_piece<FMT>(X[q], c);
+            if constexpr (PARTS) xp = part_of_f16(xp, taken);
+            dg = mfma16<OPF16>(decode<FMT, OPF16>(qg, q, c, lg[q]), __builtin_bit_cast(Op, xp), dg);
+            du = mfma16<OPF16>(decode<FMT, OPF16>(qu, q, c, lu[q]), __builtin_bit_cast(Op, xp), du);
+          }
+          if constexpr (FMT == kMx) {
+            ag = dg;
+            au = du;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              ag[i] = fmaf(dg[i], mg[q][i], ag[i]);
+              au[i] = fmaf(du[i], mu[q][i], au[i]);
+            }
           }
         }
       }
     }
-  }
-  __syncthreads();                                   // nothing is on its way into what takes the sums
-  s.red[wave][0][lane] = ag;
-  s.red[wave][1][lane] = au;
-  __syncthreads();
-  if (wave != 0) return;
-  v4f vg = s.red[0][0][lane], vu = s.red[0][1][lane];
+    __syncthreads();                                   // nothing is on its way into what takes the sums
+    s.red[wave][0][lane] = ag;
+    s.red[wave][1][lane] = au;
+    __syncthreads();
+    if (wave != 0) continue;
+    v4f vg = s.red[0][0][lane], vu = s.red[0][1][lane];
 #pragma unroll
-  for (int w = 1; w < WS; ++w) {
-    vg += s.red[w][0][lane];
-    vu += s.red[w][1][lane];
-  }
-  if constexpr (PARTS) {
+    for (int w = 1; w < WS; ++w) {
+      vg += s.red[w][0][lane];
+      vu += s.red[w][1][lane];
+    }
+    if constexpr (PARTS) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        vg[q] += __shfl_xor(vg[q], 8, kWave);
+        vu[q] += __shfl_xor(vu[q], 8, kWave);
+      }
+    }
+    if (l16 >= 8 || !mine) continue;
+    uint32_t hi[4], lo[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      vg[q] += __shfl_xor(vg[q], 8, kWave);
-      vu[q] += __shfl_xor(vu[q], 8, kWave);
+      const float m = vg[q] / (1.0f + expf(-vg[q])) * vu[q] * weight;
+      hi[q] = f32_to_bf16_rne(m);
+      const float rest = m - __uint_as_float(hi[q] << 16);
+      lo[q] = (hi[q] & 0x7F80u) != 0x7F80u ? f32_to_bf16_rne(rest) : 0u;   // (an infinity has no remainder)
     }
+    uint16_t* o = p.mid + (int64_t)(tile.row0 + row) * p.I + n0 + 4 * g;
+    *reinterpret_cast<v2i*>(o) = v2i{(int)(hi[0] | hi[1] << 16), (int)(hi[2] | hi[3] << 16)};
+    *reinterpret_cast<v2i*>(o + (int64_t)p.T * p.topk * p.I) = v2i{(int)(lo[0] | lo[1] << 16), (int)(lo[2] | lo[3] << 16)};
   }
-  if (l16 >= 8 || row >= __popc(tile.tokens)) return;
-  uint32_t hi[4], lo[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const float m = vg[q] / (1.0f + expf(-vg[q])) * vu[q] * weight;
-    hi[q] = f32_to_bf16_rne(m);
-    const float rest = m - __uint_as_float(hi[q] << 16);
-    lo[q] = (hi[q] & 0x7F80u) != 0x7F80u ? f32_to_bf16_rne(rest) : 0u;   // (an infinity has no remainder)
-  }
-  uint16_t* o = p.mid + (int64_t)(tile.row0 + row) * p.I + n0 + 4 * g;
-  *reinterpret_cast<v2i*>(o) = v2i{(int)(hi[0] | hi[1] << 16), (int)(hi[2] | hi[3] << 16)};
-  *reinterpret_cast<v2i*>(o + (int64_t)p.T * p.topk * p.I) = v2i{(int)(lo[0] | lo[1] << 16), (int)(lo[2] | lo[3] << 16)};
 }
 
 // Down: a block owns 16 output columns of all tokens; its waves share the (tile, step) pairs, each a run of them. At a
@@ -504,9 +508,10 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
     const bool last = fk == KT - 1;
     w.fetch(fk, last, to);
 #pragma unroll
-    for (int j = 0; j < NM; ++j)
-      dma16(mr, to + kX + 1024 * j, (act_row<FMT>(j, lane) >> 1) >= rows || (last && mdead[j]) ? kPast : mo[j] + row0,
-            (uint32_t)fk * (2 * COLS));
+    for (int j = 0; j < NM; ++j)                     // (rows that the tile does not have: whatever lies there, not stored)
+      if (kRowsPerDma<FMT> * j < 2 * rows)
+        dma16(mr, to + kX + 1024 * j, (act_row<FMT>(j, lane) >> 1) >= rows || (last && mdead[j]) ? kPast : mo[j] + row0,
+              (uint32_t)fk * (2 * COLS));
     if (first || S::begins(fk)) sc.fetch(fk, to_scales, lane);
     if (++fk == KT) {
       fk = 0;
@@ -606,7 +611,7 @@ static MoeSpace moe_space(int64_t T, int64_t E, int64_t topk, int64_t I) {
   MoeSpace s;
   s.up = 16;
   s.down = s.up + up16(sizeof(MoeTile) * (size_t)most_tiles(E, R, kUpRows));
-  s.weights = s.down + up16(sizeof(MoeTile) * (size_t)most_tiles(E, R, kDownRows));
+  s.weights = s.down + up16(sizeof(MoeTile) * (size_t)most_tiles(E, R, kFewRows));
   s.mid = s.weights + up16((size_t)R * 4);
   s.end = s.mid + up16((size_t)(2 * R * I) * 2);
   return s;
@@ -616,14 +621,19 @@ size_t moe_workspace(int64_t T, int64_t E, int64_t topk, int64_t I) {
   return T == 0 ? 0 : moe_space(T, E, topk, I).end;
 }
 
-template <int FMT, bool F16, int NX, int NM>
+template <int FMT, bool F16, int NX, int NM, int WD>
 static hipError_t moe_stream(const MoeArgs& p, int64_t tiles, hipStream_t stream) {
-  constexpr int WU = 4, WD = 8;
-  hipLaunchKernelGGL((moe_up_kernel<FMT, F16, NX, WU>), dim3((unsigned)(tiles * p.NT)), dim3(64 * WU), 0, stream, p);
+  constexpr int WU = 4;
+  // Blocks of the first kernel that route for themselves do so once, for several column tiles each: at most 4 blocks per CU,
+  // equally many tiles for each (2 tokens of 64 experts, int4: 55 us with a tile per block, 50 so). Where a kernel before
+  // it routes, a tile per block is as fast or faster (32 tokens FP8: 314 us; 1024 blocks, 326).
+  const int64_t items = tiles * p.NT, turns = p.inl ? (items + 1023) / 1024 : 1;
+  const size_t lds = (size_t)WD * p.T * 64 + sizeof(MoeTile) * (size_t)most_tiles(p.E, (int64_t)p.T * p.topk, p.down_rows);
+  hipLaunchKernelGGL((moe_up_kernel<FMT, F16, NX, WU>), dim3((unsigned)((items + turns - 1) / turns)), dim3(64 * WU), 0,
+                     stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down_kernel<FMT, F16, NM, WD>), dim3((unsigned)(p.H / 16)), dim3(64 * WD),
-                     (size_t)WD * p.T * 64 + sizeof(MoeTile) * (size_t)most_tiles(p.E, (int64_t)p.T * p.topk, kDownRows), stream, p);
+  hipLaunchKernelGGL((moe_down_kernel<FMT, F16, NM, WD>), dim3((unsigned)(p.H / 16)), dim3(64 * WD), lds, stream, p);
   return hipGetLastError();
 }
 
@@ -631,6 +641,9 @@ template <int FMT, bool F16>
 static hipError_t moe_go(MoeArgs& p, hipStream_t stream) {
   const int64_t R = (int64_t)p.T * p.topk;
   p.NT = p.I / 16;
+  // Longer tiles of the second kernel read an expert's weights once for more rows and hold more LDS (32 tokens of 64
+  // experts, FP8: 220 us with 4 rows, 198 with 8; 16 tokens: 175 and 174; 8 tokens of MXFP4: 66 with 4, 72 KiB instead of 57).
+  p.down_rows = R >= 2 * p.E ? kUpRows : kFewRows;
   if (!p.inl) {
     const bool general = p.route.bias || p.route.G > 1;
     const size_t keys = p.route.G > 1 ? (size_t)8 * p.E * (kPThreads / kWave) : 0;
@@ -643,8 +656,10 @@ static hipError_t moe_go(MoeArgs& p, hipStream_t stream) {
   }
   // up to 2 tokens tiles have at most 2 rows
   constexpr int C = kCols<FMT> / 128;
-  return p.T <= 2 ? moe_stream<FMT, F16, 1, C>(p, p.inl ? (R < p.E ? R : p.E) : most_tiles(p.E, R, kUpRows), stream)
-                  : moe_stream<FMT, F16, 2 * C, 2 * C>(p, most_tiles(p.E, R, kUpRows), stream);
+  if (p.T <= 2) return moe_stream<FMT, F16, 1, C, 8>(p, p.inl ? (R < p.E ? R : p.E) : most_tiles(p.E, R, kUpRows), stream);
+  const int64_t tiles = most_tiles(p.E, R, kUpRows);
+  return p.down_rows == kFewRows ? moe_stream<FMT, F16, 2 * C, 2 * C, 8>(p, tiles, stream)
+                                 : moe_stream<FMT, F16, 2 * C, 4 * C, 8>(p, tiles, stream);
 }
 
 // fmt: 0 FP8 with block scales, 1 MXFP4, 2 int4 tiles (group: 128 m, or -1).
