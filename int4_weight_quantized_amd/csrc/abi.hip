@@ -74,7 +74,7 @@ hipError_t launch_mx_dequant(const void* codes, const void* scales, int64_t M, i
                              hipStream_t stream);
 size_t mx_gemm_workspace(int64_t M, int64_t N, int64_t K);
 int64_t mx_gemm_threads(int64_t M, int64_t N, int64_t K);
-int64_t mx_grouped_threads(int64_t E, int64_t R, int64_t N);
+int64_t mx_grouped_threads(int64_t E, int64_t R, int64_t N, int64_t K);
 bool mx_inline(int64_t M, int64_t K);
 hipError_t launch_mx_gemm(const void* a, const void* a_scale, const void* w, const void* w_scale, const void* bias,
                           void* out, int out_dt, int64_t M, int64_t N, int64_t K, void* ws, hipStream_t stream);
@@ -1094,7 +1094,7 @@ int w4_mxfp4_grouped_gemm(const void* a, const void* a_scale, const int32_t* row
   if (E < 0 || E > 65535 || T < 0)
     return fail(W4_ERR_INVALID, "%s: E=%lld T=%lld out of range", fn, (long long)E, (long long)T);
   if (R == 0 || N == 0 || E == 0) return ok();
-  rc = check_threads(fn, w4::mx_grouped_threads(E, R, N));
+  rc = check_threads(fn, w4::mx_grouped_threads(E, R, N, K));
   if (rc) return rc;
   if (row_token && (T <= 0 || T * K >= ((int64_t)1 << 32)))
     return fail(W4_ERR_UNSUPPORTED, "%s: token count T=%lld out of range for K=%lld (T*K must be below 2^32)", fn,

@@ -341,22 +341,35 @@ struct MxPlan {
   int tile, splits;
 };
 
+// Streaming reads the weights once per 16 rows, mostly from L2, and needs no second launch: 64 rows of 4096 x 4096 7.1 us
+// (tiles 10.2), of 4096 x 14336 12.7 (13.4), of 14336 x 4096 11.8 (10.6). Above that the cheapest by a model of what was
+// measured: a launch, steps of 256 columns (slower where two blocks share a CU), and for splits a second launch that adds
+// the parts. It comes within 10% of the measured times from 65 to 1024 rows of the sizes above, of 1024 x 4096 and of
+// 7168 x 2048, and takes the fastest plan or one within 5% of it. For instance 128 rows of 14336 x 4096: 11.8 us in tiles of
+// 64 x 128, 13.7 of 128 x 128, 28 of 256 x 256; 200 rows of 4096 x 14336: 20.3 in 4 splits of 128 x 128, 22.2 in 4 of 64 x
+// 128, 76 in tiles of 256 x 256; 1024 rows of 14336 x 4096: 37.9 in tiles of 256 x 256, 45.2 of 128 x 128.
 static MxPlan plan_dense(int64_t M, int64_t N, int64_t K) {
-  if (M <= 16) return {0, 1};
+  if (M <= 64) return {0, 1};
+  struct Form {
+    int64_t bm, bn, launch, step, shared;            // ns; shared: a step where two blocks share a CU (0: they cannot)
+  };
+  constexpr Form forms[] = {{64, 128, 4000, 450, 800}, {128, 128, 4000, 650, 1300}, {256, 256, 6000, 1500, 0}};
   const int64_t KT = (K + kMK - 1) / kMK;
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 192 && 3 * tiles(256, 256) <= tiles(128, 128)) return {256, 1};
-  const int tile = M <= 64 ? 64 : 128;
-  const int64_t t = tiles(tile, 128);
-  int64_t best = 1, cost = 4000 + 900 * KT;          // ns
-  for (int64_t s = 2; s * t <= 512 && 2 * s <= KT; ++s) {
-    const int64_t c = 6000 + 900 * ((KT + s - 1) / s) + 100 * s + s * M * N * 8 / 4500;
-    if (c < cost) {
-      cost = c;
-      best = s;
+  MxPlan best{0, 1};
+  int64_t least = INT64_MAX;
+  for (const Form& f : forms) {
+    const int64_t t = ((M + f.bm - 1) / f.bm) * ((N + f.bn - 1) / f.bn), slots = f.shared ? 512 : 256;
+    for (int64_t s = 1; s == 1 || (f.shared && s * t <= slots && 2 * s <= KT); ++s) {
+      const int64_t step = s * t <= 256 || !f.shared ? f.step : f.shared;
+      const int64_t cost = f.launch + step * ((KT + s - 1) / s) * ((s * t + slots - 1) / slots) +
+                           (s > 1 ? 4500 + s * M * N / 1000 : 0);
+      if (cost < least) {
+        least = cost;
+        best = {(int)f.bm, (int)s};
+      }
     }
   }
-  return {tile, (int)best};
+  return best;
 }
 
 size_t mx_gemm_workspace(int64_t M, int64_t N, int64_t K) {
@@ -445,19 +458,23 @@ hipError_t launch_mx_gemm(const void* a, const void* a_scale, const void* w, con
   return hipGetLastError();
 }
 
-// What the grouped product runs as: rows streamed (0), or the tile.
-static int plan_grouped(int64_t E, int64_t R, int64_t N) {
-  if (R <= 4 * E) return 0;
+// What the grouped product runs as: rows streamed (0), or the tile's rows. By rows per expert; measured with 64 experts of
+// 4096 x 7168: 4 rows 162 us streamed, 168 in tiles of 64 x 128, 176 of 128 x 128; 16 rows 224, 182 and 187; 64 rows (-), 258
+// and 210, 229 of 256 x 256; 128 rows (-, -), 292 and 251. Of 7168 x 2048, whose K leaves a wave two steps, tiles win from the
+// start: 4 rows 104, 96 and 100. Few tiles of 256 would leave CUs idle, or their last column tile be mostly empty.
+static int plan_grouped(int64_t E, int64_t R, int64_t N, int64_t K) {
+  if (R <= 8 * E && K >= 4096) return 0;
+  if (R <= 32 * E) return 64;
   const int64_t c256 = (N + 255) / 256, c128 = (N + 127) / 128;
   if (R <= 96 * E || (R / 256 + E / 2) * c256 < 160 || 3 * 2 * c256 > 4 * c128) return 128;
   return 256;
 }
 
-int64_t mx_grouped_threads(int64_t E, int64_t R, int64_t N) {
+int64_t mx_grouped_threads(int64_t E, int64_t R, int64_t N, int64_t K) {
   if (R == 0 || N == 0 || E == 0) return 0;
-  const int tile = plan_grouped(E, R, N);
+  const int tile = plan_grouped(E, R, N, K);
   if (tile == 0) return mx_stream_threads(0, N, E, R);
-  return grouped_blocks(E, R, N, tile, tile) * 256;
+  return grouped_blocks(E, R, N, tile, tile == 256 ? 256 : 128) * 256;
 }
 
 hipError_t launch_mx_grouped(const void* a, const void* a_scale, const int32_t* row_token, const int32_t* offsets,
@@ -469,8 +486,11 @@ hipError_t launch_mx_grouped(const void* a, const void* a_scale, const int32_t* 
   p.offsets = offsets;
   p.R = R;
   p.E = (int)E;
-  const int tile = plan_grouped(E, R, N);
+  const int tile = plan_grouped(E, R, N, K);
   if (tile == 0) return launch_mx_stream(p, 0, out_dt, stream);
+  if (tile == 64)
+    return out_dt == 0 ? tile_go<64, 128>(p, mx_tile_kernel<2, 2, 1, 2, true, 0>, stream)
+                       : tile_go<64, 128>(p, mx_tile_kernel<2, 2, 1, 2, true, 1>, stream);
   if (tile == 128)
     return out_dt == 0 ? tile_go<128, 128>(p, mx_tile_kernel<2, 2, 2, 2, true, 0>, stream)
                        : tile_go<128, 128>(p, mx_tile_kernel<2, 2, 2, 2, true, 1>, stream);

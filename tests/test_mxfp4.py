@@ -174,10 +174,12 @@ def test_gemm(M, N, K, dt):
     assert torch.equal(got, again)
 
 
-@pytest.mark.parametrize("M,N,K", [(3590, 3528, 352), (4096, 3328, 768)])
+@pytest.mark.parametrize("M,N,K", [(3590, 3528, 352), (4096, 3328, 768), (200, 14344, 544), (1000, 2056, 1056),
+                                   (320, 2184, 8224)])
 @pytest.mark.parametrize("dt", list(DT))
 def test_gemm_large_tiles(M, N, K, dt):
-    """192 tiles of 256 x 256 and more, ragged ones and a partial last step among them; compared in fp64 on the GPU."""
+    """Tiles of 256 x 256 and of 128 x 128, with and without splits, ragged ones and a partial last step among them; compared
+    in fp64 on the GPU."""
     r = rng_for(M, N, K)
     (a, sa), (w, sw) = matrix(r, M, K), matrix(r, N, K)
     say("gemm large", M, N, K, dt)
@@ -187,7 +189,8 @@ def test_gemm_large_tiles(M, N, K, dt):
     check(got, y, product_tol(y, mag, dt, K), (M, N, K, dt))
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 264, 4096), (16, 40, 96), (16, 8200, 288), (17, 136, 160), (200, 264, 2880), (300, 512, 256)])
+@pytest.mark.parametrize("M,N,K", [(1, 264, 4096), (16, 40, 96), (16, 8200, 288), (16, 264, 4160), (17, 136, 160), (200, 264, 2880),
+                                   (300, 512, 256)])
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_linear_is_quantize_and_gemm(M, N, K, dt):
     """From 16-bit activations: the same numbers as the two calls, to the bit, whatever the rows quantize to."""
@@ -233,7 +236,7 @@ def segments(r, E, R, kind):
 
 
 @pytest.mark.parametrize("E,R,N,K", [(1, 1, 8, 32), (8, 8, 136, 96), (64, 64, 264, 288), (4, 100, 136, 160), (8, 700, 264, 416),
-                                     (3, 1000, 520, 224), (4, 5600, 2056, 288)])
+                                     (3, 1000, 520, 224), (4, 5600, 2056, 288), (64, 64, 264, 4128), (3, 20, 136, 4256)])
 @pytest.mark.parametrize("kind", ["even", "one", "ragged"])
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_grouped(E, R, N, K, kind, dt):
