@@ -126,7 +126,8 @@ struct Scales {
   // begins: whether a step's scales come with it (a run's first step, and every kSteps)
   static __device__ __forceinline__ bool begins(int k) { return k % kSteps == 0; }
   __device__ __forceinline__ void fetch(int k, uint32_t dst, int lane) const {
-    k = __builtin_amdgcn_readfirstlane(k);           // (the compiler does not see everywhere that it is uniform)
+    k = __builtin_amdgcn_readfirstlane(k);           // (the compiler does not see everywhere that they are uniform)
+    dst = __builtin_amdgcn_readfirstlane(dst);
     if (lane >= kLanes) return;
     if constexpr (FMT == kFp8) {
       dma4(s, dst, off, (uint32_t)(k & ~7) * 4);

@@ -52,7 +52,7 @@ struct MoeArgs {
   int T, E, topk, H, I;
   int G13, G2;                                       // int4: scale groups along K
   int kg13, kg2;                                     // and steps per group
-  int NT;                                            // column tiles of the launch
+  int NT;                                            // column tiles of the first kernel
   int inl;                                           // the first kernel routes
   int down_rows;                                     // most rows of a tile of the second
   // workspace
@@ -456,29 +456,29 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
   }
 }
 
-// Down: a block owns 16 output columns of all tokens; its waves share the (tile, step) pairs, each a run of them. At a
+// Down: a block owns 16 NJ output columns of all tokens; its waves share the (tile, step) pairs, each a run of them. At a
 // tile's end a wave adds its sums to its own place in LDS by token: no token takes anything of an expert that it did not
 // choose, and the order is fixed. NM: DMAs of a step's middle (row r's first numbers as row 2 r, its second as 2 r + 1).
-template <int FMT, bool F16OUT, int NM, int WS>
+template <int FMT, bool F16OUT, int NM, int WS, int NJ>
 __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
   constexpr int COLS = kCols<FMT>, HALVES = FMT == kFp8 ? 1 : 2;
-  using S = Scales<FMT, 1>;
-  constexpr int kX = 2048, kSlot = kX + 1024 * NM;
+  using S = Scales<FMT, NJ>;
+  constexpr int kX = 2048 * NJ, kSlot = kX + 1024 * NM;
   constexpr int kMost = kRowsPerDma<FMT> * NM / 2;   // rows that fit
   __shared__ __attribute__((aligned(16))) uint8_t room[WS][kSlot], room_scales[WS][S::kBytes];
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  v4f* sum = reinterpret_cast<v4f*>(smem);           // [WS][T][4]
+  v4f* sum = reinterpret_cast<v4f*>(smem);           // [WS][T][4 NJ]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, l16 = lane & 15;
-  const int n0 = 16 * (int)blockIdx.x;
+  const int n0 = 16 * NJ * (int)blockIdx.x;
   const int KT = (p.I + COLS - 1) / COLS, tiles = p.counts[1], steps = tiles * KT;
-  MoeTile* list = reinterpret_cast<MoeTile*>(sum + WS * p.T * 4);
+  MoeTile* list = reinterpret_cast<MoeTile*>(sum + WS * p.T * 4 * NJ);
   for (int i = tid; i < tiles; i += 64 * WS) list[i] = p.down[i];
-  for (int i = tid; i < WS * p.T * 4; i += 64 * WS) sum[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int i = tid; i < WS * p.T * 4 * NJ; i += 64 * WS) sum[i] = v4f{0.f, 0.f, 0.f, 0.f};
   const int64_t plane = (int64_t)p.T * p.topk * p.I * 2;
   const __amdgpu_buffer_rsrc_t mr = make_rsrc(p.mid, (uint32_t)(2 * plane));
   __syncthreads();
-  v4f* mine = sum + wave * p.T * 4;
+  v4f* mine = sum + wave * p.T * 4 * NJ;
   const int i0 = (int)((int64_t)steps * wave / WS), i1 = (int)((int64_t)steps * (wave + 1) / WS);
   const uint8_t *step = &room[wave][0], *scales = &room_scales[wave][0];
   const uint32_t to = lds_address(step), to_scales = lds_address(scales);
@@ -492,7 +492,7 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
   }
   // the tile and step that are fetched next, and those that are computed
   int ft = i0 / KT, fk = i0 - ft * KT, ct = ft, ck = fk;
-  Rows<FMT> w;
+  Rows<FMT> w[NJ];
   S sc;
   int rows = 0;
   uint32_t row0 = 0;
@@ -501,12 +501,14 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
     const int e = __builtin_amdgcn_readfirstlane(tile.e);
     rows = __popc(__builtin_amdgcn_readfirstlane(tile.tokens));
     row0 = (uint32_t)__builtin_amdgcn_readfirstlane(tile.row0) * (uint32_t)p.I * 2u;
-    w.open(p.w2, e, p.H, n0, p.I);
-    sc.open(p.s2, e, p.H, n0, 0, p.I, p.G2);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) w[j].open(p.w2, e, p.H, n0 + 16 * j, p.I);
+    sc.open(p.s2, e, p.H, n0, 16, p.I, p.G2);
   };
   auto fetch = [&](bool first) {
     const bool last = fk == KT - 1;
-    w.fetch(fk, last, to);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) w[j].fetch(fk, last, to + 2048 * j);
 #pragma unroll
     for (int j = 0; j < NM; ++j)                     // (rows that the tile does not have: whatever lies there, not stored)
       if (kRowsPerDma<FMT> * j < 2 * rows)
@@ -520,26 +522,35 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
     }
   };
   if (i0 < i1) {
-    v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
-    w.lane(n0, p.I, lane);
-    sc.lane(p.H, n0, 0, p.I, p.kg2, lane);
+    v4f acc[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+      w[j].lane(n0 + 16 * j, p.I, lane);
+    }
+    sc.lane(p.H, n0, 16, p.I, p.kg2, lane);
     open_tile();
     fetch(true);
     const int mrow = (2 * (l16 & 7) + (l16 >> 3)) & (2 * kMost - 1);
     for (int i = i0; i < i1; ++i) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      v4i qw[2], M[HALVES][4];
-      float ls[HALVES];
-      v4f ms[HALVES];
+      v4i qw[NJ][2], M[HALVES][4];
+      float ls[NJ][HALVES];
+      v4f ms[NJ][HALVES];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) qw[q] = weight_piece<FMT>(step, q, l16, g);
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) qw[j][q] = weight_piece<FMT>(step + 2048 * j, q, l16, g);
 #pragma unroll
       for (int q = 0; q < HALVES; ++q) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           M[q][c] = act_chunk<FMT>(step + kX, mrow, FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
-        if constexpr (FMT == kMx) ls[q] = S::block(scales, ck, 0, q, p.I - ck * COLS, l16, g);
-        else ms[q] = S::sums(scales, ck, 0, q, g);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          if constexpr (FMT == kMx) ls[j][q] = S::block(scales, ck, j, q, p.I - ck * COLS, l16, g);
+          else ms[j][q] = S::sums(scales, ck, j, q, g);
+        }
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
@@ -547,39 +558,52 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int q = 0; q < HALVES; ++q) {
-        v4f v = FMT == kMx ? acc : v4f{0.f, 0.f, 0.f, 0.f};
+        v4f v[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) v[j] = FMT == kMx ? acc[j] : v4f{0.f, 0.f, 0.f, 0.f};
         if constexpr (FMT == kInt4) {
           const int m8 = (int)0xC100C100;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) v = mfma16<false>(bf(v4i{m8, m8, m8, m8}), bf(act_piece<FMT>(M[q], c)), v);
+          for (int c = 0; c < 4; ++c) v[0] = mfma16<false>(bf(v4i{m8, m8, m8, m8}), bf(act_piece<FMT>(M[q], c)), v[0]);
+#pragma unroll
+          for (int j = 1; j < NJ; ++j) v[j] = v[0];
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v = mfma16<false>(decode<FMT, false>(qw, q, c, ls[q]), bf(act_piece<FMT>(M[q], c)), v);
-        if constexpr (FMT == kMx) {
-          acc = v;
-        } else {
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[c] = fmaf(v[c], ms[q][c], acc[c]);
+          for (int j = 0; j < NJ; ++j)
+            v[j] = mfma16<false>(decode<FMT, false>(qw[j], q, c, ls[j][q]), bf(act_piece<FMT>(M[q], c)), v[j]);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          if constexpr (FMT == kMx) {
+            acc[j] = v[j];
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[j][c] = fmaf(v[j][c], ms[j][q][c], acc[j][c]);
+          }
         }
       }
       if (++ck == KT || i == i1 - 1) {               // the tile's last step here
         const MoeTile tile = list[ct];
         const int token = tile_token(tile.tokens, l16 & 7);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[c] += __shfl_xor(acc[c], 8, kWave);
-        if (l16 < 8 && token >= 0) mine[token * 4 + g] += acc;
-        acc = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[j][c] += __shfl_xor(acc[j][c], 8, kWave);
+          if (l16 < 8 && token >= 0) mine[(token * NJ + j) * 4 + g] += acc[j];
+          acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+        }
         ck = 0;
         ++ct;
       }
     }
   }
   __syncthreads();
-  for (int i = tid; i < p.T * 4; i += 64 * WS) {
+  for (int i = tid; i < p.T * 4 * NJ; i += 64 * WS) {
     v4f v = sum[i];
 #pragma unroll
-    for (int w = 1; w < WS; ++w) v += sum[w * p.T * 4 + i];
-    const int64_t at = (int64_t)(i / 4) * p.H + n0 + 4 * (i % 4);
+    for (int w = 1; w < WS; ++w) v += sum[w * p.T * 4 * NJ + i];
+    const int64_t at = (int64_t)(i / (4 * NJ)) * p.H + n0 + 4 * (i % (4 * NJ));
     if (p.add) {
       const v2i a = *reinterpret_cast<const v2i*>(p.add + at);
 #pragma unroll
@@ -621,19 +645,20 @@ size_t moe_workspace(int64_t T, int64_t E, int64_t topk, int64_t I) {
   return T == 0 ? 0 : moe_space(T, E, topk, I).end;
 }
 
-template <int FMT, bool F16, int NX, int NM, int WD>
+template <int FMT, bool F16, int NX, int NM, int WD, int NJ>
 static hipError_t moe_stream(const MoeArgs& p, int64_t tiles, hipStream_t stream) {
   constexpr int WU = 4;
   // Blocks of the first kernel that route for themselves do so once, for several column tiles each: at most 4 blocks per CU,
   // equally many tiles for each (2 tokens of 64 experts, int4: 55 us with a tile per block, 50 so). Where a kernel before
   // it routes, a tile per block is as fast or faster (32 tokens FP8: 314 us; 1024 blocks, 326).
   const int64_t items = tiles * p.NT, turns = p.inl ? (items + 1023) / 1024 : 1;
-  const size_t lds = (size_t)WD * p.T * 64 + sizeof(MoeTile) * (size_t)most_tiles(p.E, (int64_t)p.T * p.topk, p.down_rows);
+  // (with the most of everything, 32 tokens of 1024 experts, 64 chosen: 154 KiB with what is static)
+  const size_t lds = (size_t)WD * p.T * 64 * NJ + sizeof(MoeTile) * (size_t)most_tiles(p.E, (int64_t)p.T * p.topk, p.down_rows);
   hipLaunchKernelGGL((moe_up_kernel<FMT, F16, NX, WU>), dim3((unsigned)((items + turns - 1) / turns)), dim3(64 * WU), 0,
                      stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down_kernel<FMT, F16, NM, WD>), dim3((unsigned)(p.H / 16)), dim3(64 * WD), lds, stream, p);
+  hipLaunchKernelGGL((moe_down_kernel<FMT, F16, NM, WD, NJ>), dim3((unsigned)(p.H / (16 * NJ))), dim3(64 * WD), lds, stream, p);
   return hipGetLastError();
 }
 
@@ -642,7 +667,7 @@ static hipError_t moe_go(MoeArgs& p, hipStream_t stream) {
   const int64_t R = (int64_t)p.T * p.topk;
   p.NT = p.I / 16;
   // Longer tiles of the second kernel read an expert's weights once for more rows and hold more LDS (32 tokens of 64
-  // experts, FP8: 220 us with 4 rows, 198 with 8; 16 tokens: 175 and 174; 8 tokens of MXFP4: 66 with 4, 72 KiB instead of 57).
+  // experts, FP8: 220 us with 4 rows, 198 with 8; 16 tokens: 175 and 174; 8 tokens of MXFP4: 66 and 74).
   p.down_rows = R >= 2 * p.E ? kUpRows : kFewRows;
   if (!p.inl) {
     const bool general = p.route.bias || p.route.G > 1;
@@ -656,10 +681,18 @@ static hipError_t moe_go(MoeArgs& p, hipStream_t stream) {
   }
   // up to 2 tokens tiles have at most 2 rows
   constexpr int C = kCols<FMT> / 128;
-  if (p.T <= 2) return moe_stream<FMT, F16, 1, C, 8>(p, p.inl ? (R < p.E ? R : p.E) : most_tiles(p.E, R, kUpRows), stream);
+  if (p.T <= 2)
+    return moe_stream<FMT, F16, 1, C, 8, 1>(p, p.inl ? (R < p.E ? R : p.E) : most_tiles(p.E, R, kUpRows), stream);
   const int64_t tiles = most_tiles(p.E, R, kUpRows);
-  return p.down_rows == kFewRows ? moe_stream<FMT, F16, 2 * C, 2 * C, 8>(p, tiles, stream)
-                                 : moe_stream<FMT, F16, 2 * C, 4 * C, 8>(p, tiles, stream);
+  // The second kernel reads the middle, from L2, once per block: with 32 columns per block half as often (32 tokens, 7168 x
+  // 2048, FP8: 199 us with 16 columns, 160 with 32; 8 tokens of MXFP4: 66 and 58), if that leaves enough blocks; else more
+  // waves share the steps (32 tokens, 2048 x 1024, FP8: 32 columns 70 us, 16 columns 58, with 12 waves 51; 8 tokens of
+  // 4096 x 2048, MXFP4: 54, 46 and 39). LDS bounds the waves of long tiles.
+  if (p.H >= 6144)
+    return p.down_rows == kFewRows ? moe_stream<FMT, F16, 2 * C, 2 * C, 8, 2>(p, tiles, stream)
+                                   : moe_stream<FMT, F16, 2 * C, 4 * C, 8, 2>(p, tiles, stream);
+  return p.down_rows == kFewRows ? moe_stream<FMT, F16, 2 * C, 2 * C, 12, 1>(p, tiles, stream)
+                                 : moe_stream<FMT, F16, 2 * C, 4 * C, 10, 1>(p, tiles, stream);
 }
 
 // fmt: 0 FP8 with block scales, 1 MXFP4, 2 int4 tiles (group: 128 m, or -1).

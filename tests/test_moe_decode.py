@@ -125,7 +125,8 @@ def test_layer_ends_of_the_routing(fmt, T, E, topk):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("H,I,topk,T", [(2048, 1408, 4, 1), (7168, 256, 2, 5), (256, 2048, 8, 20)])
+@pytest.mark.parametrize("H,I,topk,T", [(2048, 1408, 4, 1), (7168, 256, 2, 5), (256, 2048, 8, 20), (6272, 128, 8, 32),
+                                        (7168, 128, 3, 17)])
 def test_layer_long_sums(fmt, H, I, topk, T):
     r = rng_for(H, I)
     w = layer(fmt, r, 8, H, I)
@@ -133,6 +134,19 @@ def test_layer_long_sums(fmt, H, I, topk, T):
     logits = gpu(r.standard_normal((T, 8)), torch.float32)
     say("long", fmt, H, I, topk, T)
     check(call(x, logits, topk, w, fmt), x, logits, topk, w, "f16")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T", [1, 2])
+def test_blocks_that_take_several_column_tiles(fmt, T):
+    """More tiles than blocks that route for themselves."""
+    r = rng_for(T, 31)
+    E, topk, H, I = 64, 24 * (3 - T), 128, 768 // T
+    w = layer(fmt, r, E, H, I)
+    x = gpu(r.standard_normal((T, H)), torch.bfloat16)
+    logits = gpu(r.standard_normal((T, E)), torch.float32)
+    say("several tiles", fmt, T)
+    check(call(x, logits, topk, w, fmt), x, logits, topk, w, "bf16")
 
 
 @pytest.mark.parametrize("fmt", FMTS)
