@@ -266,29 +266,34 @@ __global__ __launch_bounds__(kPThreads) void moe_plan_kernel(MoeArgs p) {
     }
   }
   __syncthreads();
-  // thread e: the expert's rows and tiles, and the sums of those before it
+  // thread e: the expert's rows and tiles, and the sums of those before it (the waves that hold experts)
+  const int waves = (a.E + kWave - 1) / kWave;
   const uint32_t m = mask[tid];
   const int n = __popc(m), up = (n + kUpRows - 1) / kUpRows, dn = (n + p.down_rows - 1) / p.down_rows;
   int s[3] = {n, up, dn};
+  if (wave < waves) {
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < 3; ++k) {
 #pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-      const int o = __shfl_up(s[k], off, kWave);
-      if (lane >= off) s[k] += o;
+      for (int off = 1; off < kWave; off <<= 1) {
+        const int o = __shfl_up(s[k], off, kWave);
+        if (lane >= off) s[k] += o;
+      }
+      if (lane == 63) part[k][wave] = s[k];
     }
-    if (lane == 63) part[k][wave] = s[k];
   }
-  __syncthreads();
+  if (waves > 1) __syncthreads();
+  if (wave < waves) {
 #pragma unroll
-  for (int k = 0; k < 3; ++k)
-    for (int v = 0; v < wave; ++v) s[k] += part[k][v];
-  row0[tid] = s[0] - n;
-  for (int i = 0; i < up; ++i) p.up[s[1] - up + i] = tile_of(tid, s[0] - n, m, i, kUpRows);
-  for (int i = 0; i < dn; ++i) p.down[s[2] - dn + i] = tile_of(tid, s[0] - n, m, i, p.down_rows);
-  if (tid == kPThreads - 1) {
-    p.counts[0] = s[1];
-    p.counts[1] = s[2];
+    for (int k = 0; k < 3; ++k)
+      for (int v = 0; v < wave; ++v) s[k] += part[k][v];
+    row0[tid] = s[0] - n;
+    for (int i = 0; i < up; ++i) p.up[s[1] - up + i] = tile_of(tid, s[0] - n, m, i, kUpRows);
+    for (int i = 0; i < dn; ++i) p.down[s[2] - dn + i] = tile_of(tid, s[0] - n, m, i, p.down_rows);
+    if (tid == waves * kWave - 1) {
+      p.counts[0] = s[1];
+      p.counts[1] = s[2];
+    }
   }
   __syncthreads();
 #pragma unroll
