@@ -75,7 +75,7 @@ hipError_t launch_mx_dequant(const void* codes, const void* scales, int64_t M, i
 size_t mx_gemm_workspace(int64_t M, int64_t N, int64_t K);
 int64_t mx_gemm_threads(int64_t M, int64_t N, int64_t K);
 int64_t mx_grouped_threads(int64_t E, int64_t R, int64_t N, int64_t K);
-bool mx_inline(int64_t M, int64_t K);
+bool mx_inline(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx_gemm(const void* a, const void* a_scale, const void* w, const void* w_scale, const void* bias,
                           void* out, int out_dt, int64_t M, int64_t N, int64_t K, void* ws, hipStream_t stream);
 hipError_t launch_mx_linear_few(const void* x, bool bf16, const void* w, const void* w_scale, const void* bias, void* out,
@@ -1038,7 +1038,7 @@ int w4_mxfp4_gemm(const void* a, const void* a_scale, const void* w, const void*
 static size_t mx_linear_codes(int64_t M, int64_t K) { return (size_t)M * (size_t)(K / 2); }
 static size_t mx_linear_scales(int64_t M, int64_t K) { return ((size_t)M * (size_t)mx_row_scales(K) + 15) & ~(size_t)15; }
 static size_t mx_linear_workspace(int64_t M, int64_t N, int64_t K) {
-  if (M == 0 || N == 0 || w4::mx_inline(M, K)) return 0;
+  if (M == 0 || N == 0 || w4::mx_inline(M, N, K)) return 0;
   return mx_linear_codes(M, K) + mx_linear_scales(M, K) + w4::mx_gemm_workspace(M, N, K);
 }
 
@@ -1073,7 +1073,7 @@ int w4_mxfp4_linear(const void* x, int x_dtype, const void* w, const void* w_sca
   if (rc) return rc;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const bool bf16 = x_dtype == W4_BF16;
-  if (w4::mx_inline(M, K)) return hip_status(w4::launch_mx_linear_few(x, bf16, w, w_scale, bias, out, M, N, K, s), fn);
+  if (w4::mx_inline(M, N, K)) return hip_status(w4::launch_mx_linear_few(x, bf16, w, w_scale, bias, out, M, N, K, s), fn);
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   uint8_t* scales = codes + mx_linear_codes(M, K);
   const hipError_t e = w4::launch_mx_quant(x, bf16 ? 0 : 1, false, M, K, K, codes, scales, s);

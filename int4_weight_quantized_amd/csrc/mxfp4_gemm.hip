@@ -16,13 +16,24 @@
 // - The matrix unit reads, from lane (row, half h), 16 bytes = one block of 32
 //   columns. MFMA c of a step takes the blocks c (h = 0) and 4 + c (h = 1), so
 //   a lane's four scales of a step are one word of LDS, byte c of it MFMA c's.
-// - The fragments of MFMA group c + 1 are read under the MFMAs of group c. The
-//   last group of a step runs behind the barrier that ends the step: its
-//   operands are in registers by then, so its stage is free for the DMA two
-//   steps ahead and the next step's first fragments are read under it.
+// - A step is four groups of MFMAs, one per c. Under group 0 the fragments of the
+//   other three are read; a barrier, and the stage is free: the DMA two steps
+//   ahead goes out under group 1. A second barrier before group 3, by which the
+//   next step's tiles have landed; its first fragments are read under group 3.
+//   (With the last group behind the barrier that ends the step, in the compiler's
+//   order, the 256 x 256 tile took 192 us for 4096 x 14336 x 4096; so 154.)
 // - The weights are the A operand and the activations the B operand: a lane's
 //   results lie in one activation row. Row q of a weight fragment is its column
 //   16 (q / 4 % 2) + 4 (q / 8) + q % 4, which gives a lane 16 consecutive ones.
+// - Results leave through LDS as whole rows: straight from the registers a store
+//   would be half a cache line of each of 32 rows (154 us, 151 so).
+// What bounds it: 4096 x 14336 x 4096 takes 144 us, 3.3 PFLOP/s, K = 16384 reaches
+// 4.1, where the fp4 matrix rate alone is 8.4. Each round of tiles ends in a
+// burst of stores that memory takes 7 us for and nothing overlaps (about 30 of the
+// 144 us, from the times of K = 512 to 16384); within the loop a step of 256 columns takes 2.1 us, at a clock that the
+// power limit holds near 1.6 GHz there; without its DMA it takes 1.4, and with a
+// quarter of its MFMAs 1.1 (measured at shorter K, where the clock is higher and the
+// whole step takes 1.8).
 #include <type_traits>
 
 #include "mxfp4.h"
@@ -388,7 +399,10 @@ int64_t mx_gemm_threads(int64_t M, int64_t N, int64_t K) {
   return product > reduce ? product : reduce;
 }
 
-bool mx_inline(int64_t M, int64_t K) { return M <= 16 && M * K <= 65536; }
+// Whether the linear layer's product quantizes the rows itself, every block all of them, instead of a launch before it: the
+// more the blocks, the fewer. 8 x 14336 x 4096 8.4 us (two launches 8.9), 12 rows 9.5 (8.8); 4 x 4096 x 14336 13.8 (13.8),
+// 8 rows 17.3 (13.9); 12 x 4096 x 4096 6.2 (7.2), 16 rows 7.8 (7.3); 8 x 2048 x 7168 7.5 (9.0), 16 rows 10.0 (9.0).
+bool mx_inline(int64_t M, int64_t N, int64_t K) { return M <= 16 && M * K <= (N <= 8192 ? 65536 : 32768); }
 
 template <int BM, int BN, typename F>
 static hipError_t tile_go(MxArgs p, F kernel, hipStream_t stream) {
