@@ -479,6 +479,23 @@ def _call(fn: str, *args) -> None:
     _check(fn, rc)
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _on_current_device(stream, *tensors) -> None:
+    """A launch goes to the current device, whatever memory it is given: refuses tensors or a stream of another one."""
+    here = None
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            if here is None:
+                here = _current_device()
+                if stream is not None and stream.device_index != here:
+                    raise ValueError(f"the stream is of cuda:{stream.device_index}, the current device is cuda:{here}")
+            if t.get_device() != here:
+                raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{here}")
+
+
 def _e4m3_codes(t, what: str):
     if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
         raise TypeError(f"{what} must hold E4M3 codes (torch.float8_e4m3fn or uint8), got {t.dtype}")
@@ -637,6 +654,7 @@ def w4_mxfp4_quantize(x, act: str = "none", out=None, stream=None):
     if out is None:
         out = (_new((M, K // 2), torch.uint8, x.device, stream), _new((M, _mx_row(K)), torch.uint8, x.device, stream))
     codes, scales = out
+    _on_current_device(stream, x, codes, scales)
     _call("w4_mxfp4_quantize",
         ptr, _float_code(x.dtype), M, K, ldx, W4_ACTS[act], _arg(codes, torch.uint8, (M, K // 2), "codes"),
         _arg(scales, torch.uint8, (M, _mx_row(K)), "scales"), _stream(stream))
@@ -649,6 +667,7 @@ def w4_mxfp4_dequantize(codes, scales, out=None, out_dtype=torch.bfloat16, strea
     M, K = codes.shape[0], 2 * codes.shape[1]
     if out is None:
         out = _new((M, K), out_dtype, codes.device, stream)
+    _on_current_device(stream, codes, scales, out)
     _call("w4_mxfp4_dequantize",
         _arg(codes, torch.uint8, (M, K // 2), "codes"), _arg(scales, torch.uint8, (M, _mx_row(K)), "scales"), M, K,
         _arg(out, out.dtype, (M, K), "out"), _float_code(out.dtype), _stream(stream))
@@ -677,6 +696,7 @@ def w4_mxfp4_gemm(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.b
     p_out = _arg(out, out.dtype, (M, N), "out")
     if workspace is None:
         workspace = w4_mxfp4_gemm_workspace(M, N, K, a.device, stream)
+    _on_current_device(stream, a, a_scale, w, w_scale, bias, out, workspace)
     _call("w4_mxfp4_gemm",
         p_a, p_as, p_w, p_ws, p_bias, p_out, _float_code(out.dtype), M, N, K, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
@@ -704,6 +724,7 @@ def w4_mxfp4_linear(x, w, w_scale, bias=None, out=None, workspace=None, stream=N
     p_out = _arg(out, x.dtype, (M, N), "out")
     if workspace is None:
         workspace = w4_mxfp4_linear_workspace(M, N, K, x.device, stream)
+    _on_current_device(stream, x, w, w_scale, bias, out, workspace)
     _call("w4_mxfp4_linear",
         p_x, _half_code(x.dtype), p_w, p_ws, p_bias, p_out, M, N, K, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
@@ -727,6 +748,7 @@ def w4_mxfp4_grouped_gemm(a, a_scale, row_token, expert_offsets, w, w_scale, out
     p_off = _arg(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
     p_w, p_ws = _arg(w, torch.uint8, (E, N, KH), "w"), _arg(w_scale, torch.uint8, (E, N, KS), "w_scale")
     p_out = _arg(out, out.dtype, (R, N), "out")
+    _on_current_device(stream, a, a_scale, row_token, expert_offsets, w, w_scale, out)
     _call("w4_mxfp4_grouped_gemm",
         p_a, p_as, p_token, p_off, E, p_w, p_ws, p_out, _half_code(out.dtype), T, R, N, K, _stream(stream))
     return out
@@ -794,6 +816,7 @@ def w4_moe_decode(x, logits, topk: int, w13, w13_scale, w2, w2_scale, fmt: str =
     p_add, p_out = _arg(add, x.dtype, (T, H), "add"), _arg(out, x.dtype, (T, H), "out")
     if workspace is None:
         workspace = w4_moe_decode_workspace(T, E, topk, H, I, x.device, stream)
+    _on_current_device(stream, x, logits, w13, w13_scale, w2, w2_scale, bias, add, out, workspace)
     _call("w4_moe_decode",
         _arg(x, x.dtype, (T, H), "x"), _half_code(x.dtype), ptr, _float_code(logits.dtype), ld, W4_SCORES[score], p_bias,
         n_groups, topk_groups, group_top, topk, int(renorm), scale, W4_MOE_FORMATS[fmt], p_w13, p_s13, p_w2, p_s2, group,

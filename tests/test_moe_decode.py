@@ -239,6 +239,48 @@ def test_captured_strided_in_place_and_on_another_stream(fmt, T):
         assert torch.equal(out, call(x, logits, topk, w, fmt)), k
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_two_calls_at_once(fmt):
+    """On streams and workspaces of their own: what each gives alone."""
+    r = rng_for(41)
+    E, topk, H, I = 16, 4, 512, 256
+    w = layer(fmt, r, E, H, I)
+    sets = [(gpu(r.standard_normal((T, H)), torch.bfloat16), gpu(r.standard_normal((T, E)), torch.float32)) for T in (2, 9, 32)]
+    say("at once", fmt)
+    want = [call(x, lg, topk, w, fmt) for x, lg in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[call(x, lg, topk, w, fmt, stream=s) for _ in range(8)] for (x, lg), s in zip(sets, streams)]
+    torch.cuda.synchronize()
+    for v, several in zip(want, got):
+        assert all(torch.equal(v, g) for g in several)
+
+
+def test_tensors_of_another_device(monkeypatch):
+    """Calls with tensors or a stream of another device than the current one are refused."""
+    r = rng_for(43)
+    w, x = layer("mxfp4", r, 4, 64, 32), gpu(r.standard_normal((2, 64)), torch.bfloat16)
+    logits = gpu(r.standard_normal((2, 4)), torch.float32)
+    offsets = gpu(np.array([0, 1, 1, 2, 2], dtype=np.int32))
+    a, sa = ops.w4_mxfp4_quantize(x)
+    (w13, s13), side = w[0][0], torch.cuda.Stream()
+    calls = [lambda **kw: ops.w4_mxfp4_quantize(x, **kw), lambda **kw: ops.w4_mxfp4_dequantize(a, sa, **kw),
+             lambda **kw: ops.w4_mxfp4_gemm(a, sa, w13[0], s13[0], **kw),
+             lambda **kw: ops.w4_mxfp4_linear(x, w13[0], s13[0], **kw),
+             lambda **kw: ops.w4_mxfp4_grouped_gemm(a, sa, None, offsets, w13, s13, **kw),
+             lambda **kw: call(x, logits, 2, w, "mxfp4", **kw)]
+    for f in calls:
+        f()
+        f(stream=side)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(ops, "_current_device", lambda: 1)
+    for f in calls:
+        with pytest.raises(ValueError, match="current device is cuda:1"):
+            f()
+        with pytest.raises(ValueError, match="current device is cuda:1"):
+            f(stream=side)
+
+
 def test_nothing_to_do():
     (w13, s13), (w2, s2) = (m[0] for m in layer("mxfp4", rng_for(1), 4, 64, 32))
     x = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)

@@ -332,3 +332,40 @@ def test_captured_and_on_another_stream():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, ops.w4_mxfp4_linear(x, w, sw)), (M, k)
+
+
+def test_captured_products():
+    """A gated quantization, a split product and a grouped one of few rows in one graph; every replay equals the eager calls
+    on the same inputs, with eager calls of the same operators between them."""
+    r = rng_for(5)
+    M, N, K, E = 100, 544, 4128, 4
+    w, sw = (gpu(t) for t in matrix(r, N, K))
+    we, se = (t.view(E, N // 4, -1) for t in (w[:N // 4 * E], sw[:N // 4 * E]))
+    offsets = gpu(np.array([0, 3, 3, 9, 20], dtype=np.int32))
+    x = gpu(r.standard_normal((M, 2 * K)), torch.float16)
+    a = (torch.empty(M, K // 2, dtype=torch.uint8, device=DEV), torch.empty(M, O.row_scales(K), dtype=torch.uint8, device=DEV))
+    out = torch.empty(M, N, dtype=torch.float32, device=DEV)
+    rows = torch.zeros(20, N // 4, dtype=torch.float16, device=DEV)
+    ws = ops.w4_mxfp4_gemm_workspace(M, N, K, device=DEV)
+    assert ws.numel() > 0
+
+    def run(a, out, rows, ws):
+        ops.w4_mxfp4_quantize(x, act="swiglu", out=a)
+        ops.w4_mxfp4_gemm(*a, w, sw, out=out, workspace=ws)
+        ops.w4_mxfp4_grouped_gemm(a[0][:20], a[1][:20], None, offsets, we, se, out=rows)
+
+    say("captured products")
+    graph = torch.cuda.CUDAGraph()
+    run(a, out, rows, ws)
+    with torch.cuda.graph(graph):
+        run(a, out, rows, ws)
+    for k in range(4):
+        x.copy_(gpu(r.standard_normal((M, 2 * K)), torch.float16))
+        out.zero_()
+        rows.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = tuple(torch.empty_like(t) for t in a), torch.empty_like(out), torch.empty_like(rows), torch.empty_like(ws)
+        run(*eager)
+        assert torch.equal(out, eager[1]) and torch.equal(rows, eager[2]), k
+        assert torch.equal(a[0], eager[0][0]) and torch.equal(a[1], eager[0][1]), k
