@@ -68,7 +68,7 @@ __device__ __forceinline__ v4f block_product(const v8i& w, const v8i& a) {
 // the x-th eighth of the items, column tile fastest, so that its blocks share
 // gathered rows and an expert's weights.
 struct Segment {
-  int e, mt, tn;
+  int e, mt, tn, left;                               // left: items behind it in the XCD's eighth
   int64_t row0, rows;
 };
 
@@ -91,6 +91,7 @@ __device__ __forceinline__ Segment find_segment(const P& p) {
   if (xi >= per || t >= total) return s;
   const int want = t / p.NT;                         // row tile, over all experts
   s.tn = t - want * p.NT;
+  s.left = min(per - xi, total - t) - 1;
   int cum = 0;
   for (int c = 0; c < p.E && s.e < 0; c += 64) {     // 64 experts per round, one per lane
     int o0 = 0, o1 = 0;

@@ -58,10 +58,21 @@ __device__ __forceinline__ int pack16(float x, float y) {
   else return __builtin_bit_cast(int, __builtin_convertvector(v2f{x, y}, v2h));
 }
 
+// Two words at a uniform address, through the scalar cache: the vector memory counter stays the DMAs' own.
+__device__ __forceinline__ v2i scalar_load2(const int32_t* at) {
+  v2i r;
+  asm volatile("s_load_dwordx2 %0, %1, 0x0\n\ts_waitcnt lgkmcnt(0)" : "=&s"(r) : "s"(at) : "memory");
+  return r;
+}
+
 // OUT: 0 bf16, 1 fp16, 2 fp32.
 template <int WM, int WN, int MI, int NJ, bool GROUPED, int OUT>
 __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_kernel(MxArgs p) {
   constexpr int NW = WM * WN, TH = 64 * NW, BM = 32 * MI * WM, BN = 32 * NJ * WN;
+  // Grouped 256 x 256 tiles: one block per CU takes its XCD's items in turn, and fetches an item's first step while the last
+  // one's results leave (1024 tokens x 8 of 64 experts, 7168 x 2048: 174 us with a block per item, 160 so; 8192 tokens, 2048 x
+  // 7168: 593 and 592). The dense tile has no registers left for that.
+  constexpr bool STAY = GROUPED && MI * NJ > 4;
   constexpr int RA = BM * 8 / TH, RB = BN * 8 / TH;  // LDS DMAs of codes per thread and step
   constexpr int RS = ((BM + BN) / 64 + NW - 1) / NW; // of scales, every second step
   static_assert(BM % 64 == 0 && BN % 64 == 0, "a wave fetches scales of activations or of weights");
@@ -74,16 +85,22 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int h = lane >> 5, l32 = lane & 31;
-  int e = 0, tn, split = 0;
+  int e = 0, tn, mt = 0, split = 0;                  // mt: grouped: within the expert's rows
+  int length = 0, more = 0;                          // of the expert's segment; work items after this one
   int64_t r0, row_end, out0 = 0;                     // first row and end of this tile's rows (segment-local if grouped)
   if constexpr (GROUPED) {
     const Segment s = find_segment<BM>(p);
     if (s.e < 0) return;
-    e = s.e;
-    tn = s.tn;
-    r0 = (int64_t)s.mt * BM;
-    out0 = s.row0;
-    row_end = s.rows;
+    e = __builtin_amdgcn_readfirstlane(s.e);
+    tn = __builtin_amdgcn_readfirstlane(s.tn);
+    mt = __builtin_amdgcn_readfirstlane(s.mt);
+    out0 = __builtin_amdgcn_readfirstlane((int)s.row0);
+    row_end = __builtin_amdgcn_readfirstlane((int)s.rows);
+    if constexpr (STAY) {
+      const v2i o = scalar_load2(p.offsets + e);
+      length = o[1] - o[0];
+      more = __builtin_amdgcn_readfirstlane(s.left) / (int)(gridDim.x / 8);
+    }
   } else {
     const int t = xcd_remap((int)blockIdx.x, (int)gridDim.x), tiles = (int)p.tiles;   // below 2^24
     split = t / tiles;
@@ -91,11 +108,11 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
     // four row tiles at a time, column by column: the tiles that an XCD holds at once share rows and columns
     const int MT = tiles / p.NT, grp = tile / (4 * p.NT);
     const int rows = min(4, MT - 4 * grp), in = tile - grp * 4 * p.NT;
-    r0 = (int64_t)(4 * grp + in % rows) * BM;
+    mt = 4 * grp + in % rows;
     tn = in / rows;
     row_end = p.M;
   }
-  const int n0 = tn * BN;
+  r0 = (int64_t)mt * BM;
   const int k0 = p.KT * split / p.splits, k1 = p.KT * (split + 1) / p.splits;   // KT at most 2^14, splits 2^9
   const int64_t KH = p.K >> 1;                       // code bytes of a row
 
@@ -105,40 +122,46 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
   // token, and chunks past K, by an offset of their own. (The scalar part of an address never passes the buffer's size.)
   const int lrow = lane >> 3, lchunk = lane & 7;
   const bool gather = GROUPED && p.row_token;
-  const int64_t abase = gather ? 0 : out0 + r0;
-  const int64_t arows = gather ? p.M : (GROUPED ? min(min((int64_t)BM, row_end - r0), p.M - abase) : min((int64_t)BM, p.M - abase));
-  const __amdgpu_buffer_rsrc_t arsrc = make_rsrc(p.a + abase * KH, (uint32_t)max(arows * KH, (int64_t)0));
-  const __amdgpu_buffer_rsrc_t asr = make_rsrc(p.a_scale + abase * p.KS, (uint32_t)max(arows * p.KS, (int64_t)0));
-  const int64_t wrow0 = (int64_t)e * p.N + n0;
-  const int wrows = min(BN, p.N - n0);
-  const __amdgpu_buffer_rsrc_t wrsrc = make_rsrc(p.w + wrow0 * KH, (uint32_t)(wrows * KH));
-  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(p.w_scale + wrow0 * p.KS, (uint32_t)((int64_t)wrows * p.KS));
-  auto token = [&](int r) -> int {                   // gathered: activation row of tile row r; -1: none
-    if (r0 + r >= row_end) return -1;
-    const int t = p.row_token[out0 + r0 + r];
-    return (unsigned)t < (uint64_t)p.M ? t : -1;
-  };
+  __amdgpu_buffer_rsrc_t arsrc, asr, wrsrc, wsr;
   const int drow = 8 * wave + lrow;                  // + TH / 8 per load
   const int ca = lchunk ^ ((drow >> 1) & 7), cb = lchunk ^ (((drow >> 1) & 3) + 4 * ((drow >> 4) & 1));
   static_assert(TH / 8 % 32 == 0, "f repeats");
   const uint32_t KHu = (uint32_t)KH;
   const int klast = p.K - (p.KT - 1) * kMK;          // columns of the last step
   const bool a_dead = 32 * ca >= klast, b_dead = 32 * cb >= klast;   // the lane's chunk lies past K there
-  uint32_t a_off[RA], b_off[RB];
-#pragma unroll
-  for (int i = 0; i < RA; ++i) {
-    const int t = gather ? token((TH / 8) * i + drow) : (TH / 8) * i + drow;
-    a_off[i] = t >= 0 ? (uint32_t)t * KHu + 16 * ca : kPast;
-  }
+  uint32_t a_off[RA], b_off[RB], s_off[RS];
 #pragma unroll
   for (int i = 0; i < RB; ++i) b_off[i] = (uint32_t)((TH / 8) * i + drow) * KHu + 16 * cb;
-  uint32_t s_off[RS];
+  auto open = [&]() __attribute__((always_inline)) {   // the item's buffers and rows
+    const int64_t abase = gather ? 0 : out0 + r0;
+    const int64_t mine = GROUPED ? min((int64_t)BM, row_end - r0) : (int64_t)BM;
+    const int64_t arows = gather ? p.M : min(mine, p.M - abase);
+    const int64_t wrow0 = (int64_t)e * p.N + tn * BN;
+    const int wrows = min(BN, p.N - tn * BN);
+    arsrc = make_rsrc(p.a + abase * KH, (uint32_t)max(arows * KH, (int64_t)0));
+    asr = make_rsrc(p.a_scale + abase * p.KS, (uint32_t)max(arows * p.KS, (int64_t)0));
+    wrsrc = make_rsrc(p.w + wrow0 * KH, (uint32_t)(wrows * KH));
+    wsr = make_rsrc(p.w_scale + wrow0 * p.KS, (uint32_t)((int64_t)wrows * p.KS));
+    // gathered: activation row of tile row r; -1: none (no branch: all rows' loads are on their way together)
+    const int trows = (int)min((int64_t)BM, row_end - r0);
+    const __amdgpu_buffer_rsrc_t trs = make_rsrc(p.row_token + out0 + r0, (uint32_t)max(trows, 0) * 4);
+    auto token = [&](int r) -> int {
+      const int t = __builtin_amdgcn_raw_buffer_load_b32(trs, 4 * r, 0, 0);
+      return r < trows && (unsigned)t < (uint64_t)p.M ? t : -1;
+    };
 #pragma unroll
-  for (int i = 0; i < RS; ++i) {
-    const int r = 64 * (NW * i + wave) + lane;       // activation rows, then weight rows
-    const int t = 64 * (NW * i + wave) >= BM ? r - BM : (gather ? token(r) : r);
-    s_off[i] = t >= 0 ? (uint32_t)t * (uint32_t)p.KS : kPast;
-  }
+    for (int i = 0; i < RA; ++i) {
+      const int t = gather ? token((TH / 8) * i + drow) : (TH / 8) * i + drow;
+      a_off[i] = t >= 0 ? (uint32_t)t * KHu + 16 * ca : kPast;
+    }
+#pragma unroll
+    for (int i = 0; i < RS; ++i) {
+      const int r = 64 * (NW * i + wave) + lane;     // activation rows, then weight rows
+      const int t = 64 * (NW * i + wave) >= BM ? r - BM : (gather ? token(r) : r);
+      s_off[i] = t >= 0 ? (uint32_t)t * (uint32_t)p.KS : kPast;
+    }
+  };
+  open();
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const uint32_t ldsw = __builtin_amdgcn_readfirstlane(lds0 + 8 * wave * kMB);
   // m0 holds the LDS address. The compiler keeps nothing in it here, and a clobber of a reserved register is not honoured.
@@ -174,7 +197,8 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int q = 0; q < SZ; ++q) bias[j][q] = buffer_load16(brs, (uint32_t)(n0 + 32 * (NJ * wn + j) + 16 * h) * SZ + 16 * q);
+      for (int q = 0; q < SZ; ++q)
+        bias[j][q] = buffer_load16(brs, (uint32_t)(tn * BN + 32 * (NJ * wn + j) + 16 * h) * SZ + 16 * q);
   }
 
   // ---- fragments
@@ -203,147 +227,179 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
 #pragma unroll
     for (int q = 0; q < ND; ++q) gload1(k0, 0, q);
   }
-  v16f acc[MI][NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    v16f f;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      if constexpr (GROUPED) f[c] = 0.f;
-      else if constexpr (OUT == 2) f[c] = __int_as_float(bias[j][c / 4][c % 4]);
-      else {
-        const uint16_t b = (uint16_t)((uint32_t)bias[j][c / 8][c % 8 / 2] >> (16 * (c % 2)));
-        f[c] = OUT == 0 ? bf16_to_f32(b) : f16_to_f32(b);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < MI; ++i) acc[i][j] = f;
-  }
-  if (k0 < k1) {
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-#pragma unroll
-    for (int q = 0; q < RA + RB; ++q) gload1(k0 + 1, STAGE, q);
-    if (GROUPED && r0 + 32 * MI * wm >= row_end) {   // a wave whose rows all lie past the segment only fetches
-      for (int tk = k0; tk < k1 + ((k1 - k0) & 1); ++tk) {   // as many barriers as the others
-        asm volatile("s_barrier" ::: "memory");
-        const bool odd = (tk - k0) & 1;
-#pragma unroll
-        for (int q = 0; q < ND; ++q)
-          if (q < RA + RB || !odd) gload1(tk + 2, odd * STAGE, q);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"(RA + RB) : "memory");
-      }
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      return;
-    }
-    v4i af[4][MI], bf[4][NJ];
-    int sa[2][MI], sb[2][NJ];                        // by the step's parity
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      af[0][i] = afrag(0, i, 0);
-      sa[0][i] = scale(k0, ar + 32 * i);
-    }
+  for (;;) {                                         // a work item; its first step is on its way
+    v16f acc[MI][NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      bf[0][j] = bfrag(0, j, 0);
-      sb[0][j] = scale(k0, BM + br + 32 * j);
+      v16f f;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        if constexpr (GROUPED) f[c] = 0.f;
+        else if constexpr (OUT == 2) f[c] = __int_as_float(bias[j][c / 4][c % 4]);
+        else {
+          const uint16_t b = (uint16_t)((uint32_t)bias[j][c / 8][c % 8 / 2] >> (16 * (c % 2)));
+          f[c] = OUT == 0 ? bf16_to_f32(b) : f16_to_f32(b);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) acc[i][j] = f;
     }
-    // One step; P: its parity, and so its stage. No branch inside, and every MFMA is pinned where it stands (the empty
-    // statement names its result): left alone the compiler sinks all 64 behind the barrier and reads every fragment first.
-    auto step = [&](auto parity, int tk) __attribute__((always_inline)) {
-      constexpr int P = decltype(parity)::value;
-      constexpr uint32_t st = P * STAGE;
-      constexpr int NF = MI + NJ;
+    const bool idle = GROUPED && r0 + 32 * MI * wm >= row_end;   // a wave whose rows all lie past the segment only fetches
+    if (k0 < k1) {
+      asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c == 1) {
-          // every fragment of this step is in every wave's registers: its stage is free
-          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-          __builtin_amdgcn_sched_barrier(0);
+      for (int q = 0; q < RA + RB; ++q) gload1(k0 + 1, STAGE, q);
+      if (idle) {
+        for (int tk = k0; tk < k1 + ((k1 - k0) & 1); ++tk) {   // as many barriers as the others
+          asm volatile("s_barrier" ::: "memory");
+          const bool odd = (tk - k0) & 1;
+#pragma unroll
+          for (int q = 0; q < ND; ++q)
+            if (q < RA + RB || !odd) gload1(tk + 2, odd * STAGE, q);
+          asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"(RA + RB) : "memory");
         }
-        if (c == 3) {
-          // the next step's tiles have landed (what was issued since is the step after's)
-          asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"(RA + RB + (P == 0 && NW * 64 * RS == BM + BN ? RS : 0)) : "memory");
-          __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      } else {
+        v4i af[4][MI], bf[4][NJ];
+        int sa[2][MI], sb[2][NJ];                        // by the step's parity
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          af[0][i] = afrag(0, i, 0);
+          sa[0][i] = scale(k0, ar + 32 * i);
         }
 #pragma unroll
-        for (int n = 0; n < NM; ++n) {
-          const int i = n / NJ, j = n % NJ;
-          if (c == 0) {                              // groups 1 to 3's fragments
+        for (int j = 0; j < NJ; ++j) {
+          bf[0][j] = bfrag(0, j, 0);
+          sb[0][j] = scale(k0, BM + br + 32 * j);
+        }
+        // One step; P: its parity, and so its stage. No branch inside, and every MFMA is pinned where it stands (the empty
+        // statement names its result): left alone the compiler sinks all 64 behind the barrier and reads every fragment first.
+        auto step = [&](auto parity, int tk) __attribute__((always_inline)) {
+          constexpr int P = decltype(parity)::value;
+          constexpr uint32_t st = P * STAGE;
+          constexpr int NF = MI + NJ;
 #pragma unroll
-            for (int q = n * 3 * NF / NM; q < (n + 1) * 3 * NF / NM; ++q) {
-              if (q % NF < NJ) bf[1 + q / NF][q % NF] = bfrag(st, q % NF, 1 + q / NF);
-              else af[1 + q / NF][q % NF - NJ] = afrag(st, q % NF - NJ, 1 + q / NF);
+          for (int c = 0; c < 4; ++c) {
+            if (c == 1) {
+              // every fragment of this step is in every wave's registers: its stage is free
+              asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+              __builtin_amdgcn_sched_barrier(0);
             }
-          }
-          if (c == 3) {                              // the next step's group 0 (at the end: of a stage whose contents are not used)
+            if (c == 3) {
+              // the next step's tiles have landed (what was issued since is the step after's)
+              asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier"
+                           :: "n"(RA + RB + (P == 0 && NW * 64 * RS == BM + BN ? RS : 0)) : "memory");
+              __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
-            for (int q = n * NF / NM; q < (n + 1) * NF / NM; ++q) {
-              if (q < NJ) {
-                bf[0][q] = bfrag(STAGE - st, q, 0);
-                sb[1 - P][q] = scale(tk + 1, BM + br + 32 * q);
-              } else {
-                af[0][q - NJ] = afrag(STAGE - st, q - NJ, 0);
-                sa[1 - P][q - NJ] = scale(tk + 1, ar + 32 * (q - NJ));
+            for (int n = 0; n < NM; ++n) {
+              const int i = n / NJ, j = n % NJ;
+              if (c == 0) {                              // groups 1 to 3's fragments
+#pragma unroll
+                for (int q = n * 3 * NF / NM; q < (n + 1) * 3 * NF / NM; ++q) {
+                  if (q % NF < NJ) bf[1 + q / NF][q % NF] = bfrag(st, q % NF, 1 + q / NF);
+                  else af[1 + q / NF][q % NF - NJ] = afrag(st, q % NF - NJ, 1 + q / NF);
+                }
               }
+              if (c == 3) {                          // the next step's group 0 (at the end: of a stage that is not used)
+#pragma unroll
+                for (int q = n * NF / NM; q < (n + 1) * NF / NM; ++q) {
+                  if (q < NJ) {
+                    bf[0][q] = bfrag(STAGE - st, q, 0);
+                    sb[1 - P][q] = scale(tk + 1, BM + br + 32 * q);
+                  } else {
+                    af[0][q - NJ] = afrag(STAGE - st, q - NJ, 0);
+                    sa[1 - P][q - NJ] = scale(tk + 1, ar + 32 * (q - NJ));
+                  }
+                }
+              }
+              if (c == 0) acc[i][j] = mx_mfma<0>(bf[0][j], af[0][i], acc[i][j], sb[P][j], sa[P][i]);
+              if (c == 1) acc[i][j] = mx_mfma<1>(bf[1][j], af[1][i], acc[i][j], sb[P][j], sa[P][i]);
+              if (c == 2) acc[i][j] = mx_mfma<2>(bf[2][j], af[2][i], acc[i][j], sb[P][j], sa[P][i]);
+              if (c == 3) acc[i][j] = mx_mfma<3>(bf[3][j], af[3][i], acc[i][j], sb[P][j], sa[P][i]);
+              asm volatile("" : "+a"(acc[i][j]));
+              if (c == 1) {
+                constexpr int NDP = P == 0 ? ND : RA + RB;
+#pragma unroll
+                for (int q = n * NDP / NM; q < (n + 1) * NDP / NM; ++q) gload1(tk + 2, st, q);
+              }
+              __builtin_amdgcn_sched_barrier(0);
             }
           }
-          if (c == 0) acc[i][j] = mx_mfma<0>(bf[0][j], af[0][i], acc[i][j], sb[P][j], sa[P][i]);
-          if (c == 1) acc[i][j] = mx_mfma<1>(bf[1][j], af[1][i], acc[i][j], sb[P][j], sa[P][i]);
-          if (c == 2) acc[i][j] = mx_mfma<2>(bf[2][j], af[2][i], acc[i][j], sb[P][j], sa[P][i]);
-          if (c == 3) acc[i][j] = mx_mfma<3>(bf[3][j], af[3][i], acc[i][j], sb[P][j], sa[P][i]);
-          asm volatile("" : "+a"(acc[i][j]));
-          if (c == 1) {
-            constexpr int NDP = P == 0 ? ND : RA + RB;
-#pragma unroll
-            for (int q = n * NDP / NM; q < (n + 1) * NDP / NM; ++q) gload1(tk + 2, st, q);
-          }
-          __builtin_amdgcn_sched_barrier(0);
+        };
+        for (int tk = k0; tk < k1; tk += 2) {            // an odd number's last step adds zeros
+          step(std::integral_constant<int, 0>{}, tk);
+          step(std::integral_constant<int, 1>{}, tk + 1);
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       }
-    };
-    for (int tk = k0; tk < k1; tk += 2) {            // an odd number's last step adds zeros
-      step(std::integral_constant<int, 0>{}, tk);
-      step(std::integral_constant<int, 1>{}, tk + 1);
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  }
 
-  // ---- output. A lane's results are 16 columns of one row, which as stores would be half a cache line from each of 32
-  // rows; 32 rows at a time go through the wave's own LDS and leave as whole rows. Chunk c (16 bytes) of row r lies at c ^
-  // f(r), so that 16 lanes that write one chunk of 16 rows, or read 16 of a row, fill the banks.
-  constexpr int CH = 32 * NJ * SZ / 16, PER = 16 / SZ;   // chunks of a row, columns of a chunk
-  static_assert(CH >= 8 && NW * 32 * CH * 16 <= 2 * STAGE, "the waves' rows fit the stages");
-  auto swizzle = [](int r) { return CH == 8 ? (r >> 1) & 7 : r & 15; };
-  __syncthreads();                                   // no wave's tiles are on their way any more
-  uint8_t* mine = lds + wave * (32 * CH * 16);
-  const int nw = n0 + 32 * NJ * wn;
-  const int col = nw + PER * (lane % CH), row = lane / CH;
-  constexpr int RPI = 64 / CH;                       // rows of a store
-  const int left = col < p.N ? (int)min((int64_t)BM, row_end - r0) : 0;
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-#pragma unroll
-      for (int q = 0; q < SZ; ++q) {                 // SZ chunks of the lane's 16 columns
-        v4i w;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if constexpr (OUT == 2) w[c] = __float_as_int(acc[i][j][4 * q + c]);
-          else w[c] = pack16<OUT>(acc[i][j][8 * q + 2 * c], acc[i][j][8 * q + 2 * c + 1]);
+    // ---- output. A lane's results are 16 columns of one row, which as stores would be half a cache line from each of 32
+    // rows; 32 rows at a time go through the wave's own LDS and leave as whole rows. Chunk c (16 bytes) of row r lies at c ^
+    // f(r), so that 16 lanes that write one chunk of 16 rows, or read 16 of a row, fill the banks.
+    constexpr int CH = 32 * NJ * SZ / 16, PER = 16 / SZ;   // chunks of a row, columns of a chunk
+    constexpr uint32_t ROWS = STAY ? STAGE : 0;        // where: the first stage takes the next item's first step
+    static_assert(CH >= 8 && ROWS + NW * 32 * CH * 16 <= 2 * STAGE, "the waves' rows fit the stages");
+    auto swizzle = [](int r) { return CH == 8 ? (r >> 1) & 7 : r & 15; };
+    __syncthreads();                                   // no wave's tiles are on their way any more
+    uint8_t* mine = lds + ROWS + wave * (32 * CH * 16);
+    const int nw = tn * BN + 32 * NJ * wn;
+    const int col = nw + PER * (lane % CH), row = lane / CH;
+    constexpr int RPI = 64 / CH;                       // rows of a store
+    const int left = col < p.N ? (int)min((int64_t)BM, row_end - r0) : 0;
+    const int64_t row0 = out0 + r0 + (int64_t)split * p.M;
+    const bool last = !STAY || more == 0;
+    if constexpr (STAY) {
+      if (!last) {                                   // the next item; its first step comes while this one's results leave
+        --more;
+        tn += (int)(gridDim.x / 8);
+        while (tn >= p.NT) {
+          tn -= p.NT;
+          ++mt;
+          while (mt * BM >= length && e + 1 < p.E) {
+            ++e;
+            mt = 0;
+            const v2i o = scalar_load2(p.offsets + e);
+            out0 = o[0];
+            length = o[1] - o[0];
+            row_end = min((int64_t)length, p.R - out0);
+          }
         }
-        *reinterpret_cast<v4i*>(mine + (l32 * CH + ((2 * j + h) * SZ + q ^ swizzle(l32))) * 16) = w;
+        r0 = (int64_t)mt * BM;
+        open();
+#pragma unroll
+        for (int q = 0; q < ND; ++q) gload1(k0, 0, q);
       }
     }
-    const int first = 32 * (MI * wm + i) + row;      // of the tile's rows
-    uint8_t* o = static_cast<uint8_t*>(p.out) + ((out0 + r0 + first + (int64_t)split * p.M) * p.N + col) * SZ;
+    if (!idle) {
 #pragma unroll
-    for (int k = 0; k < 32 / RPI; ++k) {
-      const int rr = row + RPI * k;
-      const v4i w = *reinterpret_cast<const v4i*>(mine + (rr * CH + (lane % CH ^ swizzle(rr))) * 16);
-      if (first + RPI * k < left) *reinterpret_cast<v4i*>(o) = w;
-      o += (int64_t)RPI * p.N * SZ;
+      for (int i = 0; i < MI; ++i) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+          for (int q = 0; q < SZ; ++q) {                 // SZ chunks of the lane's 16 columns
+            v4i w;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if constexpr (OUT == 2) w[c] = __float_as_int(acc[i][j][4 * q + c]);
+              else w[c] = pack16<OUT>(acc[i][j][8 * q + 2 * c], acc[i][j][8 * q + 2 * c + 1]);
+            }
+            *reinterpret_cast<v4i*>(mine + (l32 * CH + ((2 * j + h) * SZ + q ^ swizzle(l32))) * 16) = w;
+          }
+        }
+        const int first = 32 * (MI * wm + i) + row;      // of the tile's rows
+        uint8_t* o = static_cast<uint8_t*>(p.out) + ((row0 + first) * p.N + col) * SZ;
+#pragma unroll
+        for (int k = 0; k < 32 / RPI; ++k) {
+          const int rr = row + RPI * k;
+          const v4i w = *reinterpret_cast<const v4i*>(mine + (rr * CH + (lane % CH ^ swizzle(rr))) * 16);
+          if (first + RPI * k < left) *reinterpret_cast<v4i*>(o) = w;
+          o += (int64_t)RPI * p.N * SZ;
+        }
+      }
     }
+    if (last) break;
   }
 }
 
@@ -355,7 +411,7 @@ struct MxPlan {
 // Streaming reads the weights once per 16 rows, mostly from L2, and needs no second launch: 64 rows of 4096 x 4096 7.1 us
 // (tiles 10.2), of 4096 x 14336 12.7 (13.4), of 14336 x 4096 11.8 (10.6). Above that the cheapest by a model of what was
 // measured: a launch, steps of 256 columns (slower where two blocks share a CU), and for splits a second launch that adds
-// the parts. It comes within 10% of the measured times from 65 to 1024 rows of the sizes above, of 1024 x 4096 and of
+// the parts. It comes within 20% of the measured times from 65 to 1024 rows of the sizes above, of 1024 x 4096 and of
 // 7168 x 2048, and takes the fastest plan or one within 5% of it. For instance 128 rows of 14336 x 4096: 11.8 us in tiles of
 // 64 x 128, 13.7 of 128 x 128, 28 of 256 x 256; 200 rows of 4096 x 14336: 20.3 in 4 splits of 128 x 128, 22.2 in 4 of 64 x
 // 128, 76 in tiles of 256 x 256; 1024 rows of 14336 x 4096: 37.9 in tiles of 256 x 256, 45.2 of 128 x 128.
@@ -408,7 +464,9 @@ template <int BM, int BN, typename F>
 static hipError_t tile_go(MxArgs p, F kernel, hipStream_t stream) {
   p.NT = (p.N + BN - 1) / BN;
   p.tiles = (p.M + BM - 1) / BM * p.NT;
-  const dim3 grid((unsigned)(p.offsets ? grouped_blocks(p.E, p.R, p.N, BM, BN) : p.tiles * p.splits)), block(256);
+  int64_t blocks = p.offsets ? grouped_blocks(p.E, p.R, p.N, BM, BN) : p.tiles * p.splits;
+  if (p.offsets && BM == 256) blocks = blocks < 256 ? blocks : 256;   // they stay
+  const dim3 grid((unsigned)blocks), block(256);
   hipLaunchKernelGGL(kernel, grid, block, 0, stream, p);
   return hipGetLastError();
 }
