@@ -483,17 +483,19 @@ def _current_device() -> int:
     return torch._C._cuda_getDevice()
 
 
-def _on_current_device(stream, *tensors) -> None:
-    """A launch goes to the current device, whatever memory it is given: refuses tensors or a stream of another one."""
-    here = None
-    for t in tensors:
-        if t is not None and t.is_cuda:
-            if here is None:
-                here = _current_device()
-                if stream is not None and stream.device_index != here:
-                    raise ValueError(f"the stream is of cuda:{stream.device_index}, the current device is cuda:{here}")
-            if t.get_device() != here:
-                raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{here}")
+def _on_current_device(stream, first, *others) -> None:
+    """A launch goes to the current device, whatever memory it is given: refuses tensors or a stream of another one. (One
+    that is not on a GPU is refused for that.)"""
+    here = first.get_device()
+    if here < 0:
+        return
+    if here != _current_device():
+        raise ValueError(f"a tensor is on cuda:{here}, the current device is cuda:{_current_device()}")
+    if stream is not None and stream.device_index != here:
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, the current device is cuda:{here}")
+    for t in others:
+        if t is not None and t.get_device() != here and t.is_cuda:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{here}")
 
 
 def _e4m3_codes(t, what: str):
