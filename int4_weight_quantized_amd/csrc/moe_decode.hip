@@ -660,7 +660,7 @@ size_t moe_workspace(int64_t T, int64_t E, int64_t topk, int64_t I) {
 
 template <int FMT, bool F16, int NX, int NM, int WD, int NJ>
 static hipError_t moe_stream(const MoeArgs& p, int64_t tiles, hipStream_t stream) {
-  constexpr int WU = 4;
+  constexpr int WU = 4;                              // (2, 3 and 8 waves: within 5%)
   // Blocks of the first kernel that route for themselves do so once, for several column tiles each: at most 4 blocks per CU,
   // equally many tiles for each (2 tokens of 64 experts, int4: 55 us with a tile per block, 50 so). Where a kernel before
   // it routes, a tile per block is as fast or faster (32 tokens FP8: 314 us; 1024 blocks, 326).

@@ -27,7 +27,8 @@
 //   16 (q / 4 % 2) + 4 (q / 8) + q % 4, which gives a lane 16 consecutive ones.
 // - Results leave through LDS as whole rows: straight from the registers a store
 //   would be half a cache line of each of 32 rows (154 us, 151 so).
-// What bounds it: 4096 x 14336 x 4096 takes 144 us, 3.3 PFLOP/s, K = 16384 reaches
+// What bounds it: 4096 x 14336 x 4096 takes 144 us (up to 170 on cards whose clock
+// the power limit holds lower), 3.3 PFLOP/s, K = 16384 reaches
 // 4.1, where the fp4 matrix rate alone is 8.4. Each round of tiles ends in a
 // burst of stores that memory takes 7 us for and nothing overlaps (about 30 of the
 // 144 us, from the times of K = 512 to 16384); within the loop a step of 256 columns takes 2.1 us, at a clock that the
