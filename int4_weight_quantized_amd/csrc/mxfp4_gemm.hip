@@ -35,6 +35,7 @@
 // power limit holds near 1.6 GHz there; without its DMA it takes 1.4, and with a
 // quarter of its MFMAs 1.1 (measured at shorter K, where the clock is higher and the
 // whole step takes 1.8).
+#include <cmath>
 #include <type_traits>
 
 #include "mxfp4.h"
@@ -70,7 +71,7 @@ __device__ __forceinline__ v2i scalar_load2(const int32_t* at) {
 template <int WM, int WN, int MI, int NJ, bool GROUPED, int OUT>
 __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_kernel(MxArgs p) {
   constexpr int NW = WM * WN, TH = 64 * NW, BM = 32 * MI * WM, BN = 32 * NJ * WN;
-  // Grouped 256 x 256 tiles: one block per CU takes its XCD's items in turn, and fetches an item's first step while the last
+  // Grouped tiles of 192 and 256 rows: one block per CU takes its XCD's items in turn, and fetches an item's first step while the last
   // one's results leave (1024 tokens x 8 of 64 experts, 7168 x 2048: 174 us with a block per item, 160 so; 8192 tokens, 2048 x
   // 7168: 593 and 592). The dense tile has no registers left for that.
   constexpr bool STAY = GROUPED && MI * NJ > 4;
@@ -466,7 +467,7 @@ static hipError_t tile_go(MxArgs p, F kernel, hipStream_t stream) {
   p.NT = (p.N + BN - 1) / BN;
   p.tiles = (p.M + BM - 1) / BM * p.NT;
   int64_t blocks = p.offsets ? grouped_blocks(p.E, p.R, p.N, BM, BN) : p.tiles * p.splits;
-  if (p.offsets && BM == 256) blocks = blocks < 256 ? blocks : 256;   // they stay
+  if (p.offsets && BM > 128) blocks = blocks < 256 ? blocks : 256;   // they stay
   const dim3 grid((unsigned)blocks), block(256);
   hipLaunchKernelGGL(kernel, grid, block, 0, stream, p);
   return hipGetLastError();
@@ -531,23 +532,33 @@ hipError_t launch_mx_gemm(const void* a, const void* a_scale, const void* w, con
   return hipGetLastError();
 }
 
+// Row tiles of bm that an expert takes, if its rows spread about their mean as by chance.
+static double tiles_of(double mean, int bm) {
+  double t = 1.0;
+  for (int j = 1; j * bm < mean + 4.0 * std::sqrt(mean); ++j) t += 0.5 * std::erfc((j * bm - mean) / std::sqrt(2.0 * mean));
+  return t;
+}
+
 // What the grouped product runs as: rows streamed (0), or the tile's rows. By rows per expert; measured with 64 experts of
-// 4096 x 7168: 4 rows 162 us streamed, 168 in tiles of 64 x 128, 176 of 128 x 128; 16 rows 224, 182 and 187; 64 rows (-), 258
-// and 210, 229 of 256 x 256; 128 rows (-, -), 292 and 251. Of 7168 x 2048, whose K leaves a wave two steps, tiles win from the
-// start: 4 rows 104, 96 and 100. Few tiles of 256 would leave CUs idle, or their last column tile be mostly empty.
+// 4096 x 7168 (us): 4 rows 162 streamed, 168 in tiles of 64 x 128, 176 of 128 x 128; 16 rows 224, 182 and 187; 48 rows 211 and
+// 202, 199 of 192 x 256; 96 rows (-), 229, 222, and 235 of 256 x 256; 128 rows (-), 289, 240 and 263; 256 rows (-), 456, 433
+// and 394; 320 rows (-), 545, 455 and 513. Of 7168 x 2048, whose K leaves a streaming wave two steps, tiles win from the
+// start (4 rows 104, 96 and 100) and those of 128 up to 112 rows (138, of 192 147). A tile of 192 rows costs about 0.87 of one
+// of 256. Few of the larger tiles would leave CUs idle, or their last column tile be mostly empty.
 static int plan_grouped(int64_t E, int64_t R, int64_t N, int64_t K) {
   if (R <= 8 * E && K >= 4096) return 0;
   if (R <= 32 * E) return 64;
   const int64_t c256 = (N + 255) / 256, c128 = (N + 127) / 128;
-  if (R <= 96 * E || (R / 256 + E / 2) * c256 < 160 || 3 * 2 * c256 > 4 * c128) return 128;
-  return 256;
+  if (R <= (K < 6144 ? 104 : 48) * E || (R / 256 + E / 2) * c256 < 160 || 3 * 2 * c256 > 4 * c128) return 128;
+  const double mean = (double)R / (double)E;
+  return mean <= 2048 && 0.87 * tiles_of(mean, 192) < tiles_of(mean, 256) ? 192 : 256;
 }
 
 int64_t mx_grouped_threads(int64_t E, int64_t R, int64_t N, int64_t K) {
   if (R == 0 || N == 0 || E == 0) return 0;
   const int tile = plan_grouped(E, R, N, K);
   if (tile == 0) return mx_stream_threads(0, N, E, R);
-  return grouped_blocks(E, R, N, tile, tile == 256 ? 256 : 128) * 256;
+  return grouped_blocks(E, R, N, tile, tile > 128 ? 256 : 128) * 256;
 }
 
 hipError_t launch_mx_grouped(const void* a, const void* a_scale, const int32_t* row_token, const int32_t* offsets,
@@ -567,6 +578,9 @@ hipError_t launch_mx_grouped(const void* a, const void* a_scale, const int32_t* 
   if (tile == 128)
     return out_dt == 0 ? tile_go<128, 128>(p, mx_tile_kernel<2, 2, 2, 2, true, 0>, stream)
                        : tile_go<128, 128>(p, mx_tile_kernel<2, 2, 2, 2, true, 1>, stream);
+  if (tile == 192)
+    return out_dt == 0 ? tile_go<192, 256>(p, mx_tile_kernel<2, 2, 3, 4, true, 0>, stream)
+                       : tile_go<192, 256>(p, mx_tile_kernel<2, 2, 3, 4, true, 1>, stream);
   return out_dt == 0 ? tile_go<256, 256>(p, mx_tile_kernel<2, 2, 4, 4, true, 0>, stream)
                      : tile_go<256, 256>(p, mx_tile_kernel<2, 2, 4, 4, true, 1>, stream);
 }

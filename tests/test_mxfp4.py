@@ -236,7 +236,7 @@ def segments(r, E, R, kind):
 
 
 @pytest.mark.parametrize("E,R,N,K", [(1, 1, 8, 32), (8, 8, 136, 96), (64, 64, 264, 288), (4, 100, 136, 160), (8, 700, 264, 416),
-                                     (3, 1000, 520, 224), (4, 5600, 2056, 288), (6, 9000, 2056, 288), (64, 64, 264, 4128), (3, 20, 136, 4256)])
+                                     (3, 1000, 520, 224), (4, 5600, 2056, 288), (6, 9000, 2056, 288), (16, 2500, 4104, 288), (64, 64, 264, 4128), (3, 20, 136, 4256)])
 @pytest.mark.parametrize("kind", ["even", "one", "ragged"])
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_grouped(E, R, N, K, kind, dt):
