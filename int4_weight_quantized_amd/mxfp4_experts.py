@@ -19,7 +19,9 @@ class Mxfp4Experts:
     """w13 uint8 [E, 2 I, H / 2] (gate rows, then up rows) and w2 [E, H, I / 2] codes, w13_scale uint8
     [E, 2 I, 4 ceil(H / 128)] and w2_scale [E, H, 4 ceil(I / 128)], as ops.w4_mxfp4_quantize lays them out. `routing` goes
     to ops.w4_route (score, bias, n_groups, ...). Up to `decode_tokens` tokens (at most W4_MOE_DECODE_MAX_TOKENS) take the
-    one call; its activations are not quantized, so the two paths differ by the quantization."""
+    one call; its activations are not quantized, so the two paths differ by the quantization. (64 experts of 7168 x
+    2048, 8 chosen: 1 token 41 us in one call and 55 in stages, 8 tokens 178 and 195, 24 tokens 268 and 272, 32 tokens 292
+    and 280.)"""
 
     def __init__(self, w13, w13_scale, w2, w2_scale, topk: int, max_tokens: int, dtype=torch.bfloat16,
                  decode_tokens: int = ops.W4_MOE_DECODE_MAX_TOKENS, **routing):
