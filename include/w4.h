@@ -742,9 +742,8 @@ int w4_mxfp4_grouped_gemm(const void* a, const void* a_scale, const int32_t* row
  * from the same arguments:
  *   out[t] = sum_j weights[t, j] * W2[e] (silu(W1[e] x[t]) * (W3[e] x[t]))  (+ add[t]),
  *   e = ids[t, j]; an id of -1 adds nothing
- * Products and sums in fp32; between the two products the gated rows (times their
- * routing weight) are held to 16 bits of mantissa; one rounding to the output
- * type at the end. Two kernels up to 2 tokens of 256 experts, three above.
+ * Products, sums and, between the two products, the gated rows (times their routing
+ * weight) in fp32; one rounding to the output type at the end. Two kernels up to 2 tokens of 256 experts, three above.
  *   x        device, [T, H] contiguous, bf16 or fp16;  add: device or NULL, [T, H];
  *            out: device, [T, H], all x_dtype and 16-byte aligned; out may be add
  *   logits .. scale  as w4_route

@@ -11,7 +11,7 @@
 // tokens are routed by a block before it.
 //
 // The plan: pairs (token, expert) are rows, ordered by expert, then token. Tiles
-// of at most 8 (gate and up) or 4 or 8 (down) rows of an expert name it, their
+// of at most 8 (gate and up) or 4 or 5 (down) rows of an expert name it, their
 // first row and their tokens as bits.
 //
 // Both kernels stream weights through the matrix unit, 16 weight rows as its A
@@ -22,18 +22,18 @@
 // What a wave reads passes through LDS of its own (lds_weights.h): rows lie there with their 16-byte chunks permuted by the
 // row, so that the reads of 8 rows touch 8 different chunks.
 //
-// What lies between the two is held to 16 bits of mantissa as the sum of two bf16
-// numbers (2^-17 relative, below what the output's own rounding leaves visible).
-// The matrix unit takes them in one go: columns 0..7 are 8 rows' first numbers,
-// columns 8..15 their second ones, added at the end. MXFP4 with fp16 activations
-// takes x apart in the same way, exactly (11 bits).
+// What lies between the two stays fp32: it is held as the sum of three bf16 numbers,
+// 8 bits of mantissa each, exactly. The matrix unit takes them in one go: of its 16
+// columns the first are a tile's rows' first numbers, the next ones their second and
+// third ones, added at the end; hence tiles of at most 5 rows. MXFP4 with fp16
+// activations takes x apart in two such numbers, exactly (11 bits).
 //
-// 64 experts, 8 chosen, 7168 x 2048, kernels only: one token FP8 47 + 23 us (5.1 TB/s
-// of weights); two tokens int4 50 + 26; 8 tokens MXFP4 9 + 114 + 58 (5.6 and 5.5
-// TB/s); 32 tokens FP8 13 + 315 + 159 (5.9 and 5.8). What bounds them is memory and,
-// with many rows, the activations and the middle, which every block reads from L2:
-// without those reads the down products of 32 tokens took 184 us where they took
-// 224 at the time.
+// 64 experts, 8 chosen, 7168 x 2048, kernels only (medians): one token FP8 47 + 23 us
+// (5.1 TB/s of weights); two tokens int4 52 + 29; 8 tokens MXFP4 7 + 114 + 65; 32
+// tokens FP8 13 + 320 + 204, MXFP4 13 + 194 + 152. What bounds them is memory and, with
+// many rows, the activations and the middle, which every block reads from L2: with a
+// middle of two bf16 numbers (16 bits) and so tiles of 8 rows the down products took
+// 59 us for 8 tokens, 170 and 121 for 32.
 #include <type_traits>
 
 #include "lds_weights.h"
@@ -44,7 +44,10 @@ namespace w4 {
 constexpr int kInline = 2;                           // tokens that the first kernel routes itself
 constexpr int kInlineE = 256;
 constexpr int kInlineRows = kInline * 64;
-constexpr int kUpRows = 8, kFewRows = 4;             // most rows of a tile (down: kUpRows where experts hold many)
+constexpr int kUpRows = 8, kFewRows = 4, kDownRows = 5;   // most rows of a tile: up, down, down where experts hold many
+constexpr int kParts = 3;                            // bf16 numbers of a value of the middle
+constexpr int kMaxT = 32, kMaxTopk = 64;             // the host lets no more through
+constexpr size_t kLds = 160 * 1024;                  // of a CU
 
 struct MoeTile {
   uint16_t e, row0;
@@ -67,7 +70,7 @@ struct MoeArgs {
   int32_t* counts;                                   // tiles of the first kernel, of the second
   MoeTile *up, *down;
   float* weights;                                    // of the rows
-  uint16_t* mid;                                     // [2][R][I]: the middle, as two bf16
+  uint16_t* mid;                                     // [kParts][R][I]: the middle
   RouteArgs route;
 };
 
@@ -455,29 +458,39 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
       }
     }
     if (l16 >= 8 || !mine) continue;
-    uint32_t hi[4], lo[4];
+    uint32_t part[kParts][4];                        // the upper 8 bits of mantissa, of what is left the next 8, the last 8
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float m = vg[q] / (1.0f + expf(-vg[q])) * vu[q] * weight;
-      hi[q] = f32_to_bf16_rne(m);
-      const float rest = m - __uint_as_float(hi[q] << 16);
-      lo[q] = (hi[q] & 0x7F80u) != 0x7F80u ? f32_to_bf16_rne(rest) : 0u;   // (an infinity has no remainder)
+      float m = vg[q] / (1.0f + expf(-vg[q])) * vu[q] * weight;
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        part[k][q] = __float_as_uint(m) & 0xFFFF0000u;
+        // (an infinity or a NaN, whose quiet bit the upper half holds, leaves no remainder)
+        m = (part[k][q] & 0x7F800000u) != 0x7F800000u ? m - __uint_as_float(part[k][q]) : 0.f;
+      }
     }
     uint16_t* o = p.mid + (int64_t)(tile.row0 + row) * p.I + n0 + 4 * g;
-    *reinterpret_cast<v2i*>(o) = v2i{(int)(hi[0] | hi[1] << 16), (int)(hi[2] | hi[3] << 16)};
-    *reinterpret_cast<v2i*>(o + (int64_t)p.T * p.topk * p.I) = v2i{(int)(lo[0] | lo[1] << 16), (int)(lo[2] | lo[3] << 16)};
+#pragma unroll
+    for (int k = 0; k < kParts; ++k)
+      *reinterpret_cast<v2i*>(o + k * ((int64_t)p.T * p.topk * p.I)) =
+          v2i{(int)(part[k][0] >> 16 | part[k][1]), (int)(part[k][2] >> 16 | part[k][3])};
   }
 }
 
+// DMAs of a step's middle.
+template <int FMT, int ROWS>
+constexpr int kMidDmas = (kParts * ROWS + kRowsPerDma<FMT> - 1) / kRowsPerDma<FMT>;
+
 // Down: a block owns 16 NJ output columns of all tokens; its waves share the (tile, step) pairs, each a run of them. At a
 // tile's end a wave adds its sums to its own place in LDS by token: no token takes anything of an expert that it did not
-// choose, and the order is fixed. NM: DMAs of a step's middle (row r's first numbers as row 2 r, its second as 2 r + 1).
-template <int FMT, bool F16OUT, int NM, int WS, int NJ>
+// choose, and the order is fixed. ROWS: most rows of a tile; number k of row r is row 3 r + k of a step's middle in LDS, and
+// column ROWS k + r of the products.
+template <int FMT, bool F16OUT, int ROWS, int WS, int NJ>
 __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
   constexpr int COLS = kCols<FMT>, HALVES = FMT == kFp8 ? 1 : 2;
   using S = Scales<FMT, NJ>;
-  constexpr int kX = 2048 * NJ, kSlot = kX + 1024 * NM;
-  constexpr int kMost = kRowsPerDma<FMT> * NM / 2;   // rows that fit
+  constexpr int NM = kMidDmas<FMT, ROWS>, kX = 2048 * NJ, kSlot = kX + 1024 * NM;
+  static_assert(kParts * ROWS <= 16, "the parts of a tile's rows are columns of one product");
   __shared__ __attribute__((aligned(16))) uint8_t room[WS][kSlot], room_scales[WS][S::kBytes];
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   v4f* sum = reinterpret_cast<v4f*>(smem);           // [WS][T][4 NJ]
@@ -489,7 +502,7 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
   for (int i = tid; i < tiles; i += 64 * WS) list[i] = p.down[i];
   for (int i = tid; i < WS * p.T * 4 * NJ; i += 64 * WS) sum[i] = v4f{0.f, 0.f, 0.f, 0.f};
   const int64_t plane = (int64_t)p.T * p.topk * p.I * 2;
-  const __amdgpu_buffer_rsrc_t mr = make_rsrc(p.mid, (uint32_t)(2 * plane));
+  const __amdgpu_buffer_rsrc_t mr = make_rsrc(p.mid, (uint32_t)(kParts * plane));
   __syncthreads();
   v4f* mine = sum + wave * p.T * 4 * NJ;
   const int i0 = (int)((int64_t)steps * wave / WS), i1 = (int)((int64_t)steps * (wave + 1) / WS);
@@ -500,7 +513,7 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
 #pragma unroll
   for (int j = 0; j < NM; ++j) {
     const int r = act_row<FMT>(j, lane), col = act_column<FMT>(r, lane);
-    mo[j] = (uint32_t)((int64_t)(r >> 1) * p.I * 2 + 2 * col + (r & 1) * plane);
+    mo[j] = (uint32_t)((int64_t)(r / kParts) * p.I * 2 + 2 * col + r % kParts * plane);
     mdead[j] = col >= p.I - (KT - 1) * COLS;
   }
   // the tile and step that are fetched next, and those that are computed
@@ -524,8 +537,8 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
     for (int j = 0; j < NJ; ++j) w[j].fetch(fk, last, to + 2048 * j);
 #pragma unroll
     for (int j = 0; j < NM; ++j)                     // (rows that the tile does not have: whatever lies there, not stored)
-      if (kRowsPerDma<FMT> * j < 2 * rows)
-        dma16(mr, to + kX + 1024 * j, (act_row<FMT>(j, lane) >> 1) >= rows || (last && mdead[j]) ? kPast : mo[j] + row0,
+      if (kRowsPerDma<FMT> * j < kParts * rows)
+        dma16(mr, to + kX + 1024 * j, act_row<FMT>(j, lane) / kParts >= rows || (last && mdead[j]) ? kPast : mo[j] + row0,
               (uint32_t)fk * (2 * COLS));
     if (first || S::begins(fk)) sc.fetch(fk, to_scales, lane);
     if (++fk == KT) {
@@ -544,7 +557,7 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
     sc.lane(p.H, n0, 16, p.I, p.kg2, lane);
     open_tile();
     fetch(true);
-    const int mrow = (2 * (l16 & 7) + (l16 >> 3)) & (2 * kMost - 1);
+    const int mrow = l16 < kParts * ROWS ? l16 % ROWS * kParts + l16 / ROWS : 0;   // (columns past the parts: not used)
     for (int i = i0; i < i1; ++i) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       v4i qw[NJ][2], M[HALVES][4];
@@ -598,12 +611,14 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
       }
       if (++ck == KT || i == i1 - 1) {               // the tile's last step here
         const MoeTile tile = list[ct];
-        const int token = tile_token(tile.tokens, l16 & 7);
+        const int token = tile_token(tile.tokens, min(l16, ROWS - 1));
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
+          v4f t = acc[j];                            // the smallest parts first
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[j][c] += __shfl_xor(acc[j][c], 8, kWave);
-          if (l16 < 8 && token >= 0) mine[(token * NJ + j) * 4 + g] += acc[j];
+          for (int c = 0; c < 4; ++c)
+            t[c] += __shfl(t[c], lane + ROWS, kWave) + __shfl(t[c], lane + 2 * ROWS, kWave);
+          if (l16 < ROWS && token >= 0) mine[(token * NJ + j) * 4 + g] += t;
           acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
         }
         ck = 0;
@@ -638,7 +653,7 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
 static size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 // Most tiles of `most` rows: one partial one for each expert with rows.
-static int64_t most_tiles(int64_t E, int64_t R, int64_t most) { return R / most + (E < R ? E : R); }
+static constexpr int64_t most_tiles(int64_t E, int64_t R, int64_t most) { return R / most + (E < R ? E : R); }
 
 struct MoeSpace {
   size_t up, down, weights, mid, end;
@@ -650,7 +665,7 @@ static MoeSpace moe_space(int64_t T, int64_t E, int64_t topk, int64_t I) {
   s.down = s.up + up16(sizeof(MoeTile) * (size_t)most_tiles(E, R, kUpRows));
   s.weights = s.down + up16(sizeof(MoeTile) * (size_t)most_tiles(E, R, kFewRows));
   s.mid = s.weights + up16((size_t)R * 4);
-  s.end = s.mid + up16((size_t)(2 * R * I) * 2);
+  s.end = s.mid + up16((size_t)(kParts * R * I) * 2);
   return s;
 }
 
@@ -658,20 +673,25 @@ size_t moe_workspace(int64_t T, int64_t E, int64_t topk, int64_t I) {
   return T == 0 ? 0 : moe_space(T, E, topk, I).end;
 }
 
-template <int FMT, bool F16, int NX, int NM, int WD, int NJ>
+template <int FMT, bool F16, int NX, int ROWS, int WD, int NJ>
 static hipError_t moe_stream(const MoeArgs& p, int64_t tiles, hipStream_t stream) {
   constexpr int WU = 4;                              // (2, 3 and 8 waves: within 5%)
   // Blocks of the first kernel that route for themselves do so once, for several column tiles each: at most 4 blocks per CU,
   // equally many tiles for each (2 tokens of 64 experts, int4: 55 us with a tile per block, 50 so). Where a kernel before
   // it routes, a tile per block is as fast or faster (32 tokens FP8: 314 us; 1024 blocks, 326).
   const int64_t items = tiles * p.NT, turns = p.inl ? (items + 1023) / 1024 : 1;
-  // (with the most of everything, 32 tokens of 1024 experts, 64 chosen: 154 KiB with what is static)
-  const size_t lds = (size_t)WD * p.T * 64 * NJ + sizeof(MoeTile) * (size_t)most_tiles(p.E, (int64_t)p.T * p.topk, p.down_rows);
+  // LDS of the second kernel: its waves' steps, their sums by token, the tiles; with the most of everything (32 tokens of 1024
+  // experts, 64 chosen) at most 156 KiB
+  const size_t lds = (size_t)WD * p.T * 64 * NJ + sizeof(MoeTile) * (size_t)most_tiles(p.E, (int64_t)p.T * p.topk, ROWS);
+  constexpr size_t steps = (size_t)WD * (2048 * NJ + 1024 * kMidDmas<FMT, ROWS> + Scales<FMT, NJ>::kBytes);
+  constexpr int64_t maxT = ROWS == kInline ? kInline : kMaxT;
+  static_assert(steps + (size_t)WD * maxT * 64 * NJ + sizeof(MoeTile) * (size_t)most_tiles(kMaxE, maxT * kMaxTopk, ROWS) <= kLds,
+                "every accepted size fits a CU's LDS");
   hipLaunchKernelGGL((moe_up_kernel<FMT, F16, NX, WU>), dim3((unsigned)((items + turns - 1) / turns)), dim3(64 * WU), 0,
                      stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down_kernel<FMT, F16, NM, WD, NJ>), dim3((unsigned)(p.H / (16 * NJ))), dim3(64 * WD), lds, stream, p);
+  hipLaunchKernelGGL((moe_down_kernel<FMT, F16, ROWS, WD, NJ>), dim3((unsigned)(p.H / (16 * NJ))), dim3(64 * WD), lds, stream, p);
   return hipGetLastError();
 }
 
@@ -680,8 +700,8 @@ static hipError_t moe_go(MoeArgs& p, hipStream_t stream) {
   const int64_t R = (int64_t)p.T * p.topk;
   p.NT = p.I / 16;
   // Longer tiles of the second kernel read an expert's weights once for more rows and hold more LDS (32 tokens of 64
-  // experts, FP8: 220 us with 4 rows, 198 with 8; 16 tokens: 175 and 174; 8 tokens of MXFP4: 66 and 74).
-  p.down_rows = R >= 2 * p.E ? kUpRows : kFewRows;
+  // experts, 7168 x 2048: FP8 222 us with 4 rows, 205 with 5, MXFP4 157 and 152; 16 tokens: the same).
+  p.down_rows = p.T <= kInline ? kInline : R >= 2 * p.E ? kDownRows : kFewRows;
   if (!p.inl) {
     const bool general = p.route.bias || p.route.G > 1;
     const size_t keys = p.route.G > 1 ? (size_t)8 * p.E * (kPThreads / kWave) : 0;
@@ -694,18 +714,19 @@ static hipError_t moe_go(MoeArgs& p, hipStream_t stream) {
   }
   // up to 2 tokens tiles have at most 2 rows
   constexpr int C = kCols<FMT> / 128;
-  if (p.T <= 2)
-    return moe_stream<FMT, F16, 1, C, 8, 1>(p, p.inl ? (R < p.E ? R : p.E) : most_tiles(p.E, R, kUpRows), stream);
+  if (p.T <= kInline)
+    return moe_stream<FMT, F16, 1, kInline, 8, 1>(p, p.inl ? (R < p.E ? R : p.E) : most_tiles(p.E, R, kUpRows), stream);
   const int64_t tiles = most_tiles(p.E, R, kUpRows);
-  // The second kernel reads the middle, from L2, once per block: with 32 columns per block half as often (32 tokens, 7168 x
-  // 2048, FP8: 199 us with 16 columns, 160 with 32; 8 tokens of MXFP4: 66 and 58), if that leaves enough blocks; else more
+  // The second kernel reads the middle, from L2, once per block: with 32 columns per block half as often (measured with a
+  // middle of two numbers and tiles of 8 rows: 32 tokens, 7168 x 2048, FP8: 199 us with 16 columns, 160 with 32; 8 tokens
+  // of MXFP4: 66 and 58), if that leaves enough blocks; else more
   // waves share the steps (32 tokens, 2048 x 1024, FP8: 32 columns 70 us, 16 columns 58, with 12 waves 51; 8 tokens of
   // 4096 x 2048, MXFP4: 54, 46 and 39). LDS bounds the waves of long tiles.
   if (p.H >= 6144)
-    return p.down_rows == kFewRows ? moe_stream<FMT, F16, 2 * C, 2 * C, 8, 2>(p, tiles, stream)
-                                   : moe_stream<FMT, F16, 2 * C, 4 * C, 8, 2>(p, tiles, stream);
-  return p.down_rows == kFewRows ? moe_stream<FMT, F16, 2 * C, 2 * C, 12, 1>(p, tiles, stream)
-                                 : moe_stream<FMT, F16, 2 * C, 4 * C, 10, 1>(p, tiles, stream);
+    return p.down_rows == kFewRows ? moe_stream<FMT, F16, 2 * C, kFewRows, 8, 2>(p, tiles, stream)
+                                   : moe_stream<FMT, F16, 2 * C, kDownRows, 8, 2>(p, tiles, stream);
+  return p.down_rows == kFewRows ? moe_stream<FMT, F16, 2 * C, kFewRows, 12, 1>(p, tiles, stream)
+                                 : moe_stream<FMT, F16, 2 * C, kDownRows, 10, 1>(p, tiles, stream);
 }
 
 // fmt: 0 FP8 with block scales, 1 MXFP4, 2 int4 tiles (group: 128 m, or -1).
