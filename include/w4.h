@@ -678,7 +678,7 @@ int w4_mxfp4_dequantize(const void* codes, const void* scales, int64_t M, int64_
  * over the blocks b of 32 columns, the sums in fp32, rounded once to the output
  * type.
  *   a, a_scale  device, [M, K] as above;  w, w_scale: [N, K]
- *   bias     device or NULL, [N] in the output type
+ *   bias     device or NULL, [N] in the output type, aligned to it
  *   out      device, [M, N] in out_dtype: bf16, fp16 or fp32
  *   a, w and out must be 16-byte aligned, the scales 4-byte; N a multiple of 8, K
  *   of 32 and at most 2^22.

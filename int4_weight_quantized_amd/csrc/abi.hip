@@ -995,6 +995,13 @@ static int check_mx(const char* fn, int64_t M, int64_t N, int64_t K) {
   return W4_OK;
 }
 
+// dt: its type's place among bf16, fp16 and fp32.
+static int check_bias(const char* fn, const void* bias, int dt) {
+  if (reinterpret_cast<uintptr_t>(bias) & (dt == 2 ? 3u : 1u))
+    return fail(W4_ERR_ALIGN, "%s: bias must be aligned to its type", fn);
+  return W4_OK;
+}
+
 static int check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need, int64_t M, int64_t N,
                            int64_t K) {
   if (bytes < need || (need && !workspace))
@@ -1027,7 +1034,8 @@ int w4_mxfp4_gemm(const void* a, const void* a_scale, const void* w, const void*
   if (!aligned16(a) || !aligned16(w) || !aligned16(out))
     return fail(W4_ERR_ALIGN, "%s: a, w and out must be 16-byte aligned", fn);
   if (!aligned4(a_scale) || !aligned4(w_scale)) return fail(W4_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
-  rc = check_workspace(fn, workspace, workspace_bytes, w4::mx_gemm_workspace(M, N, K), M, N, K);
+  rc = check_bias(fn, bias, dt);
+  if (!rc) rc = check_workspace(fn, workspace, workspace_bytes, w4::mx_gemm_workspace(M, N, K), M, N, K);
   if (rc) return rc;
   return hip_status(w4::launch_mx_gemm(a, a_scale, w, w_scale, bias, out, dt, M, N, K, workspace,
                                        static_cast<hipStream_t>(stream)),
@@ -1069,7 +1077,8 @@ int w4_mxfp4_linear(const void* x, int x_dtype, const void* w, const void* w_sca
   if (!aligned16(x) || !aligned16(w) || !aligned16(out))
     return fail(W4_ERR_ALIGN, "%s: x, w and out must be 16-byte aligned", fn);
   if (!aligned4(w_scale)) return fail(W4_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
-  rc = check_workspace(fn, workspace, workspace_bytes, mx_linear_workspace(M, N, K), M, N, K);
+  rc = check_bias(fn, bias, float_index(x_dtype));
+  if (!rc) rc = check_workspace(fn, workspace, workspace_bytes, mx_linear_workspace(M, N, K), M, N, K);
   if (rc) return rc;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const bool bf16 = x_dtype == W4_BF16;

@@ -191,16 +191,27 @@ __global__ __launch_bounds__(64 * WM * WN, MI * NJ > 4 ? 1 : 2) void mx_tile_ker
     else dma(wrsrc, ldsw + stage + (BM + (TH / 8) * (q - RA)) * kMB, tk >= k1 || (last && b_dead) ? kPast : b_off[q - RA], ks);
   };
 
-  // the accumulators start from the bias, of 16 consecutive columns each (without one an empty buffer, which reads as zero)
+  // the accumulators start from the bias, of 16 consecutive columns each (without one an empty buffer, which reads as zero).
+  // One of 16-bit values may begin in the middle of a word: whole words are loaded, from there on, and shifted.
   constexpr int SZ = OUT == 2 ? 4 : 2;               // bytes of a result
   v4i bias[NJ][SZ];
   if constexpr (!GROUPED) {
-    const __amdgpu_buffer_rsrc_t brs = make_rsrc(p.bias, p.bias && p.splits == 1 ? (uint32_t)p.N * SZ : 0u);
+    const uint32_t odd = (uint32_t)(uintptr_t)p.bias & 2;
+    const __amdgpu_buffer_rsrc_t brs = make_rsrc(static_cast<const uint8_t*>(p.bias) - odd,
+                                                 p.bias && p.splits == 1 ? (uint32_t)p.N * SZ + 2 * odd : 0u);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int j = 0; j < NJ; ++j) {
+      const uint32_t at = (uint32_t)(tn * BN + 32 * (NJ * wn + j) + 16 * h) * SZ;
 #pragma unroll
-      for (int q = 0; q < SZ; ++q)
-        bias[j][q] = buffer_load16(brs, (uint32_t)(tn * BN + 32 * (NJ * wn + j) + 16 * h) * SZ + 16 * q);
+      for (int q = 0; q < SZ; ++q) bias[j][q] = buffer_load16(brs, at + 16 * q);
+      if constexpr (OUT != 2) {
+        const int next = __builtin_amdgcn_raw_buffer_load_b32(brs, at + 32, 0, 0);
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+          bias[j][d / 4][d % 4] = (int)__builtin_amdgcn_alignbyte((uint32_t)(d < 7 ? bias[j][(d + 1) / 4][(d + 1) % 4] : next),
+                                                                  (uint32_t)bias[j][d / 4][d % 4], odd);
+      }
+    }
   }
 
   // ---- fragments
