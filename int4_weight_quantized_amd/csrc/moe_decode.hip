@@ -705,6 +705,7 @@ static hipError_t moe_go(MoeArgs& p, hipStream_t stream) {
   if (!p.inl) {
     const bool general = p.route.bias || p.route.G > 1;
     const size_t keys = p.route.G > 1 ? (size_t)8 * p.E * (kPThreads / kWave) : 0;
+    static_assert(8 * kMaxE * (kPThreads / kWave) + 8 * kMaxE + 3 * 4 * (kPThreads / kWave) <= kLds, "as does the plan");
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(1), dim3(kPThreads), keys, stream, p); };
     if (p.E <= 64) general ? go(moe_plan_kernel<1, true>) : go(moe_plan_kernel<1, false>);
     else if (p.E <= 256) general ? go(moe_plan_kernel<4, true>) : go(moe_plan_kernel<4, false>);
