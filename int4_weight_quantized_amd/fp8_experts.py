@@ -52,6 +52,8 @@ class Fp8Experts:
         T = x.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens exceed max_tokens={self.max_tokens}")
+        if self.decode_tokens and x.dtype != self.dtype:     # the same types on both sides of decode_tokens
+            raise TypeError(f"x must be {self.dtype}, the layer's type, got {x.dtype}")
         if T and T <= self.decode_tokens:
             return ops.w4_moe_decode(x, logits, self.topk, self.w13, self.w13_scale, self.w2, self.w2_scale, add=add, out=out,
                                      workspace=self._decode_ws, stream=stream, **self.routing)
