@@ -697,9 +697,9 @@ int w4_mxfp4_gemm(const void* a, const void* a_scale, const void* w, const void*
 /*
  * The linear layer on MXFP4 weights, activations quantized within: the same as
  * w4_mxfp4_quantize (without an activation) and w4_mxfp4_gemm with the output in
- * the activations' type. Few rows (up to 16 of together at most 32768
- * values, or 65536 with N up to 8192) are quantized by the product itself, in one
- * launch.
+ * the activations' type. Few rows (up to 16 of together at most 65536 values,
+ * fewer where N is large) are quantized by the product itself, in one launch and
+ * without a workspace.
  *   x        device, [M, K] contiguous, bf16 or fp16, 16-byte aligned
  *   workspace device, w4_mxfp4_linear_workspace_bytes (16-byte aligned; may be
  *            NULL when that is 0), owned by the caller: codes, scales and the

@@ -469,9 +469,12 @@ int64_t mx_gemm_threads(int64_t M, int64_t N, int64_t K) {
 }
 
 // Whether the linear layer's product quantizes the rows itself, every block all of them, instead of a launch before it: the
-// more the blocks, the fewer. 8 x 14336 x 4096 8.4 us (two launches 8.9), 12 rows 9.5 (8.8); 4 x 4096 x 14336 13.8 (13.8),
-// 8 rows 17.3 (13.9); 12 x 4096 x 4096 6.2 (7.2), 16 rows 7.8 (7.3); 8 x 2048 x 7168 7.5 (9.0), 16 rows 10.0 (9.0).
-bool mx_inline(int64_t M, int64_t N, int64_t K) { return M <= 16 && M * K <= (N <= 8192 ? 65536 : 32768); }
+// more the blocks, the fewer. With weights from memory, us (two launches): 16 x 256 x 4096 7.2 (7.1); 12 x 4096 x 4096 8.6
+// (9.1), 14 rows 9.0 (9.2), 16 rows 9.3 (9.1); 8 x 4096 x 7168 11.7 (12.1); 4 x 4096 x 14336 19.1 (19.2); 8 x 8192 x 4096
+// 9.2 (10.0), 12 rows 10.3 (10.0); 8 x 14336 x 4096 10.8 (11.1); 4 x 28672 x 4096 16.4 (18.0), 8 rows 20.5 (18.0).
+bool mx_inline(int64_t M, int64_t N, int64_t K) {
+  return M <= 16 && M * K <= (N <= 512 ? 65536 : N <= 4096 ? 57344 : N <= 8192 ? 40960 : N <= 16384 ? 32768 : 16384);
+}
 
 template <int BM, int BN, typename F>
 static hipError_t tile_go(MxArgs p, F kernel, hipStream_t stream) {
