@@ -96,18 +96,19 @@ __device__ __forceinline__ int cvt_fp8(int w, float scale, bool high) {
                 : __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false));
 }
 
-// Rows of 16-bit activations: a DMA takes kCols columns of 4 (FP8) or 2 rows; row r, chunk c at 2 kCols r + 16 (c ^ (r & 7)).
+// Rows of 16-bit activations: a DMA takes kCols columns of 4 (FP8) or 2 rows; row r, chunk c at 2 kCols r + 16 (c ^ (by & 7)),
+// by: the row, or the column of the product that it becomes.
 template <int FMT>
 constexpr int kRowsPerDma = 512 / kCols<FMT>;
 template <int FMT>
 __device__ __forceinline__ int act_row(int j, int lane) { return j * kRowsPerDma<FMT> + lane / (kCols<FMT> / 8); }
 template <int FMT>
-__device__ __forceinline__ int act_column(int row, int lane) { return 8 * ((lane & (kCols<FMT> / 8 - 1)) ^ (row & 7)); }
+__device__ __forceinline__ int act_column(int by, int lane) { return 8 * ((lane & (kCols<FMT> / 8 - 1)) ^ (by & 7)); }
 // MFMA c's 8 activations of a lane (of the step's half q: MXFP4 and int4 have 4 MFMAs in each): FP8: columns 64 (c / 2) +
 // 16 g + 8 (c % 2) ..; MXFP4: 128 q + 32 g + 8 c ..; int4: 128 q + 32 g + 4 c .. + 3 and 16 after them.
 template <int FMT>
-__device__ __forceinline__ v4i act_chunk(const uint8_t* at, int row, int chunk) {
-  return *reinterpret_cast<const v4i*>(at + 2 * kCols<FMT> * row + 16 * (chunk ^ (row & 7)));
+__device__ __forceinline__ v4i act_chunk(const uint8_t* at, int row, int by, int chunk) {
+  return *reinterpret_cast<const v4i*>(at + 2 * kCols<FMT> * row + 16 * (chunk ^ (by & 7)));
 }
 template <int FMT>
 __device__ __forceinline__ v4i act_piece(const v4i (&X)[4], int c) {
@@ -394,7 +395,7 @@ __global__ __launch_bounds__(64 * WS) void moe_up_kernel(MoeArgs p) {
         for (int q = 0; q < HALVES; ++q) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            X[q][c] = act_chunk<FMT>(step + kX, row & (kRowsPerDma<FMT> * NX - 1),
+            X[q][c] = act_chunk<FMT>(step + kX, row & (kRowsPerDma<FMT> * NX - 1), row & (kRowsPerDma<FMT> * NX - 1),
                                      FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
           if constexpr (FMT == kMx) {
             lg[q] = S::block(scales, k, 0, q, p.H - k * COLS, l16, g);
@@ -512,7 +513,7 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
   bool mdead[NM];
 #pragma unroll
   for (int j = 0; j < NM; ++j) {
-    const int r = act_row<FMT>(j, lane), col = act_column<FMT>(r, lane);
+    const int r = act_row<FMT>(j, lane), col = act_column<FMT>(ROWS * (r % kParts) + r / kParts, lane);
     mo[j] = (uint32_t)((int64_t)(r / kParts) * p.I * 2 + 2 * col + r % kParts * plane);
     mdead[j] = col >= p.I - (KT - 1) * COLS;
   }
@@ -571,7 +572,7 @@ __global__ __launch_bounds__(64 * WS) void moe_down_kernel(MoeArgs p) {
       for (int q = 0; q < HALVES; ++q) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          M[q][c] = act_chunk<FMT>(step + kX, mrow, FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
+          M[q][c] = act_chunk<FMT>(step + kX, mrow, l16, FMT == kFp8 ? 8 * (c / 2) + 2 * g + c % 2 : 16 * q + 4 * g + c);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           if constexpr (FMT == kMx) ls[j][q] = S::block(scales, ck, j, q, p.I - ck * COLS, l16, g);
