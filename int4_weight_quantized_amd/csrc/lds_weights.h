@@ -3,7 +3,7 @@
 // layout (lane = row + 16 * column group) would touch 64 cache lines per load and cost the address unit 60 clocks where a
 // DMA of 8 rows' full lines costs 16 (measured); it bound such kernels at 2 to 4 TB/s. One step of room is enough: a wave
 // takes it into registers and asks for the next before it computes. More room per wave means fewer waves, which costs more
-// than it hides: two steps took 131 us instead of 117 for the gate and up products of 8 tokens (64 experts, 7168 x 2048,
+// than it hides: two steps took 131 us instead of 115 for the gate and up products of 8 tokens (64 experts, 7168 x 2048,
 // MXFP4) and 69 instead of 64 for a grouped product of 8 tokens' 64 rows; three (the former in blocks of two waves) 151 and 85.
 #pragma once
 #include "mxfp4.h"

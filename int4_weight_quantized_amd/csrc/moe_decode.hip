@@ -29,11 +29,13 @@
 // activations takes x apart in two such numbers, exactly (11 bits).
 //
 // 64 experts, 8 chosen, 7168 x 2048, kernels only (medians): one token FP8 47 + 23 us
-// (5.1 TB/s of weights); two tokens int4 52 + 29; 8 tokens MXFP4 7 + 114 + 65; 32
-// tokens FP8 13 + 320 + 204, MXFP4 13 + 194 + 152. What bounds them is memory and, with
-// many rows, the activations and the middle, which every block reads from L2: with a
-// middle of two bf16 numbers (16 bits) and so tiles of 8 rows the down products took
-// 59 us for 8 tokens, 170 and 121 for 32.
+// (5.1 TB/s of weights); two tokens int4 50 + 28; 8 tokens MXFP4 9 + 113 + 62, int4 8 +
+// 123 + 68; 32 tokens FP8 15 + 320 + 194, MXFP4 21 + 189 + 143, int4 14 + 199 + 135. What
+// bounds them is memory and, with many rows, the activations and the middle, which every
+// block reads from L2: with a middle of two bf16 numbers (16 bits) and so tiles of 8 rows
+// the down products took 59 us for the 8 tokens of MXFP4, 160 for the 32 of FP8. Tiles of
+// 10 rows in two turns on the same weights instead of two tiles of 5 gain 2% there and
+// cost as much in smaller layers.
 #include <type_traits>
 
 #include "lds_weights.h"
@@ -121,7 +123,9 @@ __device__ __forceinline__ v4i act_piece(const v4i (&X)[4], int c) {
 }
 
 // 8 weights for MFMA c from a lane's pieces. int4 codes come as the code itself, 0..15 (E4M3's codes 0..15 are 0..15 times
-// 2^-9); the sums start from -8 sum x.
+// 2^-9); the sums start from -8 sum x. So a term counts up to 23 steps of the scale in fp32's rounding where a signed code
+// counts 8: of two tokens' output the error before its own rounding is 2.1e-7, of FP8's 1.9e-7. (Codes in sign and
+// magnitude would take 11 instructions more per word of 8.)
 template <int FMT, bool F16>
 __device__ __forceinline__ typename Operand<F16>::V decode(const v4i (&w)[2], int q, int c, float scale) {
   v4i r;

@@ -30,7 +30,7 @@ __device__ __forceinline__ float mx_scale_value(uint32_t code) {
   return __uint_as_float(code ? code << 23 : 0x00400000u);
 }
 
-// Largest magnitude of 8 values of 16 bits in 4 words, as fp32 bits. Positive
+// Largest magnitude of 2 W values of 16 bits in W words, as fp32 bits. Positive
 // bf16 and fp16 numbers order as their bits do.
 template <bool BF16, int W>
 __device__ __forceinline__ uint32_t mx_amax16(const int (&raw)[W]) {

@@ -27,14 +27,15 @@
 //   16 (q / 4 % 2) + 4 (q / 8) + q % 4, which gives a lane 16 consecutive ones.
 // - Results leave through LDS as whole rows: straight from the registers a store
 //   would be half a cache line of each of 32 rows (154 us, 151 so).
-// What bounds it: 4096 x 14336 x 4096 takes 144 us (up to 170 on cards whose clock
-// the power limit holds lower), 3.3 PFLOP/s, K = 16384 reaches
-// 4.1, where the fp4 matrix rate alone is 8.4. Each round of tiles ends in a
+// What bounds it: 4096 x 14336 x 4096 takes 146 us, 3.3 PFLOP/s, K = 16384 reaches
+// 4.1, where the fp4 matrix rate alone is 8.4. At K = 4096 the clock is 2.0 GHz, as in a
+// loop of the matrix instruction alone, and 39% of the SIMDs' cycles are MFMA: what is
+// lost are stores, rounds and the loop's waits. Each round of tiles ends in a
 // burst of stores that memory takes 7 us for and nothing overlaps (about 30 of the
-// 144 us, from the times of K = 512 to 16384); within the loop a step of 256 columns takes 2.1 us, at a clock that the
-// power limit holds near 1.6 GHz there; without its DMA it takes 1.4, and with a
-// quarter of its MFMAs 1.1 (measured at shorter K, where the clock is higher and the
-// whole step takes 1.8).
+// 146 us, from the times of K = 512 to 16384), and 896 tiles are 3.5 rounds of 256 CUs.
+// Within the loop a step of 256 columns takes 1.8 us; without its DMA 1.4, with a quarter
+// of its MFMAs 1.1. Only at K = 16384 the power limit holds the clock near 1.6 GHz and
+// the step takes 2.1 us.
 #include <cmath>
 #include <type_traits>
 

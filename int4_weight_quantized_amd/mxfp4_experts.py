@@ -19,9 +19,10 @@ class Mxfp4Experts:
     """w13 uint8 [E, 2 I, H / 2] (gate rows, then up rows) and w2 [E, H, I / 2] codes, w13_scale uint8
     [E, 2 I, 4 ceil(H / 128)] and w2_scale [E, H, 4 ceil(I / 128)], as ops.w4_mxfp4_quantize lays them out. `routing` goes
     to ops.w4_route (score, bias, n_groups, ...). Up to `decode_tokens` tokens (at most W4_MOE_DECODE_MAX_TOKENS) take the
-    one call; its activations are not quantized, so the two paths differ by the quantization. (64 experts of 7168 x
-    2048, 8 chosen: 1 token 41 us in one call and 55 in stages, 8 tokens 178 and 195, 24 tokens 268 and 272, 32 tokens 292
-    and 280.)"""
+    one call; its activations are not quantized, so the two paths differ by the quantization. The default prefers
+    that to time: the one call is the faster up to about 12 tokens. (64 experts, 8 chosen, of 7168 x 2048: 1 token 44 us in
+    one call and 56 in stages, 8 tokens 187 and 194, 12 tokens 225 and 233, 16 tokens 258 and 253, 32 tokens 324 and 281;
+    of 2048 x 1024: 17 and 29, 46 and 49, 54 and 54, 62 and 55, 80 and 58.)"""
 
     def __init__(self, w13, w13_scale, w2, w2_scale, topk: int, max_tokens: int, dtype=torch.bfloat16,
                  decode_tokens: int = ops.W4_MOE_DECODE_MAX_TOKENS, **routing):
